@@ -15,6 +15,7 @@ MK_OK, MK_ERR_TIMEOUT, MK_ERR_DEVICE = 0, 5, 6
 _I = C.c_int32
 _F = C.c_float
 _P = C.c_void_p
+_L = C.c_int64
 
 
 class ModelDesc(C.Structure):
@@ -74,11 +75,45 @@ class StateBuffers(C.Structure):
     _fields_ = [("kcache", _P), ("vcache", _P), ("state", _P), ("pending", _P), ("seq", _P), ("epoch", C.c_uint32)]
 
 
+class PageTablesArgs(C.Structure):
+    _fields_ = [("table", _P), ("table_stride", _L), ("held", _P), ("start", _P), ("count", _P), ("ring", _P),
+                ("ring_state", _P), ("ring_state_out", _P), ("slots", _P), ("positions", _P), ("owners", _P),
+                ("starts", _P), ("lens", _P), ("status", _P), ("batch", _I), ("max_pages", _I), ("page_size", _I),
+                ("n_pages", _I), ("ring_size", _I), ("n_tokens", _I)]
+
+
+class QkNormRopeArgs(C.Structure):
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("q_out", _P), ("k_out", _P), ("q_gain", _P), ("k_gain", _P),
+                ("inv_freq", _P), ("positions", _P), ("slots", _P), ("k_pages", _P), ("v_pages", _P), ("k_scale", _P),
+                ("v_scale", _P), ("status", _P), ("q_stride", _L * 2), ("k_stride", _L * 2), ("v_stride", _L * 2),
+                ("q_out_stride", _L * 2), ("k_out_stride", _L * 2), ("k_page_stride", _L * 3),
+                ("v_page_stride", _L * 3), ("n_tokens", _I), ("n_q_heads", _I), ("n_kv_heads", _I), ("head_dim", _I),
+                ("rope_dim", _I), ("n_pages", _I), ("page_size", _I), ("dtype", _I), ("cache_dtype", _I), ("eps", _F)]
+
+
+class PagedAttentionArgs(C.Structure):
+    _fields_ = [("q", _P), ("k_pages", _P), ("v_pages", _P), ("table", _P), ("lens", _P), ("k_scale", _P),
+                ("v_scale", _P), ("out", _P), ("lse", _P), ("workspace", _P), ("status", _P), ("workspace_bytes", _L),
+                ("table_stride", _L), ("q_stride", _L * 3), ("out_stride", _L * 3), ("k_page_stride", _L * 3),
+                ("v_page_stride", _L * 3), ("batch", _I), ("rows", _I), ("n_q_heads", _I), ("n_kv_heads", _I),
+                ("head_dim", _I), ("n_pages", _I), ("page_size", _I), ("max_pages", _I), ("dtype", _I),
+                ("cache_dtype", _I), ("scale", _F)]
+
+
+class LogitControlsArgs(C.Structure):
+    _fields_ = [("logits", _P), ("out", _P), ("token", _P), ("history", _P), ("prompt_len", _P), ("total_len", _P),
+                ("repetition", _P), ("presence", _P), ("frequency", _P), ("bias_ids", _P), ("bias_vals", _P),
+                ("allowed", _P), ("logits_stride", _L), ("out_stride", _L), ("history_stride", _L), ("bias_stride", _L),
+                ("allowed_stride", _L), ("rows", _I), ("vocab", _I), ("max_history", _I), ("n_biases", _I),
+                ("dtype", _I)]
+
+
 EXPORTS = ["mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host", "mk_get_status",
            "mk_last_error", "mk_get_info", "mk_destroy", "mk_decode_step_static", "mk_set_routing_log",
            "mk_fork_sequence", "mk_plan", "mk_set_wait_limit",
            "mk_set_routing_override", "mk_decode_steps", "mk_decode_steps_host", "mk_verify_step",
-           "mk_packed_weight_bytes", "mk_pack_weights"]
+           "mk_packed_weight_bytes", "mk_pack_weights", "mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention",
+           "mk_paged_attention_workspace", "mk_logit_controls"]
 
 _lib = None
 
@@ -120,6 +155,12 @@ def load(path: str | None = None) -> C.CDLL:
                                           _P, _P, C.c_int, C.c_int, _P, _P, _P]
     lib.mk_packed_weight_bytes.argtypes = [C.POINTER(ModelDesc), C.POINTER(Weights), C.c_int, C.POINTER(C.c_uint64)]
     lib.mk_pack_weights.argtypes = [C.POINTER(ModelDesc), C.POINTER(Weights), C.c_int, _P, _P]
+    # the argument structs go in by address (a structure's byref or the bytes of one)
+    for f in ("mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention", "mk_logit_controls"):
+        getattr(lib, f).argtypes = [_P, C.c_int, _P]
+        getattr(lib, f).restype = C.c_int
+    lib.mk_paged_attention_workspace.argtypes = [_P, C.c_int, C.POINTER(C.c_uint64)]
+    lib.mk_paged_attention_workspace.restype = C.c_int
     for f in ("mk_packed_weight_bytes", "mk_pack_weights", "mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host", "mk_get_status", "mk_get_info",
               "mk_decode_step_static", "mk_set_routing_log", "mk_fork_sequence", "mk_plan", "mk_set_wait_limit",
               "mk_set_routing_override", "mk_decode_steps", "mk_decode_steps_host", "mk_verify_step"):
@@ -231,6 +272,7 @@ class Megakernel:
         model (kept alive by the caller), or 0 to let the handle make its own."""
         self.lib = load()
         self.cfg = cfg
+        self.device = device
         self._weights = weights  # keep the tensors alive for the handle's lifetime
         self.desc = model_desc(cfg, max_batch, max_rows, max_ctx)
         self.wtab = weight_table(cfg, weights)
@@ -250,9 +292,21 @@ class Megakernel:
         B, T = tokens.shape
         self._check(self.lib.mk_prefill_kv(self.h, tokens.data_ptr(), B, T, stream))
 
-    def step(self, tokens, positions, logits=None, argmax=None, stream=None):
-        """tokens: device int32 [B, R]; positions: device int32 [B]; outputs preallocated device tensors."""
+    def step(self, tokens, positions, logits=None, argmax=None, stream=None, controls=None):
+        """tokens: device int32 [B, R]; positions: device int32 [B]; outputs preallocated device tensors.
+        controls: a dict of serving.logit_controls' arguments (history, repetition, bias_ids, allowed, ...; one row
+        for each of the B * R rows): the step's logits (then required: contiguous fp32 [B * R, vocab]) are controlled
+        in place on the same stream and argmax is the greedy token of what is left (-1: nothing is allowed)."""
         B, R = tokens.shape
+        if controls is not None:
+            from .serving import logit_controls
+            z = None if logits is None else logits.view(-1, self.cfg.vocab)
+            if z is None or z.shape[0] != B * R or z.get_device() != self.device:
+                raise ValueError("controls need logits [batch * rows, vocab] on the handle's device")
+            self._check(self.lib.mk_decode_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R, z.data_ptr(),
+                                                 None, stream))
+            logit_controls(z, z, token=None if argmax is None else argmax.view(-1), stream=stream or 0, **controls)
+            return
         self._check(self.lib.mk_decode_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R,
                                              _ptr(logits), _ptr(argmax), stream))
 

@@ -1,0 +1,208 @@
+// mk_paged_attention: arguments, the choice of a build, and the second kernel, which joins the parts of requests that
+// were cut (paged_attention.cuh has the attention kernel).
+#include "paged_attention.cuh"
+
+namespace mkop {
+namespace attn {
+namespace {
+
+constexpr int kJoinWarps = 8;
+
+// Block (x, y): the request cut at the beginning of piece x + 1, if that is the first cut in it; rows y, y + gridDim.y, ...
+// A row's parts are weighted by exp2(maximum - largest maximum); the warps take the parts in turn and are summed in a
+// fixed order. Launched so that it may start while the attention kernel runs; it waits for that kernel's end before
+// it reads anything.
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p, int dp, int rows_of_block,
+                                                             bool scaled) {
+  __shared__ float weight[kMaxCtas];
+  __shared__ __align__(16) float sums[kJoinWarps][256];
+  __shared__ float red[2][kJoinWarps];
+  const mk_paged_attention_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = blockIdx.x + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Piece pc = p.piece[c];
+  if (c >= pc.used) return;
+  const long long begin = piece_begin(c, pc.total, pc.used), prev = piece_begin(c - 1, pc.total, pc.used);
+  if (begin == pc.item0 || prev > pc.item0) return;  // cut between requests, or not the first cut of this one
+  // the last piece that begins inside the request: q * total / used < item1
+  const int last = static_cast<int>((pc.item1 * pc.used - 1) / pc.total);
+  const int n = last - (c - 1) + 1;
+  const long long slot0 = 2ll * (c - 1) + (prev == pc.item0 ? 0 : 1);
+  auto slot = [&](int k) { return k == 0 ? slot0 : 2ll * (c - 1 + k); };
+  const int head = pc.hm / p.blocks, block = pc.hm - head * p.blocks;
+  const int rows = min(rows_of_block, p.n_rows - block * rows_of_block);
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    float top = -INFINITY;
+    for (int k = tid; k < n; k += kJoinWarps * 32) top = fmaxf(top, p.part_ml[slot(k) * rows_of_block + row].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[0][w]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0;
+    for (int k = tid; k < n; k += kJoinWarps * 32) {
+      const float2 s = p.part_ml[slot(k) * rows_of_block + row];
+      const float f = exp2_fast(s.x - base);
+      weight[k] = f;
+      sum += f * s.y;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
+    for (int d = lane * 4; d < dp; d += 128) {
+      float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+      for (int k = warp; k < n; k += kJoinWarps) {
+        const float4 x = *reinterpret_cast<const float4*>(p.part + (slot(k) * rows_of_block + row) * dp + d);
+        const float f = weight[k];
+        y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+      }
+      *reinterpret_cast<float4*>(&sums[warp][d]) = y;
+    }
+    __syncthreads();
+    const int mrow = block * rows_of_block + row, r = mrow / p.group, h = head * p.group + mrow - r * p.group;
+    const float f = sum == 0.0f ? 0.0f : (scaled ? a.v_scale[head] : 1.0f) / sum;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + pc.b * a.out_stride[0] +
+                                                r * a.out_stride[1] + h * a.out_stride[2]);
+    for (int d = 2 * tid; d < a.head_dim; d += 2 * kJoinWarps * 32) {
+      float x = 0, y = 0;
+      for (int w = 0; w < kJoinWarps; ++w) x += sums[w][d], y += sums[w][d + 1];
+      out[d / 2] = pack2<T>(x * f, y * f);
+    }
+    if (tid == 0 && a.lse)
+      a.lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] =
+          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+    __syncthreads();
+  }
+}
+
+const char* const kMe = "mk_paged_attention";
+
+// What follows from the shape fields alone: the build, the grid, the workspace.
+struct Plan {
+  const Build* build;
+  int dp, group, n_rows, blocks, ctas;
+  size_t piece_at, ml_at, bytes;
+};
+
+mk_status check_shape(const mk_paged_attention_args& a, int device) {
+  if (a.rows < 1 || a.rows > 4096 || a.n_q_heads < 1 || a.n_q_heads > 4096 || a.n_kv_heads < 1 || a.n_q_heads % a.n_kv_heads)
+    return refuse(MK_ERR_INVALID_ARG, kMe, "rows %d, heads %d / %d", a.rows, a.n_q_heads, a.n_kv_heads);
+  if (a.head_dim < 16 || a.head_dim > 256 || a.head_dim % 16)
+    return refuse(MK_ERR_UNSUPPORTED, kMe, "head_dim %d is not a multiple of 16 in 16..256", a.head_dim);
+  if (a.dtype != MK_BF16 && a.dtype != MK_F16) return refuse(MK_ERR_UNSUPPORTED, kMe, "dtype %d", a.dtype);
+  if (a.cache_dtype != a.dtype && a.cache_dtype != MK_E4M3)
+    return refuse(MK_ERR_UNSUPPORTED, kMe, "cache dtype %d with dtype %d", a.cache_dtype, a.dtype);
+  return check_device(kMe, device);
+}
+
+cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
+  Plan& pl = *out;
+  pl.group = a.n_q_heads / a.n_kv_heads;
+  pl.n_rows = a.rows * pl.group;
+  pl.dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
+  // Row blocks of up to 64 rows, as equal as whole 16-row tiles allow (80 rows: 48 + 32, not 64 + 16).
+  const int tiles = (pl.n_rows + 15) / 16;
+  pl.blocks = (tiles + 3) / 4;
+  const int mt = (tiles + pl.blocks - 1) / pl.blocks;
+  pl.build = a.cache_dtype == MK_E4M3 ? pick_e4m3(pl.dp, mt) : a.dtype == MK_BF16 ? pick_bf16(pl.dp, mt) : pick_f16(pl.dp, mt);
+  int sms, per_sm;
+  cudaError_t e = sm_count(device, &sms);
+  if (e == cudaSuccess) e = pl.build->occupancy(device, &per_sm);
+  if (e != cudaSuccess) return e;
+  pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+  const size_t slots = 2 * static_cast<size_t>(pl.ctas);
+  pl.ml_at = slots * pl.build->rows * pl.dp * sizeof(float);
+  pl.piece_at = pl.ml_at + slots * pl.build->rows * sizeof(float2);
+  pl.bytes = pl.piece_at + pl.ctas * sizeof(Piece);
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t join(const Params& p, const Plan& pl, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  // a few rows each, so that the blocks without a cut to join stay few
+  const int rows = p.n_rows < pl.build->rows ? p.n_rows : pl.build->rows;
+  const int y = 1216 / pl.ctas < 1 ? 1 : 1216 / pl.ctas > rows ? rows : 1216 / pl.ctas;
+  cfg.gridDim = dim3(pl.ctas - 1, y);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T>, p, pl.dp, pl.build->rows, p.a.cache_dtype == MK_E4M3);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace mkop
+
+extern "C" mk_status mk_paged_attention_workspace(const mk_paged_attention_args* p, int device, uint64_t* bytes) {
+  using namespace mkop;
+  using namespace mkop::attn;
+  if (!p || !bytes) return MK_ERR_INVALID_ARG;
+  if (mk_status s = check_shape(*p, device)) return s;
+  DeviceGuard guard(device);
+  if (guard.err != cudaSuccess) return launched(kMe, guard.err);
+  Plan pl;
+  if (const cudaError_t e = plan(*p, device, &pl)) return launched(kMe, e);
+  *bytes = pl.bytes;
+  return MK_OK;
+}
+
+extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream) {
+  using namespace mkop;
+  using namespace mkop::attn;
+  if (!args) return MK_ERR_INVALID_ARG;
+  Params p;
+  p.a = *args;
+  const mk_paged_attention_args& a = p.a;
+  const bool e4m3 = a.cache_dtype == MK_E4M3;
+  if (a.batch < 0 || a.batch > 1 << 24 || a.n_pages < 1 || a.page_size < 1 || a.max_pages < 1)
+    return refuse(MK_ERR_INVALID_ARG, kMe, "batch %d, n_pages %d, page_size %d, max_pages %d", a.batch, a.n_pages,
+                  a.page_size, a.max_pages);
+  // a tile may end past max_len, so that leaves room below 2^31
+  if (static_cast<int64_t>(a.max_pages) * a.page_size > INT32_MAX - 1024)
+    return refuse(MK_ERR_UNSUPPORTED, kMe, "positions beyond 2^31 - 1024");
+  if (mk_status s = check_shape(a, device)) return s;
+  if (a.batch == 0) return MK_OK;
+  if (!a.q || !a.k_pages || !a.v_pages || !a.table || !a.lens || !a.out || !a.workspace || (e4m3 && (!a.k_scale || !a.v_scale)))
+    return refuse(MK_ERR_INVALID_ARG, kMe, "a required pointer is NULL");
+  if (a.table_stride < a.max_pages) return refuse(MK_ERR_INVALID_ARG, kMe, "table rows shorter than max_pages");
+  if (!aligned(a.q, 16) || !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) || !aligned(a.out, 16) || !aligned(a.workspace, 16))
+    return refuse(MK_ERR_INVALID_ARG, kMe, "a pointer is not 16-byte aligned");
+  for (int i = 0; i < 3; ++i) {
+    if (a.q_stride[i] % 8 || a.out_stride[i] % 8)
+      return refuse(MK_ERR_INVALID_ARG, kMe, "a stride is not a multiple of 8 elements");
+    if (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8))
+      return refuse(MK_ERR_INVALID_ARG, kMe, "a cache stride is not a multiple of 16 bytes");
+  }
+  DeviceGuard guard(device);
+  if (guard.err != cudaSuccess) return launched(kMe, guard.err);
+  Plan pl;
+  if (const cudaError_t e = plan(a, device, &pl)) return launched(kMe, e);
+  if (a.workspace_bytes < static_cast<int64_t>(pl.bytes))
+    return refuse(MK_ERR_INVALID_ARG, kMe, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), pl.bytes);
+  char* ws = static_cast<char*>(a.workspace);
+  p.group = pl.group;
+  p.n_rows = pl.n_rows;
+  p.blocks = pl.blocks;
+  p.max_len = a.max_pages * a.page_size;
+  p.ctas = pl.ctas;
+  p.scale_log2 = a.scale * 1.44269504088896340736f;
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_at);
+  p.piece = reinterpret_cast<Piece*>(ws + pl.piece_at);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = pl.build->launch(p, device, s);
+  if (e == cudaSuccess && pl.ctas > 1) e = a.dtype == MK_BF16 ? join<__nv_bfloat16>(p, pl, s) : join<__half>(p, pl, s);
+  return launched(kMe, e);
+}

@@ -1,0 +1,8 @@
+// The attention kernels over bf16 caches.
+#include "paged_attention.cuh"
+
+namespace mkop {
+namespace attn {
+const Build* pick_bf16(int dp, int mt) { return pick<__nv_bfloat16, false>(dp, mt); }
+}  // namespace attn
+}  // namespace mkop

@@ -390,6 +390,189 @@ mk_status mk_decode_step_static(const mk_model_desc* desc, const mk_weights* wei
                                 const int32_t* tokens, const int32_t* positions, int batch, int rows,
                                 float* logits_out, int32_t* argmax_out, void* stream);
 
+/* ---- Serving operators ---------------------------------------------------------------------------
+ * The step's own kinds of work (RoPE and cache append, grouped-query attention, the choice of the next
+ * token) as calls of their own, over a PAGED cache, for serving programs that keep many ragged requests:
+ * mk_page_tables (pages and slots from request lengths), mk_qk_norm_rope (per-head norms, rotation,
+ * append), mk_paged_attention, mk_logit_controls. The source pages have no counterpart for these calls.
+ *
+ * They need no handle. Each takes its arguments as one struct, the device and a stream, enqueues its
+ * kernels on that stream and returns without waiting; nothing is allocated, nothing is kept between
+ * calls, the current device is left as it was, and every call may be captured into a CUDA graph. The
+ * struct is read during the call only. Host-side argument errors return MK_ERR_INVALID_ARG or
+ * MK_ERR_UNSUPPORTED with a line on stderr and enqueue nothing. What only the device can see (a page id
+ * or a length out of range) never leads to an access out of bounds: the call's text says what happens
+ * instead, and, where `status` is not NULL, the mk_op_flag bits are OR-ed into that device int32.
+ * Calls from several host threads, and calls on several streams, may overlap as long as the memory they
+ * write does not. Strides are in elements.
+ *
+ * A paged cache is one tensor for the keys and one for the values, [n_pages][n_kv_heads][page_size]
+ * [head_dim] by any strides with the innermost contiguous; request b's position p lives on page
+ * table[b][p / page_size] at place p % page_size, and its SLOT is table[b][p / page_size] * page_size +
+ * p % page_size. (The caches mk_decode_step_static takes are such a cache with a fixed table: sequence
+ * b's page j is id b * n_kv_heads * max_ctx / page_size + j, with a page stride of page_size * head_dim
+ * and a head stride of max_ctx * head_dim.) e4m3 caches store value / scale, scale fp32 per kv head. */
+typedef enum mk_dtype { MK_BF16 = 0, MK_F16 = 1, MK_F32 = 2, MK_E4M3 = 3 } mk_dtype;
+
+typedef enum mk_op_flag {
+  MK_OP_BAD_PAGE = 1,   /* a page id or slot outside the cache                                     */
+  MK_OP_BAD_LENGTH = 2, /* a length that is negative, inconsistent or beyond the table             */
+  MK_OP_NO_PAGES = 4,   /* mk_page_tables: the ring holds fewer free pages than the step needs      */
+  MK_OP_NO_ROOM = 8     /* mk_page_tables: more new tokens than the slot map has places             */
+} mk_op_flag;
+
+#define MK_PAGE_TABLES_MAX_BATCH 4096
+
+/* Page tables and slot map of one step, built on the device from the requests' lengths. Request b's row of
+ * the table holds pages for held[b] tokens; its new tokens sit at positions start[b] .. start[b] + count[b]
+ * - 1 with start[b] <= held[b], so start < held drops rejected drafts, start = count = 0 ends a request.
+ * With P = page_size, the row then holds ceil((start + count) / P) pages: missing ones are taken from the
+ * ring of free pages in request order, spare ones go back to it in request order.
+ * The ring is ring[(head + i) % ring_size], i = 0 .. n_free - 1, with ring_state = {head, n_free}; pages
+ * are taken at the head and returned behind the tail. ring_size at least n_pages.
+ * Outputs: table (in place: only the entries of newly taken pages are written), ring and ring_state_out
+ * (may be ring_state itself), lens[b] = start + count (may be held, start or count itself); and for each
+ * new token, requests one after the other: slots, positions, owners (its request), with starts[b] the
+ * index of request b's first one (starts[batch]: how many). Places of the slot map behind the last token
+ * get slot -1, position 0, owner -1.
+ * When a length is bad, pages run out or the tokens do not fit n_tokens places, nothing changes: table and
+ * ring stay, ring_state_out and lens repeat ring_state and held, every place gets slot -1, starts are 0.
+ * A page id in the table or ring outside 0 .. n_pages - 1 gives slot -1 (MK_OP_BAD_PAGE).
+ * One launch. Integer arithmetic only: the result does not depend on timing. */
+typedef struct mk_page_tables_args {
+  int32_t* table;              /* device [batch][table_stride], max_pages used per row              */
+  int64_t table_stride;
+  const int32_t* held;         /* device [batch]                                                  */
+  const int32_t* start;        /* device [batch]                                                  */
+  const int32_t* count;        /* device [batch]                                                  */
+  int32_t* ring;               /* device [ring_size]                                              */
+  const int32_t* ring_state;   /* device [2]                                                      */
+  int32_t* ring_state_out;     /* device [2]                                                      */
+  int64_t* slots;              /* device [n_tokens]; may be NULL when n_tokens = 0                  */
+  int32_t* positions;          /* device [n_tokens] or NULL                                       */
+  int32_t* owners;             /* device [n_tokens] or NULL                                       */
+  int32_t* starts;             /* device [batch + 1] or NULL                                      */
+  int32_t* lens;               /* device [batch] or NULL                                          */
+  int32_t* status;             /* device [1] or NULL                                              */
+  int32_t batch;               /* 1 .. MK_PAGE_TABLES_MAX_BATCH                                   */
+  int32_t max_pages, page_size, n_pages, ring_size; /* max_pages * page_size, n_pages * page_size < 2^31 */
+  int32_t n_tokens;            /* places of the slot map                                          */
+} mk_page_tables_args;
+mk_status mk_page_tables(const mk_page_tables_args* args, int device, void* stream);
+
+/* Per-head RMSNorm of queries and keys, rotate-half RoPE and the cache append in one pass.
+ *   y = x / sqrt(mean(x^2) + eps) * gain         (gain NULL: y = x, no norm)
+ *   angle_i = position * inv_freq[i], i < rope_dim / 2; (y_i, y_{i + rope_dim/2}) is turned by angle_i;
+ *   elements from rope_dim on pass.
+ * Norm and rotation are held in fp32, the angles are exact to fp32 at any int32 position (the turn count
+ * is reduced in 64-bit integers), and each value is rounded once, to its output type (e4m3: value / scale,
+ * nearest even, saturating at 448). q_out may be q, k_out may be k (same strides).
+ * Token t's key and value go to slots[t] of the paged cache; a negative slot stores nothing, one outside
+ * the cache stores nothing and sets MK_OP_BAD_PAGE. Two tokens with one slot: either may stay.
+ * Errors: head_dim not a multiple of 16 in 16..256, rope_dim not a multiple of 8 in 0..head_dim, pointers
+ * not 16-byte aligned or strides not multiples of 8 elements (16 for an e4m3 cache). One launch. */
+typedef struct mk_qk_norm_rope_args {
+  const void* q;               /* device [n_tokens][n_q_heads][head_dim], dtype                     */
+  const void* k;               /* device [n_tokens][n_kv_heads][head_dim], dtype                    */
+  const void* v;               /* the same; NULL without a cache                                   */
+  void* q_out;                 /* device [n_tokens][n_q_heads][head_dim], dtype                     */
+  void* k_out;                 /* device [n_tokens][n_kv_heads][head_dim], dtype, or NULL            */
+  const void* q_gain;          /* device [head_dim], dtype, or NULL                                 */
+  const void* k_gain;          /* device [head_dim], dtype, or NULL                                 */
+  const double* inv_freq;      /* device [rope_dim / 2], radians per position; NULL when rope_dim = 0 */
+  const int32_t* positions;    /* device [n_tokens]; NULL when rope_dim = 0                         */
+  const int64_t* slots;        /* device [n_tokens]; NULL without a cache                           */
+  void* k_pages;               /* device, cache_dtype, or NULL: no cache (then v_pages is NULL too)    */
+  void* v_pages;
+  const float* k_scale;        /* device [n_kv_heads], e4m3 caches only                             */
+  const float* v_scale;
+  int32_t* status;
+  int64_t q_stride[2], k_stride[2], v_stride[2], q_out_stride[2], k_out_stride[2];  /* token, head      */
+  int64_t k_page_stride[3], v_page_stride[3];                                       /* page, head, place */
+  int32_t n_tokens, n_q_heads, n_kv_heads, head_dim, rope_dim, n_pages, page_size;
+  int32_t dtype;               /* MK_BF16 or MK_F16                                               */
+  int32_t cache_dtype;         /* dtype or MK_E4M3                                                */
+  float eps;
+} mk_qk_norm_rope_args;
+mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* args, int device, void* stream);
+
+/* Attention of the newest `rows` tokens of each request over its paged cache (rows = 1: a decode step;
+ * rows > 1: a verify block, causal). Request b's last row sees positions 0 .. lens[b] - 1, row r sees
+ * lens[b] - (rows - 1 - r) of them. Query head h reads kv head h / (n_q_heads / n_kv_heads).
+ *   s = scale * q . k,  p = softmax(s),  out = sum p v,  lse = log(sum exp(s)) (natural)
+ * A row that sees nothing gives out = 0 and lse = -infinity. Values in the cache that a row does not see
+ * (positions from lens[b] on, later rows' keys) do not reach it, whatever they hold (NaN included).
+ * Scores, softmax statistics and sums are fp32; out is rounded once.
+ * A length below 0 counts as 0, one beyond max_pages * page_size as that (MK_OP_BAD_LENGTH); keys and
+ * values of a page outside 0 .. n_pages - 1 read as zeros (MK_OP_BAD_PAGE). Table entries of pages a
+ * request does not reach are not read.
+ * Long requests are split over the SMs by a rule on the lengths alone, computed on the device, and joined
+ * in a fixed order: the result does not depend on timing. `workspace` is device scratch of
+ * mk_paged_attention_workspace bytes, 16-byte aligned, with any contents; calls that may overlap need one each.
+ * Errors: head_dim not a multiple of 16 in 16..256; n_q_heads not a multiple of n_kv_heads; pointers not
+ * 16-byte aligned or strides not multiples of 8 elements (16 for an e4m3 cache); too small a workspace.
+ * Two launches (the second joins the splits). */
+typedef struct mk_paged_attention_args {
+  const void* q;               /* device [batch][rows][n_q_heads][head_dim], dtype                  */
+  const void* k_pages;         /* device, cache_dtype                                             */
+  const void* v_pages;
+  const int32_t* table;        /* device [batch][table_stride], max_pages used per row              */
+  const int32_t* lens;         /* device [batch]: positions in the cache, the new rows' included     */
+  const float* k_scale;        /* device [n_kv_heads], e4m3 caches only                             */
+  const float* v_scale;
+  void* out;                   /* device [batch][rows][n_q_heads][head_dim], dtype                  */
+  float* lse;                  /* device [batch][rows][n_q_heads] contiguous, or NULL                 */
+  void* workspace;
+  int32_t* status;
+  int64_t workspace_bytes;
+  int64_t table_stride;
+  int64_t q_stride[3], out_stride[3];              /* batch, row, head                             */
+  int64_t k_page_stride[3], v_page_stride[3];      /* page, head, place                            */
+  int32_t batch, rows, n_q_heads, n_kv_heads, head_dim, n_pages, page_size, max_pages;
+  int32_t dtype;               /* MK_BF16 or MK_F16                                               */
+  int32_t cache_dtype;         /* dtype or MK_E4M3                                                */
+  float scale;
+} mk_paged_attention_args;
+mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream);
+
+/* Bytes of workspace mk_paged_attention needs for these arguments on `device` (reads the shape fields
+ * only: rows, n_q_heads, n_kv_heads, head_dim, dtype, cache_dtype; the batch and the lengths do not matter). */
+mk_status mk_paged_attention_workspace(const mk_paged_attention_args* args, int device, uint64_t* bytes);
+
+#define MK_LOGIT_MAX_HISTORY ((1 << 20) - 1)
+#define MK_LOGIT_MAX_BIASES 2047
+
+/* Penalties, biases and masks on logits, and the greedy token of what is left. For row i, z = logits[i] in
+ * fp32, then for each token v, in this order:
+ *   repetition  v in history[i][0 .. total_len[i]):  z = z > 0 ? z / repetition[i] : z * repetition[i]
+ *   frequency   c = how often v is in history[i][prompt_len[i] .. total_len[i]); c > 0: z -= frequency[i] * c
+ *   presence    c > 0: z -= presence[i]
+ *   bias        v in bias_ids[i]: z += bias_vals (of the last entry that names v)
+ *   mask        bit v % 32 of allowed[i][v / 32] is 0: z = -infinity (whatever z was, NaN included)
+ * out[i] = z in fp32 (may be logits itself when that is fp32), token[i] = the lowest index of the largest z
+ * that is not NaN, -1 when none is above -infinity. Every step is rounded as written (no fused
+ * multiply-add). Ids outside 0 .. vocab - 1 in history and bias_ids are passed over (pad with -1);
+ * total_len counts as within 0 .. max_history, prompt_len as within 0 .. total_len.
+ * mk_decode_step's logits_out is such an input, with batch * rows rows. One launch. */
+typedef struct mk_logit_controls_args {
+  const void* logits;          /* device [rows][logits_stride], dtype                              */
+  float* out;                  /* device [rows][out_stride]                                       */
+  int32_t* token;              /* device [rows] or NULL                                           */
+  const int32_t* history;      /* device [rows][history_stride], max_history used, or NULL           */
+  const int32_t* prompt_len;   /* device [rows] or NULL (= 0: everything was generated)              */
+  const int32_t* total_len;    /* device [rows] or NULL (= max_history)                             */
+  const float* repetition;     /* device [rows] or NULL                                           */
+  const float* presence;       /* device [rows] or NULL                                           */
+  const float* frequency;      /* device [rows] or NULL                                           */
+  const int32_t* bias_ids;     /* device [rows][bias_stride], n_biases used, or NULL                 */
+  const float* bias_vals;      /* the same layout                                                 */
+  const int32_t* allowed;      /* device [rows][allowed_stride], (vocab + 31) / 32 words, or NULL      */
+  int64_t logits_stride, out_stride, history_stride, bias_stride, allowed_stride;
+  int32_t rows, vocab, max_history, n_biases; /* max_history <= MK_LOGIT_MAX_HISTORY, n_biases <= MK_LOGIT_MAX_BIASES */
+  int32_t dtype;               /* MK_F32, MK_BF16 or MK_F16                                        */
+} mk_logit_controls_args;
+mk_status mk_logit_controls(const mk_logit_controls_args* args, int device, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
