@@ -20,11 +20,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 8;        // of a row's cluster
 constexpr int kSlice = 28640;   // tokens of a CTA's slice at most: (28640 + 8) words, two CTAs on an SM
+constexpr int kAhead = 8;       // history tokens a thread loads before it uses the first
 constexpr uint32_t kSeen = 0x80000000u;
 
 struct RowControls {
   float repetition, presence, frequency;
-  bool has_repetition, has_presence, has_frequency, has_mask, has_words;
+  bool has_repetition, has_presence, has_frequency, has_words;
   const float* bias_vals;
 };
 
@@ -42,9 +43,8 @@ __device__ inline float control(float z, uint32_t word, bool allowed, const RowC
   return allowed ? z : -INFINITY;
 }
 
-// Larger key = larger value, then lower index; 0 = nothing above -infinity.
+// Larger key = larger value, then lower index (0 stands for no token).
 __device__ inline unsigned long long key_of(float z, int index) {
-  if (!(z > -INFINITY)) return 0;  // NaN too
   const uint32_t u = __float_as_uint(__fadd_rn(z, 0.0f));  // -0 counts as 0
   const uint32_t rank = u & 0x80000000u ? ~u : u | 0x80000000u;
   return static_cast<unsigned long long>(rank) << 32 | (0xffffffffu - static_cast<uint32_t>(index));
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 2) logit_kernel(const __grid_constan
   const int32_t* hist = a.history ? a.history + row * a.history_stride : nullptr;
   const int32_t* ids = a.bias_ids ? a.bias_ids + row * a.bias_stride : nullptr;
   RowControls c;
-  c.has_repetition = a.repetition, c.has_presence = a.presence, c.has_frequency = a.frequency, c.has_mask = mask;
+  c.has_repetition = a.repetition, c.has_presence = a.presence, c.has_frequency = a.frequency;
   c.repetition = a.repetition ? a.repetition[row] : 1.0f;
   c.presence = a.presence ? a.presence[row] : 0.0f;
   c.frequency = a.frequency ? a.frequency[row] : 0.0f;
@@ -97,13 +97,21 @@ __global__ void __launch_bounds__(kThreads, 2) logit_kernel(const __grid_constan
   const int lead = min(V, static_cast<int>((4 - (reinterpret_cast<uintptr_t>(out) >> 2 & 3)) & 3));
   const bool wide = (reinterpret_cast<uintptr_t>(z + lead) & (4 * sizeof(T) - 1)) == 0;
   const int n_words = (V + 31) >> 5;
-  unsigned long long best = 0;
+  // The greedy token so far: this thread meets its tokens in ascending order, so the first of equals stays.
+  float best_z = -INFINITY;
+  int best_v = -1;
+  auto better = [&](float y, int v) {
+    if (y > best_z) best_z = y, best_v = v;  // NaN never is
+  };
 
   for (long long g0 = lead + static_cast<long long>(rank) * slice; g0 < V || (g0 == lead && rank == 0);
        g0 += static_cast<long long>(kCtas) * slice) {
     const int g = static_cast<int>(g0);
     const int from = g == lead ? 0 : g, to = min(V, g + slice);
     if (c.has_words) {
+      // the logits come into L2 while the words are made
+      for (int i = from + tid * (128 / static_cast<int>(sizeof(T))); i < to; i += kThreads * (128 / static_cast<int>(sizeof(T))))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(z + i));
       __syncthreads();
       for (int i = tid; i < (to - g + 4 + 3) / 4; i += kThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
@@ -112,11 +120,20 @@ __global__ void __launch_bounds__(kThreads, 2) logit_kernel(const __grid_constan
         if (v >= from && v < to) atomicMax(&words[v - g + 4], static_cast<uint32_t>(e + 1));
       }
       __syncthreads();
-      for (int h = tid; h < total; h += kThreads) {
-        const int v = hist[h];
-        if (v < from || v >= to) continue;
-        if (h >= prompt) atomicAdd(&words[v - g + 4], 1u << 11);
-        else atomicOr(&words[v - g + 4], kSeen);
+      for (int h0 = tid; h0 < total; h0 += kThreads * kAhead) {
+        int seen[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int h = h0 + i * kThreads;
+          seen[i] = h < total ? hist[h] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (seen[i] < from || seen[i] >= to) continue;
+          uint32_t* word = &words[seen[i] - g + 4];
+          if (h0 + i * kThreads >= prompt) atomicAdd(word, 1u << 11);
+          else atomicOr(word, kSeen);
+        }
       }
       __syncthreads();
     }
@@ -124,33 +141,43 @@ __global__ void __launch_bounds__(kThreads, 2) logit_kernel(const __grid_constan
       const bool ok = !mask || (static_cast<uint32_t>(mask[v >> 5]) >> (v & 31) & 1);
       const float y = control(load1(z + v), c.has_words ? words[v - g + 4] : 0, ok, c);
       out[v] = y;
-      best = larger(best, key_of(y, v));
+      better(y, v);
     };
     if (tid < g - from) one(from + tid);
     const int groups = (to - g) >> 2;
 #pragma unroll 4
     for (int i = tid; i < groups; i += kThreads) {
       const int v = g + 4 * i;
-      const float4 x = wide ? load4(z + v) : make_float4(load1(z + v), load1(z + v + 1), load1(z + v + 2), load1(z + v + 3));
-      const uint4 w = c.has_words ? reinterpret_cast<const uint4*>(words)[i + 1] : make_uint4(0, 0, 0, 0);
-      uint32_t ok = 0xf;
+      float4 y = wide ? load4(z + v) : make_float4(load1(z + v), load1(z + v + 1), load1(z + v + 2), load1(z + v + 3));
+      if (c.has_words) {
+        const uint4 w = reinterpret_cast<const uint4*>(words)[i + 1];
+        if (w.x | w.y | w.z | w.w) {
+          y.x = control(y.x, w.x, true, c);
+          y.y = control(y.y, w.y, true, c);
+          y.z = control(y.z, w.z, true, c);
+          y.w = control(y.w, w.w, true, c);
+        }
+      }
       if (mask) {
         const uint32_t m0 = mask[v >> 5], m1 = mask[min((v >> 5) + 1, n_words - 1)];
-        ok = __funnelshift_r(m0, m1, v & 31);
+        const uint32_t ok = __funnelshift_r(m0, m1, v & 31);
+        y.x = ok & 1 ? y.x : -INFINITY;
+        y.y = ok & 2 ? y.y : -INFINITY;
+        y.z = ok & 4 ? y.z : -INFINITY;
+        y.w = ok & 8 ? y.w : -INFINITY;
       }
-      float4 y;
-      y.x = control(x.x, w.x, ok & 1, c);
-      y.y = control(x.y, w.y, ok & 2, c);
-      y.z = control(x.z, w.z, ok & 4, c);
-      y.w = control(x.w, w.w, ok & 8, c);
       *reinterpret_cast<float4*>(out + v) = y;
-      best = larger(best, larger(larger(key_of(y.x, v), key_of(y.y, v + 1)), larger(key_of(y.z, v + 2), key_of(y.w, v + 3))));
+      better(y.x, v);
+      better(y.y, v + 1);
+      better(y.z, v + 2);
+      better(y.w, v + 3);
     }
     const int rest = g + 4 * groups;
     if (tid < to - rest) one(rest + tid);
   }
   if (!a.token) return;  // the same for every CTA
 
+  unsigned long long best = best_v < 0 ? 0 : key_of(best_z, best_v);
 #pragma unroll
   for (int d = 16; d; d >>= 1) best = larger(best, __shfl_xor_sync(~0u, best, d));
   if ((tid & 31) == 0) best_of[tid >> 5] = best;

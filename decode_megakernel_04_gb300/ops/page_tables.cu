@@ -16,10 +16,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBatch = MK_PAGE_TABLES_MAX_BATCH;
 constexpr int kPer = kMaxBatch / kThreads;  // requests per thread
+constexpr int kRun = 8;  // neighbouring tokens of one thread, where there are many
 static_assert(kMaxBatch % kThreads == 0, "whole requests per thread");
 
 struct Sums {
@@ -135,24 +136,77 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   const int n_tok = static_cast<int>(total.tokens), n_take = static_cast<int>(total.taken);
   const int n_back = static_cast<int>(total.returned);
   const unsigned size = a.ring_size;
+  const bool whole = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.owners)) & 15) == 0;
 
   int flags = 0;
-#pragma unroll 4
-  for (int t = id; t < a.n_tokens; t += step) {
-    long long slot = -1;
-    int pos = 0, b = -1;
-    if (t < n_tok) {
-      b = owner_of(tok0, B, t);
-      pos = first[b] + t - tok0[b];
-      const int k = pos / P, h = have[b];
-      const int page = k < h ? a.table[b * a.table_stride + k]
-                             : a.ring[(static_cast<unsigned>(head) + take0[b] + (k - h)) % size];
-      if (page >= 0 && page < a.n_pages) slot = static_cast<long long>(page) * P + (pos - k * P);
-      else flags |= MK_OP_BAD_PAGE;
-    }
+  auto page_of = [&](int b, int k) {
+    const int h = have[b];
+    return k < h ? a.table[b * a.table_stride + k] : a.ring[(static_cast<unsigned>(head) + take0[b] + (k - h)) % size];
+  };
+  auto put = [&](int t, long long slot, int pos, int b) {
     a.slots[t] = slot;
     if (a.positions) a.positions[t] = pos;
     if (a.owners) a.owners[t] = b;
+  };
+  if (a.n_tokens <= kRun * step) {
+    for (int t = id; t < a.n_tokens; t += step) {
+      long long slot = -1;
+      int pos = 0, b = -1;
+      if (t < n_tok) {
+        b = owner_of(tok0, B, t);
+        pos = first[b] + t - tok0[b];
+        const int k = pos / P, page = page_of(b, k);
+        if (page >= 0 && page < a.n_pages) slot = static_cast<long long>(page) * P + (pos - k * P);
+        else flags |= MK_OP_BAD_PAGE;
+      }
+      put(t, slot, pos, b);
+    }
+  } else {
+    // Many tokens: a thread takes kRun neighbours, which mostly share a request and a page: one search and one or two
+    // page lookups for all of them, and whole 32-byte sectors of each output.
+    for (long long u = id; u * kRun < a.n_tokens; u += step) {
+      const int t0 = static_cast<int>(u) * kRun;
+      int b = -1, end = 0, pos = 0, at = P;  // end: first token of the next request; at: place on the page
+      long long base = -1;
+      long long slot[kRun];
+      int where[kRun], who[kRun];
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int t = t0 + i;
+        slot[i] = -1, where[i] = 0, who[i] = -1;
+        if (i >= n_tok - t0) continue;
+        ++pos;
+        if (b < 0 || t >= end) {
+          b = owner_of(tok0, B, t);
+          end = b + 1 < B ? tok0[b + 1] : n_tok;
+          pos = first[b] + t - tok0[b];
+          at = P;
+        }
+        if (at >= P) {
+          const int k = pos / P, page = page_of(b, k);
+          at = pos - k * P;
+          const bool ok = page >= 0 && page < a.n_pages;
+          base = ok ? static_cast<long long>(page) * P : -1;
+          if (!ok) flags |= MK_OP_BAD_PAGE;
+        }
+        slot[i] = base < 0 ? -1 : base + at;
+        where[i] = pos, who[i] = b;
+        ++at;
+      }
+      if (whole && a.n_tokens - t0 >= kRun) {
+#pragma unroll
+        for (int i = 0; i < kRun; i += 2) *reinterpret_cast<longlong2*>(a.slots + t0 + i) = make_longlong2(slot[i], slot[i + 1]);
+#pragma unroll
+        for (int i = 0; i < kRun; i += 4) {
+          if (a.positions) *reinterpret_cast<int4*>(a.positions + t0 + i) = make_int4(where[i], where[i + 1], where[i + 2], where[i + 3]);
+          if (a.owners) *reinterpret_cast<int4*>(a.owners + t0 + i) = make_int4(who[i], who[i + 1], who[i + 2], who[i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (i < a.n_tokens - t0) put(t0 + i, slot[i], where[i], who[i]);
+      }
+    }
   }
   for (int j = id; j < n_take; j += step) {
     const int b = owner_of(take0, B, j);

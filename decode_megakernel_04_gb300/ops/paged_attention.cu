@@ -87,9 +87,14 @@ const char* const kMe = "mk_paged_attention";
 // What follows from the shape fields alone: the build, the grid, the workspace.
 struct Plan {
   const Build* build;
-  int dp, group, n_rows, blocks, ctas;
+  int dp, group, n_rows, blocks, ctas, parts;
   size_t piece_at, ml_at, bytes;
 };
+
+// Small calls: a cluster of up to 16 CTAs per (request, kv head, row block) splits its keys evenly and joins through
+// distributed shared memory: no workspace, no second launch, no sums over the batch first. It does not balance ragged
+// requests against each other, so it is for calls whose CTAs are all resident and have at most this much to read each.
+constexpr size_t kClusterBytes = 512 * 1024;
 
 mk_status check_shape(const mk_paged_attention_args& a, int device) {
   if (a.rows < 1 || a.rows > 4096 || a.n_q_heads < 1 || a.n_q_heads > 4096 || a.n_kv_heads < 1 || a.n_q_heads % a.n_kv_heads)
@@ -117,6 +122,23 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
   if (e == cudaSuccess) e = pl.build->occupancy(device, &per_sm);
   if (e != cudaSuccess) return e;
   pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+  pl.parts = 0;
+  pl.ml_at = pl.piece_at = pl.bytes = 0;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.n_kv_heads * pl.blocks;
+  const int64_t key_tiles = (static_cast<int64_t>(a.max_pages) * a.page_size + pl.build->tile - 1) / pl.build->tile;
+  const size_t tile_bytes = 2 * static_cast<size_t>(pl.build->tile) * pl.dp * (a.cache_dtype == MK_E4M3 ? 1 : 2);
+  int parts = 1, resident = 0;
+  if (key_tiles > kMinTiles)
+    for (parts = 16; parts > 1; parts /= 2) {
+      if (parts > key_tiles || items * parts > pl.ctas) continue;
+      if ((e = pl.build->clusters(device, parts, &resident)) != cudaSuccess) return e;
+      if (items <= resident) break;
+    }
+  if ((parts > 1 || key_tiles <= kMinTiles) && items * parts < 1 << 24 && (key_tiles + parts - 1) / parts * tile_bytes <= kClusterBytes) {
+    pl.parts = parts;
+    pl.ctas = static_cast<int>(items) * parts;
+    return cudaSuccess;
+  }
   const size_t slots = 2 * static_cast<size_t>(pl.ctas);
   pl.ml_at = slots * pl.build->rows * pl.dp * sizeof(float);
   pl.piece_at = pl.ml_at + slots * pl.build->rows * sizeof(float2);
@@ -174,25 +196,30 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
     return refuse(MK_ERR_UNSUPPORTED, kMe, "positions beyond 2^31 - 1024");
   if (mk_status s = check_shape(a, device)) return s;
   if (a.batch == 0) return MK_OK;
-  if (!a.q || !a.k_pages || !a.v_pages || !a.table || !a.lens || !a.out || !a.workspace || (e4m3 && (!a.k_scale || !a.v_scale)))
+  if (!a.q || !a.k_pages || !a.v_pages || !a.table || !a.lens || !a.out || (e4m3 && (!a.k_scale || !a.v_scale)))
     return refuse(MK_ERR_INVALID_ARG, kMe, "a required pointer is NULL");
   if (a.table_stride < a.max_pages) return refuse(MK_ERR_INVALID_ARG, kMe, "table rows shorter than max_pages");
   if (!aligned(a.q, 16) || !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) || !aligned(a.out, 16) || !aligned(a.workspace, 16))
     return refuse(MK_ERR_INVALID_ARG, kMe, "a pointer is not 16-byte aligned");
+  // the stride of a dimension of one element is never used
+  const int q_size[3] = {a.batch, a.rows, a.n_q_heads}, page_dims[3] = {a.n_pages, a.n_kv_heads, a.page_size};
   for (int i = 0; i < 3; ++i) {
-    if (a.q_stride[i] % 8 || a.out_stride[i] % 8)
+    if (q_size[i] > 1 && (a.q_stride[i] % 8 || a.out_stride[i] % 8))
       return refuse(MK_ERR_INVALID_ARG, kMe, "a stride is not a multiple of 8 elements");
-    if (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8))
+    if (page_dims[i] > 1 && (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8)))
       return refuse(MK_ERR_INVALID_ARG, kMe, "a cache stride is not a multiple of 16 bytes");
   }
   DeviceGuard guard(device);
   if (guard.err != cudaSuccess) return launched(kMe, guard.err);
   Plan pl;
   if (const cudaError_t e = plan(a, device, &pl)) return launched(kMe, e);
-  if (a.workspace_bytes < static_cast<int64_t>(pl.bytes))
+  if (pl.bytes && (!a.workspace || a.workspace_bytes < static_cast<int64_t>(pl.bytes)))
     return refuse(MK_ERR_INVALID_ARG, kMe, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), pl.bytes);
   char* ws = static_cast<char*>(a.workspace);
+  p.page = div_by(a.page_size);
+  p.group_div = div_by(pl.group);
   p.group = pl.group;
+  p.parts = pl.parts;
   p.n_rows = pl.n_rows;
   p.blocks = pl.blocks;
   p.max_len = a.max_pages * a.page_size;
@@ -202,7 +229,7 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_at);
   p.piece = reinterpret_cast<Piece*>(ws + pl.piece_at);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = pl.build->launch(p, device, s);
-  if (e == cudaSuccess && pl.ctas > 1) e = a.dtype == MK_BF16 ? join<__nv_bfloat16>(p, pl, s) : join<__half>(p, pl, s);
+  cudaError_t e = pl.build->launch(p, s);
+  if (e == cudaSuccess && !pl.parts && pl.ctas > 1) e = a.dtype == MK_BF16 ? join<__nv_bfloat16>(p, pl, s) : join<__half>(p, pl, s);
   return launched(kMe, e);
 }

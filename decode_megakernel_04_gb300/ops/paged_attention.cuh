@@ -21,21 +21,44 @@
 //   queries fp16 scaled per row by a power of two (bf16 mantissas fit; what falls under 2^-24 of a row's largest is
 //   rounded); probabilities are one fp16 (2^-12), an eighth of a bf16 result's rounding.
 #pragma once
+#include <type_traits>
+
+#include <cooperative_groups.h>
+
 #include "mk_ops.cuh"
 
 namespace mkop {
 namespace attn {
 
+namespace cg = cooperative_groups;
+
 constexpr int kMaxCtas = 2048;   // pieces a call is cut into at most
 constexpr int kMinTiles = 2;     // tiles of a piece at least: less is not worth joining
 
+// n / d for 0 <= n < 2^31 by a product: with 2^(k-1) < d <= 2^k, mul = floor(2^(31+k) / d) + 1 is off by at most 1 from
+// 2^(31+k) / d, so n * mul / 2^(31+k) is off by less than 1 / d.
+struct Div {
+  uint32_t mul;
+  int shift;  // k - 1; -1: d = 1
+  __device__ int operator()(int n) const {
+    return shift < 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+  }
+};
+inline Div div_by(int d) {
+  int k = 0;
+  while ((1ll << k) < d) ++k;
+  return {static_cast<uint32_t>((1ull << (31 + k)) / d + 1), k - 1};
+}
+
 struct Params {
   mk_paged_attention_args a;
+  Div page, group_div;
   int group;        // query heads per kv head
   int n_rows;       // query rows of a (request, kv head): rows * group
   int blocks;       // blocks of 16 MT rows
   int max_len;      // max_pages * page_size
   int ctas;         // grid of the attention kernel
+  int parts;        // > 0: clusters of `parts` CTAs share a (request, kv head, row block); 0: pieces of the line
   float scale_log2; // scale * log2(e)
   float* part;      // [2 ctas][16 MT][DP] sums of a part
   float2* part_ml;  // [2 ctas][16 MT] its maximum (log2 units) and sum
@@ -87,11 +110,10 @@ __device__ inline void mma<__half>(float (&c)[4], const uint32_t (&a)[4], uint32
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 codes (the low 16 bits) as an fp16 pair; exact
-__device__ inline uint32_t e4m3_to_f16(uint32_t codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
-  return r;
+// four e4m3 codes as two fp16 pairs; exact
+__device__ inline void e4m3_to_f16(uint32_t (&r)[2], uint32_t codes) {
+  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+      : "=r"(r[0]), "=r"(r[1]) : "r"(codes));
 }
 __device__ inline float exp2_fast(float x) {
   float y;
@@ -124,19 +146,25 @@ struct Shape {
   static constexpr int kOffMeta = kOffAddr + kRing * 2 * kTile * 8;    // Tile [kRing]
   static constexpr int kOffMl = kOffMeta + kRing * 48;                 // float2 [WK][kRows]
   static constexpr int kSmem = kOffMl + WK * kRows * 8;
+  static constexpr int kFit = 227 * 1024 / (kSmem + 1024) < 1 ? 1 : 227 * 1024 / (kSmem + 1024);
+  // CTAs on an SM: what shared memory allows, with at least 168 registers a thread (128 at 64 wide)
+  static constexpr int kRegFit = 65536 / (kThreads * (DP == 64 ? 128 : DP == 128 ? 168 : 255));
+  static constexpr int kCtas = kFit < kRegFit ? kFit : kRegFit < 1 ? 1 : kRegFit;
   static_assert(kWarpKeys % 16 == 0, "a warp's keys are whole k16 steps");
   static_assert(kStageBytes >= WK * kRows * kJoin * 4, "the join fits a stage");
+  static_assert(kStages * kStageBytes >= kRows * DP * 4 + WK * kRows * kJoin * 4, "the cluster's join fits the ring");
   static_assert(kTile <= kThreads, "one thread looks up one key's page");
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
 struct Tile {
-  int b, hm, len, key0;    // request, kv head and row block, its length, first key
+  int b, head, block, len; // request, kv head, row block, the request's length
+  int key0;                // first key
   int first, last;         // of the CTA's part of this request
   int whole;               // the part is the whole request
   int slot;                // else: which of the CTA's two places in the workspace (0: the piece begins with it)
   int q;                   // place in the ring of query rows
-  int pad[3];
+  int pad[2];
 };
 static_assert(sizeof(Tile) == 48, "three 16-byte words");
 
@@ -147,7 +175,8 @@ __device__ inline uint32_t place(int row, int chunk) {  // byte offset of a 16-b
 }
 
 template <typename T, int DP, int MT, bool E4M3>
-__global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads, Shape<DP, MT, E4M3>::kCtas)
+    attention_kernel(const __grid_constant__ Params p) {
   using S = Shape<DP, MT, E4M3>;
   extern __shared__ __align__(128) unsigned char smem[];
   const mk_paged_attention_args& a = p.a;
@@ -164,13 +193,23 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's piece -------------------------------------------------------------------------------------------
+  // ---- this CTA's tiles -------------------------------------------------------------------------------------------
   const int hm_n = a.n_kv_heads * p.blocks;
   auto length = [&](int b) { return min(max(a.lens[b], 0), p.max_len); };
   auto tiles_of = [&](int len) { return max(1, (len + S::kTile - 1) / S::kTile); };  // an empty request has one to write its zeros
-  long long total;
-  int used;
-  {
+  // c_*: the load side's place in the line, the next tile to describe
+  int c_b, c_hm, c_tile, c_len, c_n, c_next_len = 0;
+  long long count;
+  if (p.parts) {
+    const int item = blockIdx.x / p.parts, rank = blockIdx.x - item * p.parts;
+    c_b = item / hm_n;
+    c_hm = item - c_b * hm_n;
+    if (rank == 0 && c_hm == 0 && tid == 0 && (a.lens[c_b] < 0 || a.lens[c_b] > p.max_len)) flag(a.status, MK_OP_BAD_LENGTH);
+    c_len = length(c_b);
+    c_n = tiles_of(c_len);
+    c_tile = static_cast<int>(static_cast<long long>(rank) * c_n / p.parts);
+    count = static_cast<int>(static_cast<long long>(rank + 1) * c_n / p.parts) - c_tile;
+  } else {
     const int per = (a.batch + S::kThreads - 1) / S::kThreads;
     const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
     long long mine = 0;
@@ -186,78 +225,70 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
     }
     if (lane == 31) warp_tiles[warp] = incl;
     __syncthreads();
-    long long before = incl - mine;
-    total = 0;
+    long long before = incl - mine, total = 0;
     for (int w = 0; w < S::kWarps; ++w) {
       if (w < warp) before += warp_tiles[w];
       total += warp_tiles[w];
     }
     total *= hm_n;
     const long long worth = (total + kMinTiles - 1) / kMinTiles;
-    used = worth < p.ctas ? static_cast<int>(worth) : p.ctas;
-    if (static_cast<int>(blockIdx.x) < used) {
-      const long long at = piece_begin(blockIdx.x, total, used);
-      if (before * hm_n <= at && at < (before + mine) * hm_n) {
-        for (int b = b0; b < b1; ++b) {
-          const int n = tiles_of(length(b));
-          if (at < (before + n) * hm_n) {
-            at_b = b;
-            at_rem = at - before * hm_n;
-            break;
-          }
-          before += n;
+    const int used = worth < p.ctas ? static_cast<int>(worth) : p.ctas;
+    const long long begin = piece_begin(blockIdx.x, total, used);
+    if (static_cast<int>(blockIdx.x) < used && before * hm_n <= begin && begin < (before + mine) * hm_n) {
+      for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(length(b));
+        if (begin < (before + n) * hm_n) {
+          at_b = b;
+          at_rem = begin - before * hm_n;
+          break;
         }
+        before += n;
       }
     }
     __syncthreads();
+    if (static_cast<int>(blockIdx.x) >= used) {
+      if (tid == 0) p.piece[blockIdx.x].used = used;
+      return;
+    }
+    count = piece_begin(blockIdx.x + 1, total, used) - begin;
+    c_b = at_b;
+    c_len = length(c_b);
+    c_n = tiles_of(c_len);
+    c_hm = static_cast<int>(at_rem / c_n);
+    c_tile = static_cast<int>(at_rem % c_n);
+    c_next_len = c_b + 1 < a.batch ? length(c_b + 1) : 0;
+    if (tid == 0) {
+      Piece& pc = p.piece[blockIdx.x];
+      pc.total = total;
+      pc.item0 = begin - c_tile;
+      pc.item1 = pc.item0 + c_n;
+      pc.used = used;
+      pc.b = c_b;
+      pc.hm = c_hm;
+    }
   }
-  if (static_cast<int>(blockIdx.x) >= used) {
-    if (tid == 0) p.piece[blockIdx.x].used = used;
-    return;
-  }
-  const long long begin = piece_begin(blockIdx.x, total, used);
-  const long long count = piece_begin(blockIdx.x + 1, total, used) - begin;
-
-  // ---- the load side's place in the line: the next tile to describe ------------------------------------------------
-  int c_b = at_b, c_len = length(c_b), c_n = tiles_of(c_len);
-  int c_hm = static_cast<int>(at_rem / c_n), c_tile = static_cast<int>(at_rem % c_n);
-  int c_next_len = c_b + 1 < a.batch ? length(c_b + 1) : 0;
+  int c_head = c_hm / p.blocks, c_block = c_hm - c_head * p.blocks;
   int c_first_tile = c_tile, c_items = 0;
   long long c_done = 0;
-  if (tid == 0) {
-    Piece& pc = p.piece[blockIdx.x];
-    pc.total = total;
-    pc.item0 = begin - c_tile;
-    pc.item1 = pc.item0 + c_n;
-    pc.used = used;
-    pc.b = c_b;
-    pc.hm = c_hm;
-  }
+
   // A tile is described in two halves with a tile's products between them, so that the page id's load is not waited for.
-  struct Look {
-    int page, key, ok;
+  auto look_up = [&]() -> int {  // the page of this thread's key, -1: no key
+    if (c_done >= count || tid >= S::kTile) return -1;
+    const int key = c_tile * S::kTile + tid;
+    if (key >= c_len) return -1;
+    const int page = a.table[c_b * a.table_stride + p.page(key)];
+    return page >= 0 && page < a.n_pages ? page : -2;
   };
-  auto look_up = [&]() -> Look {
-    Look l{0, 0, 0};
-    if (c_done < count && tid < S::kTile) {
-      l.key = c_tile * S::kTile + tid;
-      l.ok = l.key < c_len;
-      if (l.ok) l.page = a.table[c_b * a.table_stride + l.key / a.page_size];
-    }
-    return l;
-  };
-  auto describe = [&](const Look& l, int ring) {
+  auto describe = [&](int page, int ring) {
     if (c_done >= count) return;
     if (tid < S::kTile) {
       long long k = -1, v = -1;
-      if (l.ok) {
-        if (l.page >= 0 && l.page < a.n_pages) {
-          const int at = l.key % a.page_size;
-          k = l.page * a.k_page_stride[0] + at * a.k_page_stride[2];
-          v = l.page * a.v_page_stride[0] + at * a.v_page_stride[2];
-        } else {
-          flag(a.status, MK_OP_BAD_PAGE);
-        }
+      if (page >= 0) {
+        const int key = c_tile * S::kTile + tid, at = key - p.page(key) * a.page_size;
+        k = (page * a.k_page_stride[0] + c_head * a.k_page_stride[1] + at * a.k_page_stride[2]) * S::kElt;
+        v = (page * a.v_page_stride[0] + c_head * a.v_page_stride[1] + at * a.v_page_stride[2]) * S::kElt;
+      } else if (page == -2) {
+        flag(a.status, MK_OP_BAD_PAGE);
       }
       addr[(ring * 2) * S::kTile + tid] = k;
       addr[(ring * 2 + 1) * S::kTile + tid] = v;
@@ -267,7 +298,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
     const bool last = c_done == count - 1 || c_tile == c_n - 1;
     if (tid == 0) {
       Tile& m = meta[ring];
-      m.b = c_b, m.hm = c_hm, m.len = c_len, m.key0 = c_tile * S::kTile;
+      m.b = c_b, m.head = c_head, m.block = c_block, m.len = c_len, m.key0 = c_tile * S::kTile;
       m.first = first, m.last = last, m.whole = c_first_tile == 0 && c_tile == c_n - 1;
       m.slot = c_done == c_tile - c_first_tile ? 0 : 1;
       m.q = c_items % S::kStages;
@@ -276,38 +307,46 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
     ++c_done;
     if (++c_tile == c_n) {
       c_tile = 0;
-      if (++c_hm == hm_n) {
-        c_hm = 0;
-        ++c_b;
-        c_len = c_next_len;
-        c_n = tiles_of(c_len);
-        c_next_len = c_b + 1 < a.batch ? length(c_b + 1) : 0;
+      if (++c_block == p.blocks) {
+        c_block = 0;
+        if (++c_head == a.n_kv_heads) {
+          c_head = 0;
+          ++c_b;
+          c_len = c_next_len;
+          c_n = tiles_of(c_len);
+          c_next_len = c_b + 1 < a.batch ? length(c_b + 1) : 0;
+        }
       }
     }
   };
+  // A loading thread has one 16-byte column and every kLoadRows-th key.
+  constexpr int kLoaders = S::kThreads & (S::kThreads - 1) ? 128 : S::kThreads;
+  constexpr int kLoadRows = kLoaders / S::kChunks;
+  static_assert(S::kTile % kLoadRows == 0, "whole rounds");
   auto load = [&](int stage, int ring) {
     const Tile m = meta[ring];
-    const int head = m.hm / p.blocks, block = m.hm - head * p.blocks;
-    const long long* ka = addr + (ring * 2) * S::kTile;
-    const long long* va = ka + S::kTile;
-    const unsigned char* kp = static_cast<const unsigned char*>(a.k_pages) + head * a.k_page_stride[1] * S::kElt;
-    const unsigned char* vp = static_cast<const unsigned char*>(a.v_pages) + head * a.v_page_stride[1] * S::kElt;
     const uint32_t kd = s0 + S::kOffKV + stage * S::kStageBytes, vd = kd + S::kKeyBytes;
-#pragma unroll 4
-    for (int i = tid; i < S::kTile * S::kChunks; i += S::kThreads) {
-      const int row = i / S::kChunks, chunk = i % S::kChunks;
+    if (kLoaders == S::kThreads || tid < kLoaders) {
+      const int chunk = tid % S::kChunks, row0 = tid / S::kChunks;
       const bool in = chunk * 16 < a.head_dim * S::kElt;
-      const long long k = ka[row], v = va[row];
-      cp16(kd + place<S::kChunks>(row, chunk), k >= 0 ? kp + k * S::kElt + chunk * 16 : kp, in && k >= 0);
-      cp16(vd + place<S::kChunks>(row, chunk), v >= 0 ? vp + v * S::kElt + chunk * 16 : vp, in && v >= 0);
+      const long long* at = addr + (ring * 2) * S::kTile + row0;
+      const unsigned char* kp = static_cast<const unsigned char*>(a.k_pages) + (in ? chunk * 16 : 0);
+      const unsigned char* vp = static_cast<const unsigned char*>(a.v_pages) + (in ? chunk * 16 : 0);
+#pragma unroll 8
+      for (int i = 0; i < S::kTile / kLoadRows; ++i) {
+        const uint32_t to = place<S::kChunks>(row0 + i * kLoadRows, chunk);
+        const long long k = at[i * kLoadRows], v = at[S::kTile + i * kLoadRows];
+        cp16(kd + to, kp + max(k, 0ll), in && k >= 0);
+        cp16(vd + to, vp + max(v, 0ll), in && v >= 0);
+      }
     }
     if (m.first) {
       const uint32_t qd = s0 + S::kOffQ + m.q * S::kQBytes;
       const unsigned char* q = static_cast<const unsigned char*>(a.q);
       for (int i = tid; i < S::kRows * (DP / 8); i += S::kThreads) {
-        const int row = i / (DP / 8), chunk = i % (DP / 8), mrow = block * S::kRows + row;
+        const int row = i / (DP / 8), chunk = i % (DP / 8), mrow = m.block * S::kRows + row;
         const bool in = mrow < p.n_rows && chunk * 8 < a.head_dim;
-        const int r = mrow / p.group, h = head * p.group + mrow - r * p.group;
+        const int r = p.group_div(mrow), h = m.head * p.group + mrow - r * p.group;
         const long long off = in ? m.b * a.q_stride[0] + r * a.q_stride[1] + h * a.q_stride[2] + chunk * 8 : 0;
         cp16(qd + place<DP / 8>(row, chunk), q + off * 2, in);
       }
@@ -325,10 +364,78 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
   }
 
   float o[DP / 8][4];
-  float m_run[2], l_run[2];
+  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0, 0};
   uint32_t qf[DP / 16][4];
   float row_scale[2];
   int limit[2];
+#pragma unroll
+  for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0;
+
+  // Joins the warps that share rows: their sums, kJoin columns at a time, through `buf` ([WK][kRows][kJoin]);
+  // sink(row, first of 4 columns, sums, largest maximum, sum of exponentials) gets every row below `rows`.
+  auto join_warps = [&](float* buf, int rows, auto&& sink) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l_run[h] += __shfl_xor_sync(~0u, l_run[h], 1);
+      l_run[h] += __shfl_xor_sync(~0u, l_run[h], 2);
+      if (t4 == 0) ml[wk * S::kRows + wm * 16 + g + 8 * h] = make_float2(m_run[h], l_run[h]);
+    }
+#pragma unroll
+    for (int c = 0; c < DP / S::kJoin; ++c) {
+      __syncthreads();  // what buf held (c = 0) or the last columns have been read by every warp
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = wm * 16 + g + 8 * h;
+        float* to = buf + (wk * S::kRows + row) * S::kJoin;
+        const int turn = (row & 3) * 8;  // spreads the rows over the banks
+#pragma unroll
+        for (int i = 0; i < S::kJoin / 16; ++i) {
+          const int n = c * (S::kJoin / 8) + 2 * i;
+          if (!E4M3) {
+            *reinterpret_cast<float2*>(to + ((16 * i + 2 * t4) ^ turn)) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+            *reinterpret_cast<float2*>(to + ((16 * i + 8 + 2 * t4) ^ turn)) = make_float2(o[n + 1][2 * h], o[n + 1][2 * h + 1]);
+          } else {
+            *reinterpret_cast<float4*>(to + ((16 * i + 4 * t4) ^ turn)) =
+                make_float4(o[n][2 * h], o[n + 1][2 * h], o[n][2 * h + 1], o[n + 1][2 * h + 1]);
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * (S::kJoin / 4); i += S::kThreads) {
+        const int row = i / (S::kJoin / 4), col = (i % (S::kJoin / 4)) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < S::WK; ++w) top = fmaxf(top, ml[w * S::kRows + row].x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0;
+        float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < S::WK; ++w) {
+          const float2 s = ml[w * S::kRows + row];
+          const float f = exp2_fast(s.x - base);
+          const float4 x = *reinterpret_cast<const float4*>(buf + (w * S::kRows + row) * S::kJoin + (col ^ ((row & 3) * 8)));
+          sum += f * s.y;
+          y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+        }
+        sink(row, c * S::kJoin + col, y, top, sum);
+      }
+    }
+  };
+  // 4 columns of a finished row
+  auto finish = [&](int b, int head, int block, int row, int d, float4 y, float top, float sum) {
+    if (d >= a.head_dim) return;
+    const int mrow = block * S::kRows + row, r = p.group_div(mrow), h = head * p.group + mrow - r * p.group;
+    const float f = sum == 0.0f ? 0.0f : (E4M3 ? a.v_scale[head] : 1.0f) / sum;
+    const uint2 u = a.dtype == MK_BF16
+                        ? make_uint2(pack2<__nv_bfloat16>(y.x * f, y.y * f), pack2<__nv_bfloat16>(y.z * f, y.w * f))
+                        : make_uint2(pack2<__half>(y.x * f, y.y * f), pack2<__half>(y.z * f, y.w * f));
+    uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2] + d;
+    *reinterpret_cast<uint2*>(out) = u;
+    if (d == 0 && a.lse)
+      a.lse[(static_cast<long long>(b) * a.rows + r) * a.n_q_heads + h] =
+          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+  };
+
   int stage = 0, ring = 0;
 #pragma unroll 1
   for (long long j = 0; j < count; ++j) {
@@ -339,9 +446,8 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
       if (j + ahead < count) load((stage + ahead) % S::kStages, (ring + ahead) % S::kRing);
       cp_commit();
     }
-    const Look next = look_up();
+    const int next = look_up();
     const Tile m = meta[ring];
-    const int head = m.hm / p.blocks, block = m.hm - head * p.blocks;
     if (m.first) {
       const uint32_t qd = s0 + S::kOffQ + m.q * S::kQBytes;
       if (!E4M3) {
@@ -352,7 +458,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
       } else {
         // Key fragments hold 4 neighbouring elements a lane (one byte each), so the k order within 16 is that of
         // the lanes' quadruples; the query fragments follow it.
-        const float ks = p.scale_log2 * a.k_scale[head];
+        const float ks = p.scale_log2 * a.k_scale[m.head];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = wm * 16 + g + 8 * h;
@@ -390,8 +496,8 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
       l_run[0] = l_run[1] = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int mrow = block * S::kRows + wm * 16 + g + 8 * h;
-        limit[h] = mrow < p.n_rows ? m.len - (a.rows - 1 - mrow / p.group) : 0;
+        const int mrow = m.block * S::kRows + wm * 16 + g + 8 * h;
+        limit[h] = mrow < p.n_rows ? m.len - (a.rows - 1 - p.group_div(mrow)) : 0;
       }
     }
 
@@ -423,19 +529,29 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
             uint32_t f[4];
             ldsm4(f, kd + place<S::kChunks>(kb + 8 * n + (lane & 7), 4 * k + (lane >> 3)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma<T>(s[n], qf[4 * k + i], e4m3_to_f16(f[i]), e4m3_to_f16(f[i] >> 16));
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b[2];
+              e4m3_to_f16(b, f[i]);
+              mma<T>(s[n], qf[4 * k + i], b[0], b[1]);
+            }
           }
       }
       const bool ragged = key + S::kBlock > all_see;
+#pragma unroll
+      for (int n = 0; n < S::kBlock / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] *= row_scale[i >> 1];
+      if (ragged)
+#pragma unroll
+        for (int n = 0; n < S::kBlock / 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key + 8 * n + 2 * t4 + (i & 1) >= limit[i >> 1]) s[n][i] = -INFINITY;
       float top[2] = {m_run[0], m_run[1]};
 #pragma unroll
       for (int n = 0; n < S::kBlock / 8; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[n][i] *= row_scale[i >> 1];
-          if (ragged && key + 8 * n + 2 * t4 + (i & 1) >= limit[i >> 1]) s[n][i] = -INFINITY;
-          top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
-        }
+        for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
       float base[2];
       bool grew = false;
 #pragma unroll
@@ -462,55 +578,64 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
           s[n][i] = exp2_fast(s[n][i] - base[i >> 1]);
           l_run[i >> 1] += s[n][i];
         }
-      // Keys that some rows see and others do not (at most rows - 1): a hidden value must not reach a row even times 0
-      // (it may be NaN), so they leave the product and are added one by one below.
-      const bool mixed = ragged && a.rows > 1;
+      // o += p v. Keys that some rows see and others do not (at most rows - 1): a hidden value must not reach a row
+      // even times 0 (it may be NaN), so they leave the product (Mixed) and are added one by one below.
+      auto add_values = [&](auto mixed_tag) {
+        constexpr bool kMixed = decltype(mixed_tag)::value;
 #pragma unroll
-      for (int q = 0; q < S::kBlock / 16; ++q) {
-        uint32_t hi[4], lo[4];
+        for (int q = 0; q < S::kBlock / 16; ++q) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = s[2 * q + (i >> 1)][2 * (i & 1)], y = s[2 * q + (i >> 1)][2 * (i & 1) + 1];
-          hi[i] = pack2<T>(x, y);
-          if (!E4M3) {
-            const float2 r = unpack2<T>(hi[i]);
-            lo[i] = pack2<T>(x - r.x, y - r.y);
+          for (int i = 0; i < 4; ++i) {
+            const float x = s[2 * q + (i >> 1)][2 * (i & 1)], y = s[2 * q + (i >> 1)][2 * (i & 1) + 1];
+            hi[i] = pack2<T>(x, y);
+            if (!E4M3) {
+              const float2 r = unpack2<T>(hi[i]);
+              lo[i] = pack2<T>(x - r.x, y - r.y);
+            }
           }
-        }
-        uint32_t keep0 = ~0u, keep1 = ~0u;
-        if (mixed) {
-          const int k0 = key + 16 * q + 2 * t4;
-          keep0 = (k0 < all_see ? 0xffffu : 0) | (k0 + 1 < all_see ? 0xffff0000u : 0);
-          keep1 = (k0 + 8 < all_see ? 0xffffu : 0) | (k0 + 9 < all_see ? 0xffff0000u : 0);
-        }
-        const int vrow = kb + 16 * q + (lane & 7) + ((lane >> 3) & 1) * 8;
-        if (!E4M3) {
-#pragma unroll
-          for (int d = 0; d < DP / 16; ++d) {
-            uint32_t f[4];
-            ldsm4t(f, vd + place<S::kChunks>(vrow, 2 * d + (lane >> 4)));
-            f[0] &= keep0, f[1] &= keep1, f[2] &= keep0, f[3] &= keep1;
-            mma<T>(o[2 * d], hi, f[0], f[1]);
-            mma<T>(o[2 * d + 1], hi, f[2], f[3]);
-            mma<T>(o[2 * d], lo, f[0], f[1]);
-            mma<T>(o[2 * d + 1], lo, f[2], f[3]);
-          }
-        } else {
-          // transposed pairs of bytes: even elements of 16 make one n8 tile, odd ones the next
-#pragma unroll
-          for (int d = 0; d < DP / 32; ++d) {
-            uint32_t f[4];
-            ldsm4t(f, vd + place<S::kChunks>(vrow, 2 * d + (lane >> 4)));
+          uint32_t keep[2] = {~0u, ~0u};
+          if (kMixed)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t u = __byte_perm(f[2 * i], 0, 0x3120), v = __byte_perm(f[2 * i + 1], 0, 0x3120);
-              mma<T>(o[4 * d + 2 * i], hi, e4m3_to_f16(u) & keep0, e4m3_to_f16(v) & keep1);
-              mma<T>(o[4 * d + 2 * i + 1], hi, e4m3_to_f16(u >> 16) & keep0, e4m3_to_f16(v >> 16) & keep1);
+              const int k0 = key + 16 * q + 8 * i + 2 * t4;
+              keep[i] = (k0 < all_see ? 0xffffu : 0) | (k0 + 1 < all_see ? 0xffff0000u : 0);
+            }
+          const int vrow = kb + 16 * q + (lane & 7) + ((lane >> 3) & 1) * 8;
+          if (!E4M3) {
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) {
+              uint32_t f[4];
+              ldsm4t(f, vd + place<S::kChunks>(vrow, 2 * d + (lane >> 4)));
+              if (kMixed) f[0] &= keep[0], f[1] &= keep[1], f[2] &= keep[0], f[3] &= keep[1];
+              mma<T>(o[2 * d], hi, f[0], f[1]);
+              mma<T>(o[2 * d + 1], hi, f[2], f[3]);
+              mma<T>(o[2 * d], lo, f[0], f[1]);
+              mma<T>(o[2 * d + 1], lo, f[2], f[3]);
+            }
+          } else {
+            // transposed pairs of bytes: even elements of 16 make one n8 tile, odd ones the next
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) {
+              uint32_t f[4];
+              ldsm4t(f, vd + place<S::kChunks>(vrow, 2 * d + (lane >> 4)));
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t u[2], v[2];
+                e4m3_to_f16(u, __byte_perm(f[2 * i], 0, 0x3120));
+                e4m3_to_f16(v, __byte_perm(f[2 * i + 1], 0, 0x3120));
+                if (kMixed) u[0] &= keep[0], u[1] &= keep[0], v[0] &= keep[1], v[1] &= keep[1];
+                mma<T>(o[4 * d + 2 * i], hi, u[0], v[0]);
+                mma<T>(o[4 * d + 2 * i + 1], hi, u[1], v[1]);
+              }
             }
           }
         }
-      }
-      if (mixed) {
+      };
+      if (!ragged || a.rows == 1) {
+        add_values(std::false_type{});
+      } else {
+        add_values(std::true_type{});
 #pragma unroll 1
         for (int x = max(0, all_see - key); x < S::kBlock && key + x < m.len; ++x) {
           // the probability of key x sits with lane (x % 8) / 2 of each row's quad
@@ -535,8 +660,9 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
             } else {
               const int d = 16 * (i >> 1) + 4 * t4;  // this tile's elements: d + (i & 1), d + 2 + (i & 1)
               const uint32_t u = *reinterpret_cast<const uint32_t*>(row + place<S::kChunks>(kb + x, d / 16) + d % 16);
-              const uint32_t pair = __byte_perm(u, 0, 0x3120) >> (i & 1 ? 16 : 0);
-              v = unpack2<__half>(e4m3_to_f16(pair));
+              uint32_t pair[2];
+              e4m3_to_f16(pair, __byte_perm(u, 0, 0x3120));
+              v = unpack2<__half>(pair[i & 1]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -546,107 +672,116 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads) attention_kerne
       }
     }
 
-    // ---- the end of this CTA's part of the request: join the warps, write -------------------------------------------------
-    if (m.last) {
-      float* buf = reinterpret_cast<float*>(smem + S::kOffKV + stage * S::kStageBytes);  // [WK][kRows][kJoin]
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l_run[h] += __shfl_xor_sync(~0u, l_run[h], 1);
-        l_run[h] += __shfl_xor_sync(~0u, l_run[h], 2);
-        if (t4 == 0) ml[wk * S::kRows + wm * 16 + g + 8 * h] = make_float2(m_run[h], l_run[h]);
-      }
-      const int rows = min(S::kRows, p.n_rows - block * S::kRows);
+    if (m.last && !p.parts) {  // the end of this CTA's part of the request
       const long long slot = 2ll * blockIdx.x + m.slot;
-#pragma unroll
-      for (int c = 0; c < DP / S::kJoin; ++c) {
-        __syncthreads();  // the tile (c = 0) or the last columns have been read by every warp
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = wm * 16 + g + 8 * h;
-          float* to = buf + (wk * S::kRows + row) * S::kJoin;
-          const int turn = (row & 3) * 8;  // spreads the rows over the banks
-#pragma unroll
-          for (int i = 0; i < S::kJoin / 16; ++i) {
-            const int n = c * (S::kJoin / 8) + 2 * i;
-            if (!E4M3) {
-              *reinterpret_cast<float2*>(to + ((16 * i + 2 * t4) ^ turn)) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
-              *reinterpret_cast<float2*>(to + ((16 * i + 8 + 2 * t4) ^ turn)) = make_float2(o[n + 1][2 * h], o[n + 1][2 * h + 1]);
-            } else {
-              *reinterpret_cast<float4*>(to + ((16 * i + 4 * t4) ^ turn)) =
-                  make_float4(o[n][2 * h], o[n + 1][2 * h], o[n][2 * h + 1], o[n + 1][2 * h + 1]);
-            }
-          }
-        }
-        __syncthreads();
-        for (int i = tid; i < rows * (S::kJoin / 4); i += S::kThreads) {
-          const int row = i / (S::kJoin / 4), col = (i % (S::kJoin / 4)) * 4, d = c * S::kJoin + col;
-          float top = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < S::WK; ++w) top = fmaxf(top, ml[w * S::kRows + row].x);
-          const float base = top == -INFINITY ? 0.0f : top;
-          float sum = 0;
-          float4 y = make_float4(0, 0, 0, 0);
-#pragma unroll
-          for (int w = 0; w < S::WK; ++w) {
-            const float2 s = ml[w * S::kRows + row];
-            const float f = exp2_fast(s.x - base);
-            const float4 x = *reinterpret_cast<const float4*>(buf + (w * S::kRows + row) * S::kJoin + (col ^ ((row & 3) * 8)));
-            sum += f * s.y;
-            y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
-          }
-          if (!m.whole) {
-            *reinterpret_cast<float4*>(p.part + (slot * S::kRows + row) * DP + d) = y;
-            if (d == 0) p.part_ml[slot * S::kRows + row] = make_float2(top, sum);
-          } else if (d < a.head_dim) {
-            const int mrow = block * S::kRows + row, r = mrow / p.group, h = head * p.group + mrow - r * p.group;
-            const float f = sum == 0.0f ? 0.0f : (E4M3 ? a.v_scale[head] : 1.0f) / sum;
-            const uint2 u = a.dtype == MK_BF16
-                                ? make_uint2(pack2<__nv_bfloat16>(y.x * f, y.y * f), pack2<__nv_bfloat16>(y.z * f, y.w * f))
-                                : make_uint2(pack2<__half>(y.x * f, y.y * f), pack2<__half>(y.z * f, y.w * f));
-            uint16_t* out = static_cast<uint16_t*>(a.out) + m.b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2] + d;
-            *reinterpret_cast<uint2*>(out) = u;
-            if (d == 0 && a.lse)
-              a.lse[(static_cast<long long>(m.b) * a.rows + r) * a.n_q_heads + h] =
-                  sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
-          }
-        }
-      }
+      join_warps(reinterpret_cast<float*>(smem + S::kOffKV + stage * S::kStageBytes),
+                 min(S::kRows, p.n_rows - m.block * S::kRows), [&](int row, int d, float4 y, float top, float sum) {
+                   if (m.whole) {
+                     finish(m.b, m.head, m.block, row, d, y, top, sum);
+                   } else {
+                     *reinterpret_cast<float4*>(p.part + (slot * S::kRows + row) * DP + d) = y;
+                     if (d == 0) p.part_ml[slot * S::kRows + row] = make_float2(top, sum);
+                   }
+                 });
     }
     describe(next, (ring + S::kStages) % S::kRing);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
     ring = ring + 1 == S::kRing ? 0 : ring + 1;
   }
   cp_wait<0>();
+  if (!p.parts) return;
+
+  // ---- a cluster's join: each CTA's rows in its own shared memory, then each CTA sums its share of the columns ------------
+  cg::cluster_group cluster = cg::this_cluster();
+  const int item = blockIdx.x / p.parts, rank = blockIdx.x - item * p.parts;
+  const int b = item / hm_n, hm = item - b * hm_n, head = hm / p.blocks, block = hm - head * p.blocks;
+  const int rows = min(S::kRows, p.n_rows - block * S::kRows);
+  float* mine = reinterpret_cast<float*>(smem + S::kOffKV);           // [kRows][DP]
+  float2* mine_ml = reinterpret_cast<float2*>(smem + S::kOffQ);       // [kRows]
+  join_warps(reinterpret_cast<float*>(smem + S::kOffKV + S::kRows * DP * 4), rows,
+             [&](int row, int d, float4 y, float top, float sum) {
+               *reinterpret_cast<float4*>(mine + row * DP + d) = y;
+               if (d == 0) mine_ml[row] = make_float2(top, sum);
+             });
+  cluster.sync();
+  for (int i = tid * p.parts + rank; i < rows * (DP / 4); i += S::kThreads * p.parts) {
+    const int row = i / (DP / 4), d = (i % (DP / 4)) * 4;
+    float top = -INFINITY;
+    for (int c = 0; c < p.parts; ++c) top = fmaxf(top, cluster.map_shared_rank(mine_ml, c)[row].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0;
+    float4 y = make_float4(0, 0, 0, 0);
+    for (int c = 0; c < p.parts; ++c) {
+      const float2 s = cluster.map_shared_rank(mine_ml, c)[row];
+      const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(mine, c) + row * DP + d);
+      const float f = exp2_fast(s.x - base);
+      sum += f * s.y;
+      y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+    }
+    finish(b, head, block, row, d, y, top, sum);
+  }
+  cluster.sync();  // the others' shared memory stays until it has been read
 }
 
 // One build's launch facts, filled by the three translation units that hold the kernels.
 struct Build {
-  int rows, tile, threads, smem;
+  int rows, tile;
   cudaError_t (*occupancy)(int device, int* ctas_per_sm);
-  cudaError_t (*launch)(const Params& p, int device, cudaStream_t s);
+  cudaError_t (*clusters)(int device, int parts, int* resident);
+  cudaError_t (*launch)(const Params& p, cudaStream_t s);
 };
 
 template <typename T, int DP, int MT, bool E4M3>
 struct Make {
   using S = Shape<DP, MT, E4M3>;
+  static constexpr auto kKernel = attention_kernel<T, DP, MT, E4M3>;
   static cudaError_t occupancy(int device, int* n) {
     static std::atomic<int> known[kMaxDevices];
     *n = known[device].load(std::memory_order_relaxed);
     if (*n) return cudaSuccess;
-    cudaError_t e = allow_smem<attention_kernel<T, DP, MT, E4M3>>(device, S::kSmem);
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, attention_kernel<T, DP, MT, E4M3>, S::kThreads, S::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kKernel, S::kThreads, S::kSmem);
     if (e == cudaSuccess && *n < 1) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess) known[device].store(*n, std::memory_order_relaxed);
     return e;
   }
-  static cudaError_t launch(const Params& p, int device, cudaStream_t s) {
-    const cudaError_t e = allow_smem<attention_kernel<T, DP, MT, E4M3>>(device, S::kSmem);
-    if (e != cudaSuccess) return e;
-    attention_kernel<T, DP, MT, E4M3><<<p.ctas, S::kThreads, S::kSmem, s>>>(p);
-    return cudaGetLastError();
+  static cudaLaunchConfig_t config(int ctas, int parts, cudaLaunchAttribute* at, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    if (parts) {
+      at->id = cudaLaunchAttributeClusterDimension;
+      at->val.clusterDim.x = parts;
+      at->val.clusterDim.y = at->val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+    }
+    return cfg;
   }
-  static constexpr Build build() { return {S::kRows, S::kTile, S::kThreads, S::kSmem, occupancy, launch}; }
+  // clusters of 2, 4, 8 or 16 CTAs the device holds at once (0: none); occupancy() has run
+  static cudaError_t clusters(int device, int parts, int* n) {
+    static std::atomic<int> known[kMaxDevices][17];
+    const int k = known[device][parts].load(std::memory_order_relaxed);
+    *n = k - 1;
+    if (k) return cudaSuccess;
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t cfg = config(parts, parts, at, nullptr);
+    if (cudaOccupancyMaxActiveClusters(n, kKernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // a size the device does not have
+      *n = 0;
+    }
+    known[device][parts].store(*n + 1, std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+  static cudaError_t launch(const Params& p, cudaStream_t s) {
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t cfg = config(p.ctas, p.parts, at, s);
+    return cudaLaunchKernelEx(&cfg, kKernel, p);
+  }
+  static constexpr Build build() { return {S::kRows, S::kTile, occupancy, clusters, launch}; }
 };
 
 template <typename T, bool E4M3>

@@ -10,6 +10,8 @@
 // Angles: inv_freq / (2 pi) is turned into a 64-bit binary fraction of a turn; position x fraction mod 2^64 is then the
 // exact phase whatever the position, and its upper 32 bits (as a signed half-turn count) go to sincospif. An fp32
 // product position x inv_freq would be off by 2^-24 of the angle: 0.06 rad at a million positions.
+#include <type_traits>
+
 #include "mk_ops.cuh"
 
 namespace mkop {
@@ -24,41 +26,50 @@ __device__ inline uint64_t turns_of(double inv_freq) {
   return __double2ull_rn(t * 18446744073709551616.0);  // a fraction that rounds to one turn saturates, 2^-64 off
 }
 
-__device__ inline uint32_t e4m3x4(const float* x, float scale) {
+__device__ inline uint32_t e4m3x4(const float* x, float inv) {
   uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] / scale), "f"(x[0] / scale));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] / scale), "f"(x[2] / scale));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * inv), "f"(x[2] * inv));
   return lo | static_cast<uint32_t>(hi) << 16;
 }
 
+enum Kind { kQuery, kKey, kValue };
+
 struct Work {
   mk_qk_norm_rope_args a;
-  int heads;       // rows of work per token: queries, keys, values
-  int per_item;    // of them in one item (one warp's turn)
-  int parts;       // items per token
+  int q_rounds, k_rounds, rounds;  // rounds of kBatch * 32 / L heads of a token: queries, keys, and with the values
+  int per_item;                    // rounds of one item (one warp's turn)
+  int parts;                       // items per token
+  float inv_width;                 // 1 / head_dim
 };
 
 template <typename T, int L, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) qk_kernel(const __grid_constant__ Work w) {
+__global__ void __launch_bounds__(kWarps * 32, 3) qk_kernel(const __grid_constant__ Work w) {
   const mk_qk_norm_rope_args& a = w.a;
   constexpr int H = 32 / L;  // heads a warp holds at once
   const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
-  const int D = a.head_dim, half = a.rope_dim / 2;
-  const bool live = 8 * l < D, turned = 8 * l < a.rope_dim;
+  const int half = a.rope_dim / 2;
+  const bool live = 8 * l < a.head_dim, turned = live && 8 * l < a.rope_dim;
   // where this lane's two groups of 4 elements sit in a head
   const int lo = turned ? 4 * l : 8 * l, hi = turned ? 4 * l + half : 8 * l + 4;
   uint64_t turns[4] = {0, 0, 0, 0};
-  if (turned && live)
+  if (turned)
 #pragma unroll
     for (int i = 0; i < 4; ++i) turns[i] = turns_of(a.inv_freq[4 * l + i]);
+  uint2 gains[2][2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const T* gain = static_cast<const T*>(i ? a.k_gain : a.q_gain);
+    if (gain && live) gains[i][0] = *reinterpret_cast<const uint2*>(gain + lo), gains[i][1] = *reinterpret_cast<const uint2*>(gain + hi);
+  }
 
   const long long items = static_cast<long long>(a.n_tokens) * w.parts;
   const long long n_warps = static_cast<long long>(gridDim.x) * kWarps;
   for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += n_warps) {
     const int t = static_cast<int>(it / w.parts), part = static_cast<int>(it - static_cast<long long>(t) * w.parts);
-    const int r0 = part * w.per_item, r1 = min(w.heads, r0 + w.per_item);
-    float c[4], s[4];
-    if (turned && live) {
+    const int r0 = part * w.per_item, r1 = min(w.rounds, r0 + w.per_item);
+    float c[4] = {1, 1, 1, 1}, s[4] = {0, 0, 0, 0};
+    if (turned && r0 < w.q_rounds + w.k_rounds) {
       const int64_t pos = a.positions[t];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -68,7 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_kernel(const __grid_constant__
       }
     }
     long long k_at = -1, v_at = -1;  // the slot's place in the cache
-    if (a.k_pages && r1 > a.n_q_heads) {
+    if (a.k_pages && r1 > w.q_rounds) {
       const long long slot = a.slots[t];
       if (slot >= static_cast<long long>(a.n_pages) * a.page_size) {
         if (lane == 0) flag(a.status, MK_OP_BAD_PAGE);
@@ -78,89 +89,87 @@ __global__ void __launch_bounds__(kWarps * 32) qk_kernel(const __grid_constant__
         v_at = page * a.v_page_stride[0] + place * a.v_page_stride[2];
       }
     }
-    for (int r = r0; r < r1; r += H * kBatch) {
+    // One round: kBatch x H heads of one kind, from `first` on. out: q_out or k_out (NULL: none); pages: the cache
+    // (NULL: none), at: the token's place in it.
+    auto round = [&](auto kind_tag, int first, int n, const T* x, const int64_t* xs, T* out, const int64_t* os,
+                     void* pages, long long at, const int64_t* ps, const float* scales) {
+      constexpr Kind kind = decltype(kind_tag)::value;
+      const int row0 = first + sub;
+      x += t * xs[0] + row0 * xs[1];
       uint2 in[kBatch][2];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int row = r + j * H + sub;
         in[j][0] = in[j][1] = make_uint2(0, 0);
-        if (row >= r1 || !live) continue;
-        const T* x;
-        if (row < a.n_q_heads) {
-          x = static_cast<const T*>(a.q) + t * a.q_stride[0] + row * a.q_stride[1];
-        } else if (row < a.n_q_heads + a.n_kv_heads) {
-          x = static_cast<const T*>(a.k) + t * a.k_stride[0] + (row - a.n_q_heads) * a.k_stride[1];
-        } else {
-          if (v_at < 0) continue;
-          x = static_cast<const T*>(a.v) + t * a.v_stride[0] + (row - a.n_q_heads - a.n_kv_heads) * a.v_stride[1];
+        if (row0 + j * H < n && live) {
+          in[j][0] = *reinterpret_cast<const uint2*>(x + j * H * xs[1] + lo);
+          in[j][1] = *reinterpret_cast<const uint2*>(x + j * H * xs[1] + hi);
         }
-        in[j][0] = *reinterpret_cast<const uint2*>(x + lo);
-        in[j][1] = *reinterpret_cast<const uint2*>(x + hi);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int row = r + j * H + sub;
-        if (r + j * H >= r1) break;  // the whole warp
-        const bool is_q = row < a.n_q_heads, is_v = row >= a.n_q_heads + a.n_kv_heads;
-        float x[8];
+        const int row = row0 + j * H;
+        if (first + j * H >= n) break;  // the whole warp
+        float y[8];
+        uint2 packed[2] = {in[j][0], in[j][1]};
+        if (kind != kValue || E4M3)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 p = unpack2<T>(in[j][i].x), q = unpack2<T>(in[j][i].y);
-          x[4 * i] = p.x, x[4 * i + 1] = p.y, x[4 * i + 2] = q.x, x[4 * i + 3] = q.y;
-        }
-        float ss = 0;
+          for (int i = 0; i < 2; ++i) {
+            const float2 p = unpack2<T>(packed[i].x), q = unpack2<T>(packed[i].y);
+            y[4 * i] = p.x, y[4 * i + 1] = p.y, y[4 * i + 2] = q.x, y[4 * i + 3] = q.y;
+          }
+        if (kind != kValue) {
+          if (kind == kQuery ? a.q_gain != nullptr : a.k_gain != nullptr) {
+            float ss = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+            for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
 #pragma unroll
-        for (int d = 1; d < L; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
-        if (row >= r1 || !live) continue;
-        if (!is_v) {
-          const T* gain = static_cast<const T*>(is_q ? a.q_gain : a.k_gain);
-          if (gain) {
-            const float inv = 1.0f / sqrtf(ss / D + a.eps);
-            const uint2 g[2] = {*reinterpret_cast<const uint2*>(gain + lo), *reinterpret_cast<const uint2*>(gain + hi)};
+            for (int d = 1; d < L; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
+            const float inv = rsqrtf(ss * w.inv_width + a.eps);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float2 p = unpack2<T>(g[i].x), q = unpack2<T>(g[i].y);
-              x[4 * i] *= inv * p.x, x[4 * i + 1] *= inv * p.y, x[4 * i + 2] *= inv * q.x, x[4 * i + 3] *= inv * q.y;
+              const float2 p = unpack2<T>(gains[kind][i].x), q = unpack2<T>(gains[kind][i].y);
+              y[4 * i] *= inv * p.x, y[4 * i + 1] *= inv * p.y, y[4 * i + 2] *= inv * q.x, y[4 * i + 3] *= inv * q.y;
             }
           }
           if (turned)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float u = x[i], v = x[4 + i];
-              x[i] = u * c[i] - v * s[i];
-              x[4 + i] = v * c[i] + u * s[i];
+              const float u = y[i], v = y[4 + i];
+              y[i] = u * c[i] - v * s[i];
+              y[4 + i] = v * c[i] + u * s[i];
             }
+          packed[0] = make_uint2(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]));
+          packed[1] = make_uint2(pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
         }
-        const int head = is_q ? row : is_v ? row - a.n_q_heads - a.n_kv_heads : row - a.n_q_heads;
-        T* out = is_q ? static_cast<T*>(a.q_out) + t * a.q_out_stride[0] + head * a.q_out_stride[1]
-                 : is_v || !a.k_out ? nullptr
-                                    : static_cast<T*>(a.k_out) + t * a.k_out_stride[0] + head * a.k_out_stride[1];
-        const long long at = is_v ? v_at : k_at;
-        const bool store = !is_q && at >= 0;
-        const int64_t* ps = is_v ? a.v_page_stride : a.k_page_stride;
-        void* pages = is_v ? a.v_pages : a.k_pages;
-        if (out || (store && !E4M3)) {
-          const uint2 y0 = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-          const uint2 y1 = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-          if (out) {
-            *reinterpret_cast<uint2*>(out + lo) = y0;
-            *reinterpret_cast<uint2*>(out + hi) = y1;
-          }
-          if (store && !E4M3) {
-            T* to = static_cast<T*>(pages) + at + head * ps[1];
-            *reinterpret_cast<uint2*>(to + lo) = y0;
-            *reinterpret_cast<uint2*>(to + hi) = y1;
-          }
+        if (row >= n || !live) continue;
+        if (kind != kValue && out) {
+          T* to = out + t * os[0] + row * os[1];
+          *reinterpret_cast<uint2*>(to + lo) = packed[0];
+          *reinterpret_cast<uint2*>(to + hi) = packed[1];
         }
-        if (E4M3 && store) {
-          const float scale = (is_v ? a.v_scale : a.k_scale)[head];
-          uint8_t* to = static_cast<uint8_t*>(pages) + at + head * ps[1];
-          *reinterpret_cast<uint32_t*>(to + lo) = e4m3x4(x, scale);
-          *reinterpret_cast<uint32_t*>(to + hi) = e4m3x4(x + 4, scale);
+        if (kind == kQuery || at < 0) continue;
+        if (E4M3) {
+          uint8_t* to = static_cast<uint8_t*>(pages) + at + row * ps[1];
+          const float inv = 1.0f / scales[row];
+          *reinterpret_cast<uint32_t*>(to + lo) = e4m3x4(y, inv);
+          *reinterpret_cast<uint32_t*>(to + hi) = e4m3x4(y + 4, inv);
+        } else {
+          T* to = static_cast<T*>(pages) + at + row * ps[1];
+          *reinterpret_cast<uint2*>(to + lo) = packed[0];
+          *reinterpret_cast<uint2*>(to + hi) = packed[1];
         }
       }
+    };
+    for (int r = r0; r < r1; ++r) {
+      if (r < w.q_rounds)
+        round(std::integral_constant<Kind, kQuery>{}, r * H * kBatch, a.n_q_heads, static_cast<const T*>(a.q), a.q_stride,
+              static_cast<T*>(a.q_out), a.q_out_stride, nullptr, -1, nullptr, nullptr);
+      else if (r < w.q_rounds + w.k_rounds)
+        round(std::integral_constant<Kind, kKey>{}, (r - w.q_rounds) * H * kBatch, a.n_kv_heads, static_cast<const T*>(a.k),
+              a.k_stride, static_cast<T*>(a.k_out), a.k_out_stride, a.k_pages, k_at, a.k_page_stride, a.k_scale);
+      else if (v_at >= 0)
+        round(std::integral_constant<Kind, kValue>{}, (r - w.q_rounds - w.k_rounds) * H * kBatch, a.n_kv_heads,
+              static_cast<const T*>(a.v), a.v_stride, static_cast<T*>(nullptr), nullptr, a.v_pages, v_at, a.v_page_stride, a.v_scale);
     }
   }
 }
@@ -210,12 +219,17 @@ extern "C" mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* p, int device, 
   const void* ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out, a.q_gain, a.k_gain, a.k_pages, a.v_pages};
   for (const void* q : ptrs)
     if (!aligned(q, 16)) return refuse(MK_ERR_INVALID_ARG, me, "a pointer is not 16-byte aligned");
-  for (int i = 0; i < 2; ++i)
-    if (a.q_stride[i] % 8 || a.k_stride[i] % 8 || a.q_out_stride[i] % 8 || (cache && a.v_stride[i] % 8) ||
-        (a.k_out && a.k_out_stride[i] % 8))
+  // the stride of a dimension of one element is never used
+  const int tokens_heads[2][2] = {{a.n_tokens, a.n_q_heads}, {a.n_tokens, a.n_kv_heads}};
+  for (int i = 0; i < 2; ++i) {
+    const bool q = tokens_heads[0][i] > 1, k = tokens_heads[1][i] > 1;
+    if ((q && (a.q_stride[i] % 8 || a.q_out_stride[i] % 8)) ||
+        (k && (a.k_stride[i] % 8 || (cache && a.v_stride[i] % 8) || (a.k_out && a.k_out_stride[i] % 8))))
       return refuse(MK_ERR_INVALID_ARG, me, "a stride is not a multiple of 8 elements");
+  }
+  const int page_dims[3] = {a.n_pages, a.n_kv_heads, a.page_size};
   for (int i = 0; cache && i < 3; ++i)
-    if (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8))
+    if (page_dims[i] > 1 && (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8)))
       return refuse(MK_ERR_INVALID_ARG, me, "a cache stride is not a multiple of 16 bytes");
   if (mk_status s = check_device(me, device)) return s;
   DeviceGuard guard(device);
@@ -223,18 +237,20 @@ extern "C" mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* p, int device, 
   int sms;
   if (const cudaError_t e = sm_count(device, &sms)) return launched(me, e);
 
-  const int lanes = a.head_dim <= 64 ? 8 : a.head_dim <= 128 ? 16 : 32, H = 32 / lanes;
-  w.heads = a.n_q_heads + a.n_kv_heads * (cache ? 2 : 1);
-  // Items: enough to give every SM its warps, and beyond that as many heads each as one token has, so that the
+  const int lanes = a.head_dim <= 64 ? 8 : a.head_dim <= 128 ? 16 : 32, heads = 32 / lanes * kBatch;
+  w.q_rounds = (a.n_q_heads + heads - 1) / heads;
+  w.k_rounds = (a.n_kv_heads + heads - 1) / heads;
+  w.rounds = w.q_rounds + w.k_rounds * (cache ? 2 : 1);
+  w.inv_width = 1.0f / a.head_dim;
+  // Items: enough to give every SM its warps, and beyond that as many rounds each as one token has, so that the
   // angles are computed once.
-  const long long room = static_cast<long long>(sms) * 4 * kWarps;
-  const int rounds = (w.heads + H * kBatch - 1) / (H * kBatch);
+  const long long room = static_cast<long long>(sms) * 3 * kWarps;
   long long parts = room / a.n_tokens;
-  parts = parts < 1 ? 1 : parts > rounds ? rounds : parts;
-  w.per_item = static_cast<int>((rounds + parts - 1) / parts) * H * kBatch;
-  w.parts = (w.heads + w.per_item - 1) / w.per_item;
+  parts = parts < 1 ? 1 : parts > w.rounds ? w.rounds : parts;
+  w.per_item = static_cast<int>((w.rounds + parts - 1) / parts);
+  w.parts = (w.rounds + w.per_item - 1) / w.per_item;
   const long long ctas = (static_cast<long long>(a.n_tokens) * w.parts + kWarps - 1) / kWarps;
-  const int grid = static_cast<int>(ctas < sms * 4 ? ctas : sms * 4);
+  const int grid = static_cast<int>(ctas < sms * 3 ? ctas : sms * 3);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return launched(me, a.dtype == MK_BF16 ? launch<__nv_bfloat16>(w, e4m3 && cache, lanes, grid, s)
                                          : launch<__half>(w, e4m3 && cache, lanes, grid, s));

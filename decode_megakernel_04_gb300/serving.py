@@ -72,16 +72,14 @@ def _rows(t, dtype, n, dev, what):
 
 
 def _heads(t, shape, dtype, dev, what):
-    """(address, leading strides) of a tensor of `shape` whose last dimension is contiguous."""
+    """(address, strides without the last) of a tensor of `shape` whose last dimension is contiguous."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{what}: {dtype} {tuple(shape)} on device {dev} is needed, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
-    *lead, one = t.stride()
-    if one != 1:
+    s = t.stride()
+    if s[-1] != 1:
         raise ValueError(f"{what}: the last dimension has to be contiguous")
-    if 1 in shape:  # the stride of a dimension of one element is never used
-        lead = [0 if n == 1 else s for n, s in zip(shape, lead)]
-    return t.data_ptr(), lead
+    return t.data_ptr(), s[:-1]
 
 
 def _call(fn, packed, dev, stream, what):
@@ -163,26 +161,46 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, *, k_out=None, q_gain=None, k
     _call(load().mk_qk_norm_rope, packed, dev, stream, "qk_norm_rope")
 
 
-_workspace_bytes: dict = {}
+def _pack_attention_args(q, k_pages, v_pages, table, lens, out, scale, lse, k_scale, v_scale, dev):
+    """The argument struct's fields before the workspace's address and those after its size."""
+    shape, cache = q.shape, k_pages.shape
+    if len(shape) != 4 or len(cache) != 4:
+        raise ValueError("q is [batch, rows, heads, head_dim] and k_pages [n_pages, kv heads, page size, head_dim]")
+    b, rows, hq, d = shape
+    n_pages, hkv, page, width = cache
+    dt, ct = q.dtype, k_pages.dtype
+    if dt not in _DTYPE or ct not in _DTYPE or width != d:
+        raise ValueError(f"types {dt}, {ct}, widths {d}, {width}")
+    qp, qs = _heads(q, shape, dt, dev, "q")
+    op, os_ = _heads(out, shape, dt, dev, "out")
+    kp, ks = _heads(k_pages, cache, ct, dev, "k_pages")
+    vp, vs = _heads(v_pages, cache, ct, dev, "v_pages")
+    tp, ts, max_pages = _rows(table, _I32, b, dev, "table")
+    ksp = vsp = 0
+    if ct is torch.float8_e4m3fn:
+        ksp, vsp = _vector(k_scale, _F32, hkv, dev, "k_scale"), _vector(v_scale, _F32, hkv, dev, "v_scale")
+    return ((qp, kp, vp, tp, _vector(lens, _I32, b, dev, "lens"), ksp, vsp, op, _vector(lse, _F32, b * rows * hq, dev, "lse")),
+            (ts, *qs, *os_, *ks, *vs, b, rows, hq, hkv, d, n_pages, page, max_pages, _DTYPE[dt], _DTYPE[ct],
+             d ** -0.5 if scale is None else scale))
 
 
-def paged_attention_workspace(q, k_pages) -> int:
-    """Bytes of device scratch paged_attention needs for such q and k_pages (their head counts, types and q's rows
-    decide; the batch, the pages and the lengths do not)."""
+def _workspace_size(packed, dev) -> int:
+    size = C.c_uint64(0)
+    rc = load().mk_paged_attention_workspace(packed, dev, C.byref(size))
+    if rc != MK_OK:
+        raise MKError(rc, "paged_attention (details on stderr)")
+    return size.value
+
+
+def paged_attention_workspace(q, k_pages, table) -> int:
+    """Bytes of device scratch paged_attention needs for q, k_pages and table of these shapes and types (0 for small
+    calls; else the heads, rows and types alone decide)."""
     dev = q.get_device()
-    _, rows, hq, d = q.shape
-    key = (dev, rows, hq, k_pages.shape[1], d, q.dtype, k_pages.dtype)
-    n = _workspace_bytes.get(key)
-    if n is None:
-        _need(q.dtype in _DTYPE and k_pages.dtype in _DTYPE, f"types {q.dtype}, {k_pages.dtype}")
-        a = PagedAttentionArgs(rows=rows, n_q_heads=hq, n_kv_heads=key[3], head_dim=d, dtype=_DTYPE[q.dtype],
-                               cache_dtype=_DTYPE[k_pages.dtype])
-        out = C.c_uint64(0)
-        rc = load().mk_paged_attention_workspace(C.byref(a), dev, C.byref(out))
-        if rc != MK_OK:
-            raise MKError(rc, "paged_attention_workspace (details on stderr)")
-        n = _workspace_bytes[key] = out.value
-    return n
+    _need(dev >= 0, "paged_attention needs CUDA tensors")
+    lens = torch.empty(q.shape[0], dtype=_I32, device=q.device)
+    scale = torch.empty(k_pages.shape[1], dtype=_F32, device=q.device)
+    head, tail = _pack_attention_args(q, k_pages, k_pages, table, lens, q, None, None, scale, scale, dev)
+    return _workspace_size(_pack_attention(*head, 0, 0, 0, *tail), dev)
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, out, *, scale: float | None = None, lse=None, k_scale=None,
@@ -193,36 +211,23 @@ def paged_attention(q, k_pages, v_pages, table, lens, out, *, scale: float | Non
     (with k_scale, v_scale float32 [Hkv]); any strides with D contiguous. table: int32 [B, max_pages]; lens: int32 [B],
     positions in the cache with the R new ones (row r sees lens - (R - 1 - r)). scale: 1 / sqrt(D) by default.
     lse: float32 [B, R, Hq] or None. workspace: a uint8 tensor of paged_attention_workspace bytes that no overlapping
-    call uses; None allocates one for the call from torch's allocator (inside a graph capture: from the graph's pool,
-    so that graphs do not share it)."""
+    call uses; None allocates what the call needs from torch's allocator (inside a graph capture: from the graph's
+    pool, so that graphs do not share it)."""
     dev = q.get_device()
-    _need(dev >= 0 and q.dim() == 4, "paged_attention needs q [batch, rows, heads, head_dim] on a CUDA device")
-    _need(k_pages.dim() == 4, "k_pages is [n_pages, kv heads, page size, head_dim]")
-    shape = q.shape
-    b, rows, hq, d = shape
-    cache = k_pages.shape
-    n_pages, hkv, page, _ = cache
-    dt, ct = q.dtype, k_pages.dtype
-    _need(dt in _DTYPE and ct in _DTYPE and cache[3] == d, f"types {dt}, {ct}, widths {d}, {cache[3]}")
-    qp, qs = _heads(q, shape, dt, dev, "q")
-    op, os_ = _heads(out, shape, dt, dev, "out")
-    kp, ks = _heads(k_pages, cache, ct, dev, "k_pages")
-    vp, vs = _heads(v_pages, cache, ct, dev, "v_pages")
-    tp, ts, max_pages = _rows(table, _I32, b, dev, "table")
-    ksp = vsp = 0
-    if ct is torch.float8_e4m3fn:
-        ksp, vsp = _vector(k_scale, _F32, hkv, dev, "k_scale"), _vector(v_scale, _F32, hkv, dev, "v_scale")
+    if dev < 0:
+        raise ValueError("paged_attention needs CUDA tensors")
+    head, tail = _pack_attention_args(q, k_pages, v_pages, table, lens, out, scale, lse, k_scale, v_scale, dev)
+    st = _vector(status, _I32, 1, dev, "status")
     if workspace is None:
-        size = paged_attention_workspace(q, k_pages)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        if stream is not None and stream != _raw_stream(dev):
-            # torch may hand this memory out again on its own stream while the call still runs on the other
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=q.device))
-    packed = _pack_attention(
-        qp, kp, vp, tp, _vector(lens, _I32, b, dev, "lens"), ksp, vsp, op, _vector(lse, _F32, b * rows * hq, dev, "lse"),
-        _vector(workspace, torch.uint8, None, dev, "workspace"), _vector(status, _I32, 1, dev, "status"),
-        workspace.numel(), ts, *qs, *os_, *ks, *vs, b, rows, hq, hkv, d, n_pages, page, max_pages, _DTYPE[dt],
-        _DTYPE[ct], d ** -0.5 if scale is None else scale)
+        packed = _pack_attention(*head, 0, st, 0, *tail)
+        size = _workspace_size(packed, dev)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            if stream is not None and stream != _raw_stream(dev):
+                # torch may hand this memory out again on its own stream while the call still runs on the other
+                workspace.record_stream(torch.cuda.ExternalStream(stream, device=q.device))
+    if workspace is not None:
+        packed = _pack_attention(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), st, workspace.numel(), *tail)
     _call(load().mk_paged_attention, packed, dev, stream, "paged_attention")
 
 

@@ -511,7 +511,7 @@ mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* args, int device, void* st
  * mk_paged_attention_workspace bytes, 16-byte aligned, with any contents; calls that may overlap need one each.
  * Errors: head_dim not a multiple of 16 in 16..256; n_q_heads not a multiple of n_kv_heads; pointers not
  * 16-byte aligned or strides not multiples of 8 elements (16 for an e4m3 cache); too small a workspace.
- * Two launches (the second joins the splits). */
+ * One launch without a workspace for small calls, else two (the second joins the splits). */
 typedef struct mk_paged_attention_args {
   const void* q;               /* device [batch][rows][n_q_heads][head_dim], dtype                  */
   const void* k_pages;         /* device, cache_dtype                                             */
@@ -535,8 +535,9 @@ typedef struct mk_paged_attention_args {
 } mk_paged_attention_args;
 mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream);
 
-/* Bytes of workspace mk_paged_attention needs for these arguments on `device` (reads the shape fields
- * only: rows, n_q_heads, n_kv_heads, head_dim, dtype, cache_dtype; the batch and the lengths do not matter). */
+/* Bytes of workspace mk_paged_attention needs for these arguments on `device`: 0 for small calls (workspace
+ * may then be NULL), else a size that depends on the heads, rows and types alone, so that the largest of a
+ * program's calls fits all of them. Reads the shape fields only (batch to cache_dtype), no pointer and no length. */
 mk_status mk_paged_attention_workspace(const mk_paged_attention_args* args, int device, uint64_t* bytes);
 
 #define MK_LOGIT_MAX_HISTORY ((1 << 20) - 1)

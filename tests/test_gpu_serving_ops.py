@@ -459,10 +459,15 @@ CASES_ATT = [  # lens, R, hq, hkv, d, page, dtype, cache, layout
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True], ids=["", "wide"])
 @pytest.mark.parametrize("case", CASES_ATT, ids=lambda c: f"{len(c[0])}x{max(c[0])}-" + "-".join(str(x) for x in c[1:]))
-def test_paged_attention(case):
+def test_paged_attention(case, wide):
+    """Each case with a table as wide as its longest request (small calls: clusters) and with one for long requests (the
+    line of tiles cut into pieces, joined by a second launch)."""
+    from decode_megakernel_04_gb300 import paged_attention_workspace
     lens, R, hq, hkv, d, page, dtype, cache, layout = case
-    s = attention_inputs(lens, R, hq, hkv, d, page, dtype, cache, layout=layout)
+    s = attention_inputs(lens, R, hq, hkv, d, page, dtype, cache, layout=layout, max_pages=1 << 20 >> (page.bit_length() - 1) if wide else None)
+    assert not wide or paged_attention_workspace(s["q"], s["k"], s["table"]) > 0
     status = i32([0])
     got, lse = run_attention(s, status=status)
     check_attention(s, got, lse, d ** -0.5)
@@ -523,8 +528,9 @@ def test_attention_lengths_and_pages_out_of_range():
     assert status.item() == 1 and torch.equal(got[[0, 2, 3]], good[[0, 2, 3]]) and got.isfinite().all()
 
 
-def test_attention_repeats_bit_for_bit_and_rows_agree():
-    s = attention_inputs([5000, 1, 800], 1, 12, 2, 128, 16, BF16, BF16, seed=7)
+@pytest.mark.parametrize("width", [None, 50000])
+def test_attention_repeats_bit_for_bit(width):
+    s = attention_inputs([5000, 1, 800], 1, 12, 2, 128, 16, BF16, BF16, seed=7, max_pages=width)
     a, b = run_attention(s), run_attention(s)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     # the same page listed twice is read twice
@@ -551,11 +557,12 @@ def test_attention_offsets_beyond_32_bits():
     check_attention(s, got, lse, d ** -0.5)
 
 
-def test_attention_in_graphs_and_on_streams():
+@pytest.mark.parametrize("width", [None, 50000])
+def test_attention_in_graphs_and_on_streams(width):
     """Two captured graphs without a workspace of their own replay at the same time; each is right after its inputs
     change; and calls on a side stream, by torch's current stream or by the argument."""
     from decode_megakernel_04_gb300 import paged_attention, paged_attention_workspace
-    sets = [attention_inputs([3000 + 500 * i, 40], 1, 8, 1, 128, 16, BF16, BF16, seed=9 + i, poison=False) for i in range(2)]
+    sets = [attention_inputs([3000 + 500 * i, 40], 1, 8, 1, 128, 16, BF16, BF16, seed=9 + i, poison=False, max_pages=width) for i in range(2)]
     outs, graphs = [], []
     for s in sets:
         run_attention(s)  # the first call sets the kernel up
@@ -580,7 +587,7 @@ def test_attention_in_graphs_and_on_streams():
         for (o, l), (wo, wl) in zip(outs, want):
             assert torch.equal(o, wo) and torch.equal(l, wl)
     s = sets[0]
-    ws = torch.empty(paged_attention_workspace(s["q"], s["k"]), dtype=torch.uint8, device=DEV).fill_(255)
+    ws = torch.empty(max(64, paged_attention_workspace(s["q"], s["k"], s["table"])), dtype=torch.uint8, device=DEV).fill_(255)
     for kw in (dict(stream=streams[1].cuda_stream), dict(stream=streams[1].cuda_stream, workspace=ws), dict(workspace=ws), dict(stream=0)):
         got = run_attention(s, **kw)
         assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[0][1])
@@ -599,7 +606,7 @@ def test_attention_refuses():
                    dict(v_pages=s["v"][:-1]), dict(k_pages=s["k"].half()), dict(q=s["q"].transpose(2, 3)), dict(lens=s["lens"].cpu())):
         with pytest.raises(ValueError):
             paged_attention(**{**ok, **change})
-    for change in (dict(q=wide[..., 1:65]), dict(k_pages=s["k"].to(E4M3), v_pages=s["v"].to(E4M3)), dict(workspace=torch.empty(64, dtype=torch.uint8, device=DEV)),
+    for change in (dict(q=wide[..., 1:65]), dict(k_pages=s["k"].to(E4M3), v_pages=s["v"].to(E4M3)), dict(table=s["table"].repeat(1, 20000), workspace=torch.empty(64, dtype=torch.uint8, device=DEV)),
                    dict(q=s["q"].repeat(1, 1, 3, 1)[:, :, :3], out=out[:, :, :3])):
         with pytest.raises(MKError):
             paged_attention(**{**ok, **change})

@@ -75,7 +75,7 @@ REFUSALS = [
         dict(head_dim=8), dict(head_dim=72), dict(head_dim=272), dict(rope_dim=136), dict(rope_dim=12), dict(rope_dim=-8),
         dict(dtype=2), dict(dtype=3), dict(cache_dtype=1), dict(cache_dtype=2), dict(n_pages=1 << 20, page_size=1 << 11)]),
     ("mk_paged_attention", attention, BAD, [
-        dict(q=0), dict(k_pages=0), dict(v_pages=0), dict(table=0), dict(lens=0), dict(out=0), dict(workspace=0),
+        dict(q=0), dict(k_pages=0), dict(v_pages=0), dict(table=0), dict(lens=0), dict(out=0),
         dict(cache_dtype=3), dict(batch=-1), dict(rows=0), dict(n_q_heads=0), dict(n_kv_heads=0), dict(n_kv_heads=3),
         dict(n_pages=0), dict(page_size=0), dict(max_pages=0), dict(table_stride=7), dict(q=P + 8), dict(out=P + 2),
         dict(workspace=P + 4), dict(q_stride=(512, 512, 4)), dict(out_stride=(4, 512, 128)),
