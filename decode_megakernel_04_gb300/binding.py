@@ -103,7 +103,7 @@ class PagedAttentionArgs(C.Structure):
 class LogitControlsArgs(C.Structure):
     _fields_ = [("logits", _P), ("out", _P), ("token", _P), ("history", _P), ("prompt_len", _P), ("total_len", _P),
                 ("repetition", _P), ("presence", _P), ("frequency", _P), ("bias_ids", _P), ("bias_vals", _P),
-                ("allowed", _P), ("logits_stride", _L), ("out_stride", _L), ("history_stride", _L), ("bias_stride", _L),
+                ("allowed", _P), ("workspace", _P), ("workspace_bytes", _L), ("logits_stride", _L), ("out_stride", _L), ("history_stride", _L), ("bias_stride", _L),
                 ("allowed_stride", _L), ("rows", _I), ("vocab", _I), ("max_history", _I), ("n_biases", _I),
                 ("dtype", _I)]
 
@@ -113,7 +113,7 @@ EXPORTS = ["mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host"
            "mk_fork_sequence", "mk_plan", "mk_set_wait_limit",
            "mk_set_routing_override", "mk_decode_steps", "mk_decode_steps_host", "mk_verify_step",
            "mk_packed_weight_bytes", "mk_pack_weights", "mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention",
-           "mk_paged_attention_workspace", "mk_logit_controls"]
+           "mk_paged_attention_workspace", "mk_logit_controls", "mk_logit_controls_workspace"]
 
 _lib = None
 
@@ -159,8 +159,9 @@ def load(path: str | None = None) -> C.CDLL:
     for f in ("mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention", "mk_logit_controls"):
         getattr(lib, f).argtypes = [_P, C.c_int, _P]
         getattr(lib, f).restype = C.c_int
-    lib.mk_paged_attention_workspace.argtypes = [_P, C.c_int, C.POINTER(C.c_uint64)]
-    lib.mk_paged_attention_workspace.restype = C.c_int
+    for f in ("mk_paged_attention_workspace", "mk_logit_controls_workspace"):
+        getattr(lib, f).argtypes = [_P, C.c_int, C.POINTER(C.c_uint64)]
+        getattr(lib, f).restype = C.c_int
     for f in ("mk_packed_weight_bytes", "mk_pack_weights", "mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host", "mk_get_status", "mk_get_info",
               "mk_decode_step_static", "mk_set_routing_log", "mk_fork_sequence", "mk_plan", "mk_set_wait_limit",
               "mk_set_routing_override", "mk_decode_steps", "mk_decode_steps_host", "mk_verify_step"):

@@ -77,6 +77,21 @@ inline mk_status launched(const char* call, cudaError_t e) {
   return e == cudaSuccess ? MK_OK : refuse(MK_ERR_CUDA, call, "%s", cudaGetErrorString(e));
 }
 
+// n / d for 0 <= n < 2^31 by a product: with 2^(k-1) < d <= 2^k, mul = floor(2^(31+k) / d) + 1 is off by at most 1 from
+// 2^(31+k) / d, so n * mul / 2^(31+k) is off by less than 1 / d.
+struct Div {
+  uint32_t mul;
+  int shift;  // k - 1; -1: d = 1
+  __device__ int operator()(int n) const {
+    return shift < 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+  }
+};
+inline Div div_by(int d) {
+  int k = 0;
+  while ((1ll << k) < d) ++k;
+  return {static_cast<uint32_t>((1ull << (31 + k)) / d + 1), k - 1};
+}
+
 __device__ inline void flag(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
 }

@@ -1,26 +1,22 @@
 // mk_page_tables: the page table rows and the slot map of one step from the requests' lengths.
 //
 // Three prefix sums over the requests (new tokens, pages taken, pages returned) place everything; after them each
-// token, each taken page and each returned page is computed on its own. One cluster of up to 8 CTAs runs the whole
-// call: every CTA repeats the sums (a few thousand integers), the CTAs share the tokens, and the one value that is
-// read by all and written by one (the ring's state, lens over held) is written behind a cluster barrier, so the
-// call is one launch that needs no workspace and may update its state in place. Pages are taken from the front of the
-// free run and returned behind its end; with n_free + returned <= ring_size (checked) the two never touch one
-// entry, so they need no order between them.
-#include <cooperative_groups.h>
+// token, each taken page and each returned page is computed on its own, so any number of CTAs share the work and each
+// repeats the sums (a few thousand integers). Pages are taken from the front of the free run and returned behind its
+// end; with n_free + returned <= ring_size (checked) the two never touch one entry, so they need no order between
+// them. What is read by all and may be written in place (the ring's state, lens over the lengths) is the one hazard:
+// a call of one CTA writes it behind a barrier, a larger one in place takes a second launch for it.
+#include <initializer_list>
 
 #include "mk_ops.cuh"
 
 namespace mkop {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBatch = MK_PAGE_TABLES_MAX_BATCH;
 constexpr int kPer = kMaxBatch / kThreads;  // requests per thread
-constexpr int kRun = 8;  // neighbouring tokens of one thread, where there are many
 static_assert(kMaxBatch % kThreads == 0, "whole requests per thread");
 
 struct Sums {
@@ -41,7 +37,9 @@ __device__ inline int owner_of(const int* at, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_constant__ mk_page_tables_args a) {
+// tokens: write slots, pages and ring entries; state: block 0 also writes the ring's state, lens and starts.
+__global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_constant__ mk_page_tables_args a, bool tokens,
+                                                              bool state) {
   extern __shared__ int sm[];
   const int B = a.batch, P = a.page_size;
   int* tok0 = sm;                // [B] first token of each request
@@ -50,9 +48,7 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   int* have = sm + 3 * B;        // [B] pages the row holds before the call
   int* first = sm + 4 * B;       // [B] position of the first new token
   __shared__ Sums warp_sum[kWarps];
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cluster.block_rank(), n_ctas = cluster.num_blocks();
   const int head = a.ring_state[0], n_free = a.ring_state[1];
 
   const int per = (B + kThreads - 1) / kThreads;
@@ -100,15 +96,16 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
     if (n_free + total.returned > a.ring_size) why |= MK_OP_BAD_LENGTH;
   }
 
-  const int step = n_ctas * kThreads, id = rank * kThreads + tid;
+  const int step = gridDim.x * kThreads, id = blockIdx.x * kThreads + tid;
+  state = state && blockIdx.x == 0;
   if (why) {  // the same decision in every CTA
-    for (int t = id; t < a.n_tokens; t += step) {
+    for (int t = id; tokens && t < a.n_tokens; t += step) {
       a.slots[t] = -1;
       if (a.positions) a.positions[t] = 0;
       if (a.owners) a.owners[t] = -1;
     }
-    cluster.sync();
-    if (rank == 0) {
+    __syncthreads();
+    if (state) {
       if (tid == 0) {
         flag(a.status, why);
         a.ring_state_out[0] = head;
@@ -136,92 +133,39 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   const int n_tok = static_cast<int>(total.tokens), n_take = static_cast<int>(total.taken);
   const int n_back = static_cast<int>(total.returned);
   const unsigned size = a.ring_size;
-  const bool whole = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.owners)) & 15) == 0;
-
-  int flags = 0;
-  auto page_of = [&](int b, int k) {
-    const int h = have[b];
-    return k < h ? a.table[b * a.table_stride + k] : a.ring[(static_cast<unsigned>(head) + take0[b] + (k - h)) % size];
-  };
-  auto put = [&](int t, long long slot, int pos, int b) {
-    a.slots[t] = slot;
-    if (a.positions) a.positions[t] = pos;
-    if (a.owners) a.owners[t] = b;
-  };
-  if (a.n_tokens <= kRun * step) {
-    for (int t = id; t < a.n_tokens; t += step) {
+  if (tokens) {
+    int flags = 0;
+    for (unsigned t = id; t < static_cast<unsigned>(a.n_tokens); t += step) {
       long long slot = -1;
       int pos = 0, b = -1;
-      if (t < n_tok) {
+      if (t < static_cast<unsigned>(n_tok)) {
         b = owner_of(tok0, B, t);
-        pos = first[b] + t - tok0[b];
-        const int k = pos / P, page = page_of(b, k);
+        pos = first[b] + (static_cast<int>(t) - tok0[b]);
+        const int k = pos / P, h = have[b];
+        const int page = k < h ? a.table[b * a.table_stride + k]
+                               : a.ring[(static_cast<unsigned>(head) + take0[b] + (k - h)) % size];
         if (page >= 0 && page < a.n_pages) slot = static_cast<long long>(page) * P + (pos - k * P);
         else flags |= MK_OP_BAD_PAGE;
       }
-      put(t, slot, pos, b);
+      a.slots[t] = slot;
+      if (a.positions) a.positions[t] = pos;
+      if (a.owners) a.owners[t] = b;
     }
-  } else {
-    // Many tokens: a thread takes kRun neighbours, which mostly share a request and a page: one search and one or two
-    // page lookups for all of them, and whole 32-byte sectors of each output.
-    for (long long u = id; u * kRun < a.n_tokens; u += step) {
-      const int t0 = static_cast<int>(u) * kRun;
-      int b = -1, end = 0, pos = 0, at = P;  // end: first token of the next request; at: place on the page
-      long long base = -1;
-      long long slot[kRun];
-      int where[kRun], who[kRun];
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const int t = t0 + i;
-        slot[i] = -1, where[i] = 0, who[i] = -1;
-        if (i >= n_tok - t0) continue;
-        ++pos;
-        if (b < 0 || t >= end) {
-          b = owner_of(tok0, B, t);
-          end = b + 1 < B ? tok0[b + 1] : n_tok;
-          pos = first[b] + t - tok0[b];
-          at = P;
-        }
-        if (at >= P) {
-          const int k = pos / P, page = page_of(b, k);
-          at = pos - k * P;
-          const bool ok = page >= 0 && page < a.n_pages;
-          base = ok ? static_cast<long long>(page) * P : -1;
-          if (!ok) flags |= MK_OP_BAD_PAGE;
-        }
-        slot[i] = base < 0 ? -1 : base + at;
-        where[i] = pos, who[i] = b;
-        ++at;
-      }
-      if (whole && a.n_tokens - t0 >= kRun) {
-#pragma unroll
-        for (int i = 0; i < kRun; i += 2) *reinterpret_cast<longlong2*>(a.slots + t0 + i) = make_longlong2(slot[i], slot[i + 1]);
-#pragma unroll
-        for (int i = 0; i < kRun; i += 4) {
-          if (a.positions) *reinterpret_cast<int4*>(a.positions + t0 + i) = make_int4(where[i], where[i + 1], where[i + 2], where[i + 3]);
-          if (a.owners) *reinterpret_cast<int4*>(a.owners + t0 + i) = make_int4(who[i], who[i + 1], who[i + 2], who[i + 3]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          if (i < a.n_tokens - t0) put(t0 + i, slot[i], where[i], who[i]);
-      }
+    for (unsigned j = id; j < static_cast<unsigned>(n_take); j += step) {
+      const int b = owner_of(take0, B, j);
+      a.table[b * a.table_stride + have[b] + (static_cast<int>(j) - take0[b])] = a.ring[(head + j) % size];
     }
+    for (unsigned j = id; j < static_cast<unsigned>(n_back); j += step) {
+      const int b = owner_of(back0, B, j);
+      // the row keeps as many pages as it held less those it returns
+      const int gone = (b + 1 < B ? back0[b + 1] : n_back) - back0[b];
+      a.ring[(static_cast<unsigned>(head) + n_free + j) % size] =
+          a.table[b * a.table_stride + have[b] - gone + (static_cast<int>(j) - back0[b])];
+    }
+    if (flags) flag(a.status, flags);
   }
-  for (int j = id; j < n_take; j += step) {
-    const int b = owner_of(take0, B, j);
-    a.table[b * a.table_stride + have[b] + (j - take0[b])] = a.ring[(static_cast<unsigned>(head) + j) % size];
-  }
-  for (int j = id; j < n_back; j += step) {
-    const int b = owner_of(back0, B, j);
-    // the row keeps as many pages as it held less those it returns
-    const int gone = (b + 1 < B ? back0[b + 1] : n_back) - back0[b];
-    a.ring[(static_cast<unsigned>(head) + n_free + j) % size] =
-        a.table[b * a.table_stride + have[b] - gone + (j - back0[b])];
-  }
-  if (flags) flag(a.status, flags);
-  cluster.sync();  // every CTA has read the lengths and the ring's state
-  if (rank == 0) {
+  __syncthreads();  // this CTA has read the lengths and the ring's state
+  if (state) {
     if (tid == 0) {
       a.ring_state_out[0] = static_cast<int>((static_cast<unsigned>(head) + n_take) % size);
       a.ring_state_out[1] = n_free - n_take + n_back;
@@ -233,6 +177,9 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
     }
   }
 }
+
+// Whether the n elements at p lie (partly) within the m at q.
+bool overlap(const int32_t* p, int n, const int32_t* q, int m) { return p && p < q + m && q < p + n; }
 
 }  // namespace
 }  // namespace mkop
@@ -264,17 +211,24 @@ extern "C" mk_status mk_page_tables(const mk_page_tables_args* p, int device, vo
     const cudaError_t e = allow_smem<page_tables_kernel>(device, static_cast<int>(sizeof(int) * 5 * kMaxBatch));
     if (e != cudaSuccess) return launched(me, e);
   }
-  const int ctas = a.n_tokens <= 4 * kThreads ? 1 : 8;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return launched(me, cudaLaunchKernelEx(&cfg, page_tables_kernel, a));
+  int sms;
+  if (const cudaError_t e = sm_count(device, &sms)) return launched(me, e);
+  // One CTA up to 1024 places (two tokens a thread): a second CTA would gain less than the second launch in place costs.
+  const int want = a.n_tokens <= 2 * kThreads ? 1 : (a.n_tokens + kThreads - 1) / kThreads;
+  const int ctas = want < 2 * sms ? want : 2 * sms;
+  bool in_place = overlap(a.ring_state_out, 2, a.ring_state, 2);
+  for (const int32_t* in : {a.held, a.start, a.count}) {
+    in_place |= overlap(a.lens, a.batch, in, a.batch) || overlap(a.starts, a.batch + 1, in, a.batch) ||
+                overlap(a.ring_state_out, 2, in, a.batch);
+  }
+  in_place |= overlap(a.lens, a.batch, a.ring_state, 2) || overlap(a.starts, a.batch + 1, a.ring_state, 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool split = in_place && ctas > 1;
+  page_tables_kernel<<<ctas, kThreads, smem, s>>>(a, true, !split);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && split) {
+    page_tables_kernel<<<1, kThreads, smem, s>>>(a, false, true);
+    e = cudaGetLastError();
+  }
+  return launched(me, e);
 }

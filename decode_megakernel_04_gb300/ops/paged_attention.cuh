@@ -35,21 +35,6 @@ namespace cg = cooperative_groups;
 constexpr int kMaxCtas = 2048;   // pieces a call is cut into at most
 constexpr int kMinTiles = 2;     // tiles of a piece at least: less is not worth joining
 
-// n / d for 0 <= n < 2^31 by a product: with 2^(k-1) < d <= 2^k, mul = floor(2^(31+k) / d) + 1 is off by at most 1 from
-// 2^(31+k) / d, so n * mul / 2^(31+k) is off by less than 1 / d.
-struct Div {
-  uint32_t mul;
-  int shift;  // k - 1; -1: d = 1
-  __device__ int operator()(int n) const {
-    return shift < 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
-  }
-};
-inline Div div_by(int d) {
-  int k = 0;
-  while ((1ll << k) < d) ++k;
-  return {static_cast<uint32_t>((1ull << (31 + k)) / d + 1), k - 1};
-}
-
 struct Params {
   mk_paged_attention_args a;
   Div page, group_div;
@@ -130,10 +115,10 @@ struct Shape {
   static constexpr int kRowBytes = DP * kElt;         // of a key in shared memory
   static constexpr int kChunks = kRowBytes / 16;
   // 16 to 32 KB of keys and values a tile (64 KB at 256 wide and 16 rows, where four warps take 16 keys each)
-  static constexpr int kTile = E4M3 ? (DP == 64 ? 128 : 64) : (DP == 256 && MT > 1 ? 32 : 64);
+  static constexpr int kTile = E4M3 ? (DP == 64 ? 128 : DP == 128 && MT == 1 ? 128 : 64) : (DP == 256 && MT > 1 ? 32 : 64);
   static constexpr int kWarpKeys = kTile / WK;
   static constexpr int kBlock = kWarpKeys < 32 ? kWarpKeys : 32;  // keys of one softmax step
-  static constexpr int kStages = 3;
+    static constexpr int kStages = MT > 2 && (DP == 256 || E4M3) ? 3 : 2;
   static constexpr int kKeyBytes = kTile * kRowBytes;  // of a tile's keys (as many of values)
   static constexpr int kStageBytes = 2 * kKeyBytes;
   static constexpr int kQBytes = kRows * DP * 2;

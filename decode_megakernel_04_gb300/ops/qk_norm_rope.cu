@@ -18,6 +18,7 @@ namespace mkop {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kCtas = 3;   // on an SM
 constexpr int kBatch = 4;  // rounds of 32 / L heads whose loads are in flight together
 
 __device__ inline uint64_t turns_of(double inv_freq) {
@@ -44,18 +45,17 @@ struct Work {
 };
 
 template <typename T, int L, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32, 3) qk_kernel(const __grid_constant__ Work w) {
-  const mk_qk_norm_rope_args& a = w.a;
+__global__ void __launch_bounds__(kWarps * 32, kCtas) qk_kernel(const __grid_constant__ Work w) {
+    const mk_qk_norm_rope_args& a = w.a;
   constexpr int H = 32 / L;  // heads a warp holds at once
   const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
   const int half = a.rope_dim / 2;
   const bool live = 8 * l < a.head_dim, turned = live && 8 * l < a.rope_dim;
   // where this lane's two groups of 4 elements sit in a head
   const int lo = turned ? 4 * l : 8 * l, hi = turned ? 4 * l + half : 8 * l + 4;
-  uint64_t turns[4] = {0, 0, 0, 0};
-  if (turned)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) turns[i] = turns_of(a.inv_freq[4 * l + i]);
+  __shared__ uint64_t turns[128];
+  for (int i = threadIdx.x; i < half; i += kWarps * 32) turns[i] = turns_of(a.inv_freq[i]);
+  __syncthreads();
   uint2 gains[2][2] = {};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_kernel(const __grid_constan
       const int64_t pos = a.positions[t];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t phase = turns[i] * static_cast<uint64_t>(pos);
+        const uint64_t phase = turns[4 * l + i] * static_cast<uint64_t>(pos);
         const int half_turns = static_cast<int>(phase >> 32);  // units of 2^-31 half turns
         sincospif(static_cast<float>(half_turns) * 4.656612873077392578125e-10f, &s[i], &c[i]);
       }
@@ -89,14 +89,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_kernel(const __grid_constan
         v_at = page * a.v_page_stride[0] + place * a.v_page_stride[2];
       }
     }
-    // One round: kBatch x H heads of one kind, from `first` on. out: q_out or k_out (NULL: none); pages: the cache
-    // (NULL: none), at: the token's place in it.
-    auto round = [&](auto kind_tag, int first, int n, const T* x, const int64_t* xs, T* out, const int64_t* os,
-                     void* pages, long long at, const int64_t* ps, const float* scales) {
-      constexpr Kind kind = decltype(kind_tag)::value;
-      const int row0 = first + sub;
-      x += t * xs[0] + row0 * xs[1];
-      uint2 in[kBatch][2];
+    // A round: kBatch x H heads of one kind. The next round is loaded before the current one is worked on.
+    auto load = [&](int r, uint2 (&in)[kBatch][2]) {
+      const bool is_q = r < w.q_rounds, is_k = !is_q && r < w.q_rounds + w.k_rounds;
+      const int row0 = (is_q ? r : is_k ? r - w.q_rounds : r - w.q_rounds - w.k_rounds) * H * kBatch + sub;
+      const int n = is_q ? a.n_q_heads : !is_k && v_at < 0 ? 0 : a.n_kv_heads;
+      const int64_t* xs = is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride;
+      const T* x = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) + t * xs[0] + row0 * xs[1];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         in[j][0] = in[j][1] = make_uint2(0, 0);
@@ -105,6 +104,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_kernel(const __grid_constan
           in[j][1] = *reinterpret_cast<const uint2*>(x + j * H * xs[1] + hi);
         }
       }
+    };
+    // out: q_out or k_out (NULL: none); pages: the cache, at: the token's place in it (< 0: none)
+    auto turn_and_store = [&](auto kind_tag, int first, int n, const uint2 (&in)[kBatch][2], T* out, const int64_t* os, void* pages,
+                    long long at, const int64_t* ps, const float* scales) {
+      constexpr Kind kind = decltype(kind_tag)::value;
+      const int row0 = first + sub;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int row = row0 + j * H;
@@ -160,16 +165,21 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_kernel(const __grid_constan
         }
       }
     };
+    uint2 in[kBatch][2], next[kBatch][2];
+    load(r0, in);
     for (int r = r0; r < r1; ++r) {
+      if (r + 1 < r1) load(r + 1, next);
       if (r < w.q_rounds)
-        round(std::integral_constant<Kind, kQuery>{}, r * H * kBatch, a.n_q_heads, static_cast<const T*>(a.q), a.q_stride,
-              static_cast<T*>(a.q_out), a.q_out_stride, nullptr, -1, nullptr, nullptr);
+        turn_and_store(std::integral_constant<Kind, kQuery>{}, r * H * kBatch, a.n_q_heads, in, static_cast<T*>(a.q_out), a.q_out_stride,
+             nullptr, -1, nullptr, nullptr);
       else if (r < w.q_rounds + w.k_rounds)
-        round(std::integral_constant<Kind, kKey>{}, (r - w.q_rounds) * H * kBatch, a.n_kv_heads, static_cast<const T*>(a.k),
-              a.k_stride, static_cast<T*>(a.k_out), a.k_out_stride, a.k_pages, k_at, a.k_page_stride, a.k_scale);
+        turn_and_store(std::integral_constant<Kind, kKey>{}, (r - w.q_rounds) * H * kBatch, a.n_kv_heads, in, static_cast<T*>(a.k_out),
+             a.k_out_stride, a.k_pages, k_at, a.k_page_stride, a.k_scale);
       else if (v_at >= 0)
-        round(std::integral_constant<Kind, kValue>{}, (r - w.q_rounds - w.k_rounds) * H * kBatch, a.n_kv_heads,
-              static_cast<const T*>(a.v), a.v_stride, static_cast<T*>(nullptr), nullptr, a.v_pages, v_at, a.v_page_stride, a.v_scale);
+        turn_and_store(std::integral_constant<Kind, kValue>{}, (r - w.q_rounds - w.k_rounds) * H * kBatch, a.n_kv_heads, in,
+             static_cast<T*>(nullptr), nullptr, a.v_pages, v_at, a.v_page_stride, a.v_scale);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) in[j][0] = next[j][0], in[j][1] = next[j][1];
     }
   }
 }
@@ -244,13 +254,13 @@ extern "C" mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* p, int device, 
   w.inv_width = 1.0f / a.head_dim;
   // Items: enough to give every SM its warps, and beyond that as many rounds each as one token has, so that the
   // angles are computed once.
-  const long long room = static_cast<long long>(sms) * 3 * kWarps;
+  const long long room = static_cast<long long>(sms) * kCtas * kWarps;
   long long parts = room / a.n_tokens;
   parts = parts < 1 ? 1 : parts > w.rounds ? w.rounds : parts;
   w.per_item = static_cast<int>((w.rounds + parts - 1) / parts);
   w.parts = (w.rounds + w.per_item - 1) / w.per_item;
   const long long ctas = (static_cast<long long>(a.n_tokens) * w.parts + kWarps - 1) / kWarps;
-  const int grid = static_cast<int>(ctas < sms * 3 ? ctas : sms * 3);
+  const int grid = static_cast<int>(ctas < sms * kCtas ? ctas : sms * kCtas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return launched(me, a.dtype == MK_BF16 ? launch<__nv_bfloat16>(w, e4m3 && cache, lanes, grid, s)
                                          : launch<__half>(w, e4m3 && cache, lanes, grid, s));

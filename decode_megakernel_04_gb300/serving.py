@@ -184,12 +184,21 @@ def _pack_attention_args(q, k_pages, v_pages, table, lens, out, scale, lse, k_sc
              d ** -0.5 if scale is None else scale))
 
 
-def _workspace_size(packed, dev) -> int:
+def _workspace_size(fn, packed, dev, what) -> int:
     size = C.c_uint64(0)
-    rc = load().mk_paged_attention_workspace(packed, dev, C.byref(size))
+    rc = fn(packed, dev, C.byref(size))
     if rc != MK_OK:
-        raise MKError(rc, "paged_attention (details on stderr)")
+        raise MKError(rc, f"{what} (details on stderr)")
     return size.value
+
+
+def _workspace(size, device, dev, stream):
+    """Scratch for one call, from torch's allocator (inside a graph capture: from the graph's pool)."""
+    workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    if stream is not None and stream != _raw_stream(dev):
+        # torch may hand this memory out again on its own stream while the call still runs on the other
+        workspace.record_stream(torch.cuda.ExternalStream(stream, device=device))
+    return workspace
 
 
 def paged_attention_workspace(q, k_pages, table) -> int:
@@ -200,7 +209,8 @@ def paged_attention_workspace(q, k_pages, table) -> int:
     lens = torch.empty(q.shape[0], dtype=_I32, device=q.device)
     scale = torch.empty(k_pages.shape[1], dtype=_F32, device=q.device)
     head, tail = _pack_attention_args(q, k_pages, k_pages, table, lens, q, None, None, scale, scale, dev)
-    return _workspace_size(_pack_attention(*head, 0, 0, 0, *tail), dev)
+    return _workspace_size(load().mk_paged_attention_workspace, _pack_attention(*head, 0, 0, 0, *tail), dev,
+                           "paged_attention_workspace")
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, out, *, scale: float | None = None, lse=None, k_scale=None,
@@ -220,25 +230,24 @@ def paged_attention(q, k_pages, v_pages, table, lens, out, *, scale: float | Non
     st = _vector(status, _I32, 1, dev, "status")
     if workspace is None:
         packed = _pack_attention(*head, 0, st, 0, *tail)
-        size = _workspace_size(packed, dev)
+        size = _workspace_size(load().mk_paged_attention_workspace, packed, dev, "paged_attention")
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-            if stream is not None and stream != _raw_stream(dev):
-                # torch may hand this memory out again on its own stream while the call still runs on the other
-                workspace.record_stream(torch.cuda.ExternalStream(stream, device=q.device))
+            workspace = _workspace(size, q.device, dev, stream)
     if workspace is not None:
         packed = _pack_attention(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), st, workspace.numel(), *tail)
     _call(load().mk_paged_attention, packed, dev, stream, "paged_attention")
 
 
 def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None, repetition=None, presence=None,
-                   frequency=None, bias_ids=None, bias_vals=None, allowed=None, token=None, stream=None) -> None:
+                   frequency=None, bias_ids=None, bias_vals=None, allowed=None, token=None, workspace=None,
+                   stream=None) -> None:
     """mk_logit_controls: penalties, biases and masks on logits, and the greedy token of what is left.
 
     logits: [rows, vocab] fp32, bf16 or fp16, rows contiguous; out: fp32 [rows, vocab] (may be logits). history: int32
     [rows, n] of token ids with prompt_len / total_len int32 [rows]; repetition, presence, frequency: fp32 [rows];
     bias_ids int32 / bias_vals fp32 [rows, m] (pad ids with -1; the last entry of a token counts); allowed: int32
-    [rows, ceil(vocab / 32)] bit mask; token: int32 [rows], -1 where nothing is allowed."""
+    [rows, ceil(vocab / 32)] bit mask; token: int32 [rows], -1 where nothing is allowed. workspace: a uint8 tensor of
+    what mk_logit_controls_workspace says; None allocates what the call needs from torch's allocator."""
     dev = logits.get_device()
     _need(dev >= 0 and logits.dim() == 2, "logit_controls needs logits [rows, vocab] on a CUDA device")
     n, vocab = logits.shape
@@ -253,9 +262,15 @@ def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None
     _need(nb == nbv and bs == bvs, "bias_ids and bias_vals have one layout")
     ap, as_, words = _rows(allowed, _I32, n, dev, "allowed")
     _need(allowed is None or words >= (vocab + 31) // 32, "allowed holds a bit for each token")
-    packed = _pack_logits(
-        lp, op, _vector(token, _I32, n, dev, "token"), hp, _vector(prompt_len, _I32, n, dev, "prompt_len"),
-        _vector(total_len, _I32, n, dev, "total_len"), _vector(repetition, _F32, n, dev, "repetition"),
-        _vector(presence, _F32, n, dev, "presence"), _vector(frequency, _F32, n, dev, "frequency"), bp, bvp, ap, ls, os_,
-        hs, bs, as_, n, vocab, hist, nb, _DTYPE[dt])
+    head = (lp, op, _vector(token, _I32, n, dev, "token"), hp, _vector(prompt_len, _I32, n, dev, "prompt_len"),
+            _vector(total_len, _I32, n, dev, "total_len"), _vector(repetition, _F32, n, dev, "repetition"),
+            _vector(presence, _F32, n, dev, "presence"), _vector(frequency, _F32, n, dev, "frequency"), bp, bvp, ap)
+    tail = (ls, os_, hs, bs, as_, n, vocab, hist, nb, _DTYPE[dt])
+    if workspace is None:
+        packed = _pack_logits(*head, 0, 0, *tail)
+        size = _workspace_size(load().mk_logit_controls_workspace, packed, dev, "logit_controls")
+        if size:
+            workspace = _workspace(size, logits.device, dev, stream)
+    if workspace is not None:
+        packed = _pack_logits(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), workspace.numel(), *tail)
     _call(load().mk_logit_controls, packed, dev, stream, "logit_controls")

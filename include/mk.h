@@ -438,7 +438,8 @@ typedef enum mk_op_flag {
  * When a length is bad, pages run out or the tokens do not fit n_tokens places, nothing changes: table and
  * ring stay, ring_state_out and lens repeat ring_state and held, every place gets slot -1, starts are 0.
  * A page id in the table or ring outside 0 .. n_pages - 1 gives slot -1 (MK_OP_BAD_PAGE).
- * One launch. Integer arithmetic only: the result does not depend on timing. */
+ * One launch; two for more than 1024 places with an output over an input it is computed from. Integer
+ * arithmetic only: the result does not depend on timing. */
 typedef struct mk_page_tables_args {
   int32_t* table;              /* device [batch][table_stride], max_pages used per row              */
   int64_t table_stride;
@@ -554,7 +555,9 @@ mk_status mk_paged_attention_workspace(const mk_paged_attention_args* args, int 
  * that is not NaN, -1 when none is above -infinity. Every step is rounded as written (no fused
  * multiply-add). Ids outside 0 .. vocab - 1 in history and bias_ids are passed over (pad with -1);
  * total_len counts as within 0 .. max_history, prompt_len as within 0 .. total_len.
- * mk_decode_step's logits_out is such an input, with batch * rows rows. One launch. */
+ * mk_decode_step's logits_out is such an input, with batch * rows rows. `workspace` is device scratch, 8-byte
+ * aligned, with any contents; calls that may overlap need one each. One launch without a workspace for few
+ * rows, else two. */
 typedef struct mk_logit_controls_args {
   const void* logits;          /* device [rows][logits_stride], dtype                              */
   float* out;                  /* device [rows][out_stride]                                       */
@@ -568,11 +571,17 @@ typedef struct mk_logit_controls_args {
   const int32_t* bias_ids;     /* device [rows][bias_stride], n_biases used, or NULL                 */
   const float* bias_vals;      /* the same layout                                                 */
   const int32_t* allowed;      /* device [rows][allowed_stride], (vocab + 31) / 32 words, or NULL      */
+  void* workspace;             /* device, mk_logit_controls_workspace bytes                        */
+  int64_t workspace_bytes;
   int64_t logits_stride, out_stride, history_stride, bias_stride, allowed_stride;
   int32_t rows, vocab, max_history, n_biases; /* max_history <= MK_LOGIT_MAX_HISTORY, n_biases <= MK_LOGIT_MAX_BIASES */
   int32_t dtype;               /* MK_F32, MK_BF16 or MK_F16                                        */
 } mk_logit_controls_args;
 mk_status mk_logit_controls(const mk_logit_controls_args* args, int device, void* stream);
+
+/* Bytes of workspace mk_logit_controls needs for these arguments on `device` (0 for few rows: workspace may then be
+ * NULL). Which pointers are NULL and the sizes decide; nothing is read through a pointer. */
+mk_status mk_logit_controls_workspace(const mk_logit_controls_args* args, int device, uint64_t* bytes);
 
 #ifdef __cplusplus
 }

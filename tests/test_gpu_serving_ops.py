@@ -697,9 +697,25 @@ def check_controls(z, kw, in_place=False, **call):
         assert (wide[:, 0] == 7).all() and (wide[:, vocab + 1:] == 7).all()
 
 
+def many(z, kw, times=24):
+    """The rows over again (more than a cluster per row is used for), each copy with its own penalties."""
+    z = z.repeat(times, 1)
+    kw = {k: v.repeat(times, *[1] * (v.dim() - 1)) for k, v in kw.items()}
+    for k in ("repetition", "presence", "frequency"):
+        if k in kw:
+            kw[k] = kw[k] * torch.linspace(0.5, 1.5, kw[k].numel(), device=DEV)
+    return z, kw
+
+
+@pytest.mark.parametrize("rows", ["few", "many"])
 @pytest.mark.parametrize("case", CASES_LOGITS, ids=str)
-def test_logit_controls(case):
+def test_logit_controls(case, rows):
+    """Few rows: clusters. Many: the plain pass and the second kernel (a history of over 12 thousand tokens: clusters)."""
     z, kw = logit_inputs(*case)
+    if rows == "many":
+        if z.shape[0] >= 20 or z.shape[1] > 200000:
+            pytest.skip("the same form as few, or long")
+        z, kw = many(z, kw)
     check_controls(z, kw)
     if case[4] is F32:
         check_controls(z, kw, in_place=True)
@@ -710,6 +726,7 @@ def test_logit_controls(case):
 def test_logit_controls_each_alone(keep):
     z, kw = logit_inputs(3, 2050, 90, 12, F32, True, 0, seed=4)
     check_controls(z, {k: kw[k] for k in keep})
+    check_controls(*many(z, {k: kw[k] for k in keep}))
 
 
 def test_logit_controls_special_values():
@@ -722,11 +739,32 @@ def test_logit_controls_special_values():
     z[4] = float("nan")
     z[5] = torch.finfo(F32).min
     check_controls(z, {})
+    check_controls(*many(z, {}))
     allowed = torch.zeros(6, -(-V // 32), dtype=torch.int32, device=DEV)   # row 0..4: nothing is allowed
     allowed[5, 100] = 1 << 5
     check_controls(z, dict(allowed=allowed))
+    check_controls(*many(z, dict(allowed=allowed)))
     allowed[1] = -1
     check_controls(z, dict(allowed=allowed))
+    check_controls(*many(z, dict(allowed=allowed)))
+    # every token of the row is in the history, and every token but one
+    z = torch.randn(2, 300, generator=gen(3), device=DEV)
+    kw = dict(history=torch.arange(300, device=DEV).to(torch.int32).repeat(2, 1), total_len=i32([300, 299]), repetition=torch.tensor([2.0, 0.5], device=DEV))
+    check_controls(z, kw)
+    check_controls(*many(z, kw))
+
+
+def test_logit_controls_largest_logits_are_in_the_history():
+    """The chunks' largest logits are mostly named tokens, so that the join has to look for others."""
+    n, V = 30, 20011
+    z = torch.randn(n, V, generator=gen(5), device=DEV)
+    top = z.topk(200, dim=1).indices.to(torch.int32)
+    for pen in (1.0, 1.02, 5.0):
+        kw = dict(history=top, total_len=i32([7 * i for i in range(n)]), frequency=torch.full((n,), pen, device=DEV))
+        check_controls(z, kw)
+        check_controls(z.clone(), kw, in_place=True)
+        kw["allowed"] = torch.randint(-2 ** 31, 2 ** 31 - 1, (n, -(-V // 32)), generator=gen(6), device=DEV).to(torch.int32)
+        check_controls(z, kw)
 
 
 def test_logit_controls_ties_take_the_lowest_index_of_the_whole_row():
@@ -736,6 +774,21 @@ def test_logit_controls_ties_take_the_lowest_index_of_the_whole_row():
         z[1, 3:] = 1.0
         z[2, :] = 5.0
         check_controls(z, {})
+        check_controls(*many(z, {}))
+
+
+def test_logit_controls_empty_lists():
+    """A history of length 0 with penalties, biases of width 0, and a history longer than one pass of slices holds."""
+    z, kw = logit_inputs(2, 777, 5, 3, F32, True, 0, seed=6)
+    kw["history"], kw["total_len"], kw["prompt_len"] = kw["history"][:, :0], None, None
+    check_controls(z, {k: v for k, v in kw.items() if v is not None and not k.startswith("bias")})
+    kw["bias_ids"], kw["bias_vals"] = kw["bias_ids"][:, :0], kw["bias_vals"][:, :0]
+    check_controls(z, {k: v for k, v in kw.items() if v is not None})
+    check_controls(*many(z, {k: v for k, v in kw.items() if v is not None}))
+    z, kw = logit_inputs(2, 300007, 60000, 3, BF16, True, 0, seed=7)
+    kw["history"] = torch.randint(0, 300007, (2, 60000), generator=gen(8), device=DEV).to(torch.int32)
+    check_controls(z, kw)
+    check_controls(*many(z[:, :3000], {**kw, "allowed": kw["allowed"][:, :94]}, times=12))
 
 
 def test_logit_controls_one_token_repeated():
@@ -744,12 +797,15 @@ def test_logit_controls_one_token_repeated():
     kw = dict(history=torch.full((2, n), 17, dtype=torch.int32, device=DEV), total_len=i32([n, n]), prompt_len=i32([0, n - 3]),
               frequency=torch.tensor([0.5, 2.0], device=DEV), repetition=torch.tensor([2.0, 4.0], device=DEV))
     check_controls(z, kw)
+    kw["history"], kw["total_len"], kw["prompt_len"] = kw["history"][:, :9000], i32([9000, 9000]), i32([0, 8998])
+    check_controls(*many(z, kw))
 
 
-def test_logit_controls_captured():
+@pytest.mark.parametrize("n", [3, 40])
+def test_logit_controls_captured(n):
     from decode_megakernel_04_gb300 import logit_controls
-    z, kw = logit_inputs(3, 30011, 200, 9, F32, True, 0)
-    out, tok = torch.empty_like(z), i32([0, 0, 0])
+    z, kw = logit_inputs(n, 30011, 200, 9, F32, True, 0)
+    out, tok = torch.empty_like(z), i32([0] * n)
     logit_controls(z, out, token=tok, **kw)
     gr = torch.cuda.CUDAGraph()
     with torch.cuda.graph(gr):
