@@ -1,6 +1,6 @@
 // mk_paged_attention: arguments, the choice of a build, and the second kernel, which joins the parts of requests that
 // were cut (paged_attention.cuh has the attention kernel).
-#include "paged_attention.cuh"
+#include "paged_attention_tc.cuh"
 
 namespace mkop {
 namespace attn {
@@ -9,8 +9,8 @@ namespace {
 constexpr int kJoinWarps = 8;
 
 // Block (x, y): the request cut at the beginning of piece x + 1, if that is the first cut in it; rows y, y + gridDim.y, ...
-// A row's parts are weighted by exp2(maximum - largest maximum); the warps take the parts in turn and are summed in a
-// fixed order. Launched so that it may start while the attention kernel runs; it waits for that kernel's end before
+// A row's parts are weighted by exp2(maximum - largest maximum). Up to 16 parts: a warp has a row; more: the warps take
+// the parts of one row in turn and are summed in a fixed order. Launched so that it may start while the attention kernel runs; it waits for that kernel's end before
 // it reads anything.
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p, int dp, int rows_of_block,
@@ -33,6 +33,39 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   auto slot = [&](int k) { return k == 0 ? slot0 : 2ll * (c - 1 + k); };
   const int head = pc.hm / p.blocks, block = pc.hm - head * p.blocks;
   const int rows = min(rows_of_block, p.n_rows - block * rows_of_block);
+  if (n <= 16) {
+    for (int row = blockIdx.y * kJoinWarps + warp; row < rows; row += gridDim.y * kJoinWarps) {
+      const float2 mine = lane < n ? p.part_ml[slot(lane) * rows_of_block + row] : make_float2(-INFINITY, 0.0f);
+      float top = mine.x;
+#pragma unroll
+      for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      top = __shfl_sync(~0u, top, 0);
+      const float f = exp2_fast(mine.x - (top == -INFINITY ? 0.0f : top));
+      float sum = f * mine.y;
+#pragma unroll
+      for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      sum = __shfl_sync(~0u, sum, 0);
+      const int mrow = block * rows_of_block + row, r = p.group_div(mrow), h = head * p.group + mrow - r * p.group;
+      const float scale = sum == 0.0f ? 0.0f : (scaled ? a.v_scale[head] : 1.0f) / sum;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + pc.b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2];
+      for (int d0 = 0; d0 < dp; d0 += 128) {
+        const int d = min(d0 + lane * 4, dp - 4);  // (64 wide: half of the lanes repeat the last columns)
+        float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(p.part + (slot(k) * rows_of_block + row) * dp + d);
+          const float g = __shfl_sync(~0u, f, k);
+          y.x += g * x.x, y.y += g * x.y, y.z += g * x.z, y.w += g * x.w;
+        }
+        if (d < a.head_dim)
+          *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(y.x * scale, y.y * scale), pack2<T>(y.z * scale, y.w * scale));
+      }
+      if (lane == 0 && a.lse)
+        a.lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] =
+            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+    }
+    return;
+  }
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     float top = -INFINITY;
     for (int k = tid; k < n; k += kJoinWarps * 32) top = fmaxf(top, p.part_ml[slot(k) * rows_of_block + row].x);
@@ -138,6 +171,12 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
     pl.parts = parts;
     pl.ctas = static_cast<int>(items) * parts;
     return cudaSuccess;
+  }
+  if (a.cache_dtype != MK_E4M3 && (a.head_dim == 128 || a.head_dim == 256) && a.rows <= kTcMaxRows) {
+    const int block_rows = pl.blocks == 1 ? pl.n_rows : 16 * mt;
+    pl.build = a.dtype == MK_BF16 ? pick_tc_bf16(pl.dp, block_rows) : pick_tc_f16(pl.dp, block_rows);
+    if ((e = pl.build->occupancy(device, &per_sm)) != cudaSuccess) return e;
+    pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
   }
   const size_t slots = 2 * static_cast<size_t>(pl.ctas);
   pl.ml_at = slots * pl.build->rows * pl.dp * sizeof(float);

@@ -17,7 +17,7 @@ import torch
 
 from .binding import (MK_OK, LogitControlsArgs, MKError, PagedAttentionArgs, PageTablesArgs, QkNormRopeArgs, load)
 
-OP_BAD_PAGE, OP_BAD_LENGTH, OP_NO_PAGES, OP_NO_ROOM = 1, 2, 4, 8
+OP_BAD_PAGE, OP_BAD_LENGTH, OP_NO_PAGES, OP_NO_ROOM, OP_TIMEOUT = 1, 2, 4, 8, 16
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 _I32, _I64, _F32, _F64 = torch.int32, torch.int64, torch.float32, torch.float64

@@ -418,7 +418,8 @@ typedef enum mk_op_flag {
   MK_OP_BAD_PAGE = 1,   /* a page id or slot outside the cache                                     */
   MK_OP_BAD_LENGTH = 2, /* a length that is negative, inconsistent or beyond the table             */
   MK_OP_NO_PAGES = 4,   /* mk_page_tables: the ring holds fewer free pages than the step needs      */
-  MK_OP_NO_ROOM = 8     /* mk_page_tables: more new tokens than the slot map has places             */
+  MK_OP_NO_ROOM = 8,    /* mk_page_tables: more new tokens than the slot map has places             */
+  MK_OP_TIMEOUT = 16    /* mk_paged_attention: a wait inside a CTA passed 2 s (a fault of the library) */
 } mk_op_flag;
 
 #define MK_PAGE_TABLES_MAX_BATCH 4096
