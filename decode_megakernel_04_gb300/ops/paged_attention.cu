@@ -172,7 +172,9 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
     pl.ctas = static_cast<int>(items) * parts;
     return cudaSuccess;
   }
-  if (a.cache_dtype != MK_E4M3 && (a.head_dim == 128 || a.head_dim == 256) && a.rows <= kTcMaxRows) {
+  // (its CTAs count their tiles in 32 bits)
+  if (items * ((static_cast<int64_t>(a.max_pages) * a.page_size >> 7) + 1) < INT32_MAX &&
+      a.cache_dtype != MK_E4M3 && (a.head_dim == 128 || a.head_dim == 256) && a.rows <= kTcMaxRows) {
     const int block_rows = pl.blocks == 1 ? pl.n_rows : 16 * mt;
     pl.build = a.dtype == MK_BF16 ? pick_tc_bf16(pl.dp, block_rows) : pick_tc_f16(pl.dp, block_rows);
     if ((e = pl.build->occupancy(device, &per_sm)) != cudaSuccess) return e;
@@ -255,6 +257,14 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
   if (pl.bytes && (!a.workspace || a.workspace_bytes < static_cast<int64_t>(pl.bytes)))
     return refuse(MK_ERR_INVALID_ARG, kMe, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), pl.bytes);
   char* ws = static_cast<char*>(a.workspace);
+  for (int i = 0; i < 3; ++i) {
+    const int64_t k = page_dims[i] > 1 ? a.k_page_stride[i] * (e4m3 ? 1 : 2) / 16 : 0;
+    const int64_t v = page_dims[i] > 1 ? a.v_page_stride[i] * (e4m3 ? 1 : 2) / 16 : 0;
+    if (k < 0 || k > UINT32_MAX || v < 0 || v > UINT32_MAX)
+      return refuse(MK_ERR_UNSUPPORTED, kMe, "a cache stride is negative or 64 GB and more");
+    p.k_step[i] = static_cast<uint32_t>(k);
+    p.v_step[i] = static_cast<uint32_t>(v);
+  }
   p.page = div_by(a.page_size);
   p.group_div = div_by(pl.group);
   p.group = pl.group;

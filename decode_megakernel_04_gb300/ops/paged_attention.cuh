@@ -45,6 +45,7 @@ struct Params {
   int ctas;         // grid of the attention kernel
   int parts;        // > 0: clusters of `parts` CTAs share a (request, kv head, row block); 0: pieces of the line
   float scale_log2; // scale * log2(e)
+  uint32_t k_step[3], v_step[3];  // the caches' strides (page, head, place) in units of 16 bytes
   float* part;      // [2 ctas][16 MT][DP] sums of a part
   float2* part_ml;  // [2 ctas][16 MT] its maximum (log2 units) and sum
   struct Piece* piece;  // [ctas]
@@ -61,12 +62,27 @@ struct Piece {
 
 __host__ __device__ inline long long piece_begin(long long c, long long total, int used) { return c * total / used; }
 
+// Rows that are not there (behind a request's length, of a page that does not exist, columns that pad a head) are copied
+// from here: an address instead of a size that every copy would have to select.
+static __device__ __align__(16) const unsigned char kZeros[512] = {};
+
+// Where key or value `place` of a page and head begins.
+__device__ inline const unsigned char* row_at(const void* cache, const uint32_t (&step)[3], int page, int head, int place) {
+  const uint64_t units = static_cast<uint64_t>(static_cast<uint32_t>(page)) * step[0] +
+                         static_cast<uint64_t>(static_cast<uint32_t>(head)) * step[1] +
+                         static_cast<uint64_t>(static_cast<uint32_t>(place)) * step[2];
+  return static_cast<const unsigned char*>(cache) + units * 16;
+}
+
 // ---- PTX ----------------------------------------------------------------------------------------------------------
 __device__ inline uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes, zeros when !valid (nothing is read then)
 __device__ inline void cp16(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ inline void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -127,7 +143,7 @@ struct Shape {
   static constexpr int kJoin = kStageBytes >= WK * kRows * 64 * 4 ? 64 : 32;
   static constexpr int kOffKV = 0;
   static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kOffAddr = kOffQ + kStages * kQBytes;           // int64 [kRing][2][kTile]
+  static constexpr int kOffAddr = kOffQ + kStages * kQBytes;           // address [kRing][2][kTile]
   static constexpr int kOffMeta = kOffAddr + kRing * 2 * kTile * 8;    // Tile [kRing]
   static constexpr int kOffMl = kOffMeta + kRing * 48;                 // float2 [WK][kRows]
   static constexpr int kSmem = kOffMl + WK * kRows * 8;
@@ -169,7 +185,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads, Shape<DP, MT, E
   const int wm = warp % S::WM, wk = warp / S::WM;
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t s0 = smem_u32(smem);
-  long long* addr = reinterpret_cast<long long*>(smem + S::kOffAddr);
+  const unsigned char** addr = reinterpret_cast<const unsigned char**>(smem + S::kOffAddr);
   Tile* meta = reinterpret_cast<Tile*>(smem + S::kOffMeta);
   float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
   __shared__ long long warp_tiles[S::kWarps];
@@ -267,11 +283,11 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads, Shape<DP, MT, E
   auto describe = [&](int page, int ring) {
     if (c_done >= count) return;
     if (tid < S::kTile) {
-      long long k = -1, v = -1;
+      const unsigned char *k = kZeros, *v = kZeros;
       if (page >= 0) {
         const int key = c_tile * S::kTile + tid, at = key - p.page(key) * a.page_size;
-        k = (page * a.k_page_stride[0] + c_head * a.k_page_stride[1] + at * a.k_page_stride[2]) * S::kElt;
-        v = (page * a.v_page_stride[0] + c_head * a.v_page_stride[1] + at * a.v_page_stride[2]) * S::kElt;
+        k = row_at(a.k_pages, p.k_step, page, c_head, at);
+        v = row_at(a.v_pages, p.v_step, page, c_head, at);
       } else if (page == -2) {
         flag(a.status, MK_OP_BAD_PAGE);
       }
@@ -314,15 +330,13 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads, Shape<DP, MT, E
     if (kLoaders == S::kThreads || tid < kLoaders) {
       const int chunk = tid % S::kChunks, row0 = tid / S::kChunks;
       const bool in = chunk * 16 < a.head_dim * S::kElt;
-      const long long* at = addr + (ring * 2) * S::kTile + row0;
-      const unsigned char* kp = static_cast<const unsigned char*>(a.k_pages) + (in ? chunk * 16 : 0);
-      const unsigned char* vp = static_cast<const unsigned char*>(a.v_pages) + (in ? chunk * 16 : 0);
+      const unsigned char* const* at = addr + (ring * 2) * S::kTile + row0;
 #pragma unroll 8
       for (int i = 0; i < S::kTile / kLoadRows; ++i) {
         const uint32_t to = place<S::kChunks>(row0 + i * kLoadRows, chunk);
-        const long long k = at[i * kLoadRows], v = at[S::kTile + i * kLoadRows];
-        cp16(kd + to, kp + max(k, 0ll), in && k >= 0);
-        cp16(vd + to, vp + max(v, 0ll), in && v >= 0);
+        const unsigned char *k = at[i * kLoadRows], *v = at[S::kTile + i * kLoadRows];
+        cp16(kd + to, in ? k + chunk * 16 : kZeros);
+        cp16(vd + to, in ? v + chunk * 16 : kZeros);
       }
     }
     if (m.first) {

@@ -223,7 +223,7 @@ struct TcShape {
   static constexpr int kOffQ = kOffP + 2 * kP;
   static constexpr int kOffTail = kOffQ + kQs * kQ;    // float [16][64]: scores of keys not all rows see
   static constexpr int kOffStat = kOffTail + 16 * 64 * 4;
-  static constexpr int kOffAddr = kOffStat + 16 * 64 * 4;  // int64 [2][2][128]
+  static constexpr int kOffAddr = kOffStat + 16 * 64 * 4;  // address [2][2][128]
   static constexpr int kOffBar = kOffAddr + 2 * 2 * 128 * 8;
   static constexpr int kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -242,11 +242,10 @@ struct Walk {
   const mk_paged_attention_args& a;
   const Params& p;
   int b, head, block, tile, n, len, next_len, first_tile;
-  long long done, count;
-  int items;
+  int done, count, items;
   __device__ int length(int i) const { return min(max(a.lens[i], 0), p.max_len); }
   __device__ static int tiles_of(int len) { return max(1, (len + 127) >> 7); }
-  __device__ Walk(const Params& pp, int b0, long long rem, long long cnt) : a(pp.a), p(pp) {
+  __device__ Walk(const Params& pp, int b0, long long rem, int cnt) : a(pp.a), p(pp) {
     b = b0;
     len = length(b);
     n = tiles_of(len);
@@ -300,7 +299,8 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
 
   // ---- this CTA's piece of the line (as in attention_kernel) --------------------------------------------------------
   const int hm_n = a.n_kv_heads * p.blocks;
-  long long total, count;
+  long long total;
+  int count;
   {
     auto length = [&](int b) { return min(max(a.lens[b], 0), p.max_len); };
     const int per = (a.batch + S::kThreads - 1) / S::kThreads;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
       if (tid == 0) p.piece[blockIdx.x].used = used;
       return;
     }
-    count = piece_begin(blockIdx.x + 1, total, used) - begin;
+    count = static_cast<int>(piece_begin(blockIdx.x + 1, total, used) - begin);
     if (tid == 0) {
       const Walk w(p, at_b, at_rem, count);
       Piece& pc = p.piece[blockIdx.x];
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
   __syncthreads();
   tc_after();
   const uint32_t tmem = bars.tmem;
-  auto scores_at = [&](long long j) { return tmem + static_cast<uint32_t>(j & 1) * 64; };
+  auto scores_at = [&](int j) { return tmem + static_cast<uint32_t>(j & 1) * 64; };
   auto sums_at = [&](int h) { return tmem + 128 + h * 128; };
   Walk w(p, at_b, at_rem, count);
 
@@ -382,26 +382,25 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
     // ---- loaders --------------------------------------------------------------------------------------------------
     const bool value = warp >= 12;  // warps 9-11 load keys (and query rows), 12-14 values
     const int t = tid - (value ? 384 : 288), barrier = value ? 3 : 2;
-    long long* addr = reinterpret_cast<long long*>(smem + S::kOffAddr) + (value ? 256 : 0);  // [2 tiles][128]
-    const int64_t* stride = value ? a.v_page_stride : a.k_page_stride;
-    const unsigned char* pages = static_cast<const unsigned char*>(value ? a.v_pages : a.k_pages);
+    const unsigned char** addr = reinterpret_cast<const unsigned char**>(smem + S::kOffAddr) + (value ? 256 : 0);  // [2 tiles][128]
     // The pages of this thread's keys (t, and t + 96 where that is one of the tile's) are loaded a tile before their
     // addresses are made, and these a tile before the copies.
     auto look_up = [&](int key) -> int {
       key += w.tile * 128;
       return w.done < count && key < w.len ? a.table[w.b * a.table_stride + p.page(key)] : -1;
     };
-    auto make_address = [&](long long* at, int page, int i) {  // of tile w's key i
-      long long to = -1;
+    auto make_address = [&](const unsigned char** at, int page, int i) {  // of tile w's key i
+      const unsigned char* from = kZeros;
       const int key = w.tile * 128 + i;
       if (w.done < count && key < w.len) {
         if (page < 0 || page >= a.n_pages)
           flag(a.status, MK_OP_BAD_PAGE);
         else if (!value || a.rows == 1 || key < w.all_see())
           // (values that not all rows see are left out of the product: see the softmax's end of a part)
-          to = (page * stride[0] + w.head * stride[1] + (key - p.page(key) * a.page_size) * stride[2]) * 2;
+          from = value ? row_at(a.v_pages, p.v_step, page, w.head, key - p.page(key) * a.page_size)
+                       : row_at(a.k_pages, p.k_step, page, w.head, key - p.page(key) * a.page_size);
       }
-      at[i] = to;
+      at[i] = from;
     };
     const bool two = t < 128 - S::kLoaders;
     struct Item {  // what the copies of a tile need besides addresses
@@ -416,8 +415,8 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
     Item now = item_of();
     w.next();
     int page = look_up(t), page2 = two ? look_up(t + S::kLoaders) : -1;  // of tile w, one ahead of `now`
-    for (long long j = 0; j < count; ++j) {
-      long long* at = addr + (j & 1) * 128;
+    for (int j = 0; j < count; ++j) {
+      const unsigned char** at = addr + (j & 1) * 128;
       if (any_of(barrier, S::kLoaders, !ok)) break;
       if (!value && now.first) {
         const int q = now.items % S::kQs;
@@ -441,14 +440,13 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
         if (turn) wait_free(&bars.empty[slot], (turn - 1) & 1);
         const int chunk = t & 15, row0 = t >> 4;
         const uint32_t to = s0 + slot * S::kSlot + (chunk >> 3) * 16384;
-        const long long* off = at + row0;
-        const unsigned char* from = pages + h * 256 + chunk * 16;
+        const unsigned char* const* from = at + row0;
+        const int column = h * 256 + chunk * 16;
 #pragma unroll
         for (int i = 0; i < (128 * 16 + S::kLoaders - 1) / S::kLoaders; ++i) {
           const int row = row0 + S::kLoaders / 16 * i;
           if (row >= 128) break;
-          const long long o = off[S::kLoaders / 16 * i];
-          cp16(to + row * 128 + (((chunk ^ row) & 7) << 4), from + max(o, 0ll), o >= 0);
+          cp16(to + row * 128 + (((chunk ^ row) & 7) << 4), from[S::kLoaders / 16 * i] + column);
         }
         cp_arrive(&bars.full[slot]);
         if (h == 0) {  // the next tile's addresses, while copies are in flight
@@ -467,7 +465,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
     if (lane == 0) {
       constexpr uint32_t kScores = tc_idesc<T>(N, false), kSums = tc_idesc<T>(S::kPairs, true);
       bool ok = true;
-      auto scores = [&](long long j) {
+      auto scores = [&](int j) {
         const int q = w.items % S::kQs;
         if (w.first()) ok = ok && bar_wait(&bars.q_full[q], (w.items / S::kQs) & 1, dead);
         if (j >= 2) ok = ok && bar_wait(&bars.s_empty[j & 1], static_cast<uint32_t>((j >> 1) - 1) & 1, dead);
@@ -491,7 +489,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
         tc_commit(&bars.s_full[j & 1]);
       };
       scores(0);
-      for (long long j = 0; j < count && ok; ++j) {
+      for (int j = 0; j < count && ok; ++j) {
         const bool fresh = w.first();
         w.next();
         if (j + 1 < count) scores(j + 1);
@@ -531,7 +529,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
     float l[RH];
     bool ok = true;
     int first_tile = 0;
-    for (long long j = 0; j < count; ++j) {
+    for (int j = 0; j < count; ++j) {
       const bool first = w.first(), last = w.last();
       const int rows = min(R, p.n_rows - w.block * R), all_see = w.all_see();
       if (first) {
