@@ -3,7 +3,9 @@
 //
 // Work, workspace and join are those of paged_attention.cuh's line of tiles; a tile is 128 keys and one CTA has an SM.
 // With mma.sync every warp loads fragments, rescales and moves its sums itself: 4800 warp instructions for 64 keys
-// of 48 rows, which bound it (IPC 1.3, 31 % of the tensor pipe). Here one thread issues the products of whole tiles
+// of 48 rows, which bound it (IPC 1.3, 31 % of the tensor pipe; 107 us for 8 requests of 8192 positions and 8 rows of
+// 48 / 8 heads x 128, against 67 us here; 64 requests of 1 to 8192 positions, one row: 209 and 177 us, 91 % of the measured
+// copy rate). Here one thread issues the products of whole tiles
 // from shared memory and the softmax has one thread per key:
 //   scores  S [128 keys x R rows] = K Q^T         A = the tile's keys (K-major), B = the query rows
 //   sums    O [128 of D x 2 R] += V^T [P hi, P lo]  A = the tile's values as they lie (M-major), B = the probabilities
@@ -211,6 +213,7 @@ template <int D, int R>
 struct TcShape {
   static constexpr int N = R < 16 ? 16 : R;   // columns of the scores
   static constexpr int kPairs = 2 * R;        // columns of the sums
+  static constexpr int kTmem = 128 + 128 * (D / 128) <= 256 ? 256 : 512;  // two score buffers, then the sums
   static constexpr int kTile = 128, kThreads = 480, kSoftmax = 256, kLoaders = 96;
   static constexpr int kHalves = D / 128;              // 128-wide pieces of a key or a value
   static constexpr int kSlot = 128 * 128 * 2, kP = 128 * 128, kQ = N * D * 2;
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
     }
   }
   if (warp == 8) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)), "r"(S::kTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
@@ -714,7 +717,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem) : "memory");
   if (tid == 0 && *dead) flag(a.status, MK_OP_TIMEOUT);
 }
 

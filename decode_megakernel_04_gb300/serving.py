@@ -197,7 +197,8 @@ def _workspace(size, device, dev, stream):
     workspace = torch.empty(size, dtype=torch.uint8, device=device)
     if stream is not None and stream != _raw_stream(dev):
         # torch may hand this memory out again on its own stream while the call still runs on the other
-        workspace.record_stream(torch.cuda.ExternalStream(stream, device=device))
+        workspace.record_stream(torch.cuda.ExternalStream(stream, device=device) if stream else
+                                torch.cuda.default_stream(device))
     return workspace
 
 

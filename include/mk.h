@@ -575,7 +575,8 @@ typedef struct mk_logit_controls_args {
   void* workspace;             /* device, mk_logit_controls_workspace bytes                        */
   int64_t workspace_bytes;
   int64_t logits_stride, out_stride, history_stride, bias_stride, allowed_stride;
-  int32_t rows, vocab, max_history, n_biases; /* max_history <= MK_LOGIT_MAX_HISTORY, n_biases <= MK_LOGIT_MAX_BIASES */
+  int32_t rows, vocab;         /* rows <= 2^20, vocab <= 2^24                                      */
+  int32_t max_history, n_biases; /* at most MK_LOGIT_MAX_HISTORY and MK_LOGIT_MAX_BIASES              */
   int32_t dtype;               /* MK_F32, MK_BF16 or MK_F16                                        */
 } mk_logit_controls_args;
 mk_status mk_logit_controls(const mk_logit_controls_args* args, int device, void* stream);

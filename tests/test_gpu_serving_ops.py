@@ -456,6 +456,13 @@ CASES_ATT = [  # lens, R, hq, hkv, d, page, dtype, cache, layout
     ([30000], 1, 2, 1, 64, 16, F16, F16, "head"),
     ([12000, 50], 1, 6, 1, 256, 32, F16, E4M3, "head"),
     ([i * 7 % 400 for i in range(300)], 1, 4, 1, 64, 16, F16, F16, "head"),
+    # keys that only some rows see on both sides of a tile's end
+    ([128, 129, 131, 135, 136, 255, 256, 257, 260, 1025], 8, 6, 1, 128, 16, BF16, BF16, "head"),
+    ([128, 129, 133, 256, 258, 7], 8, 3, 1, 256, 64, F16, F16, "place"),
+    ([140, 128, 143, 15, 16, 17, 300], 16, 2, 1, 128, 16, BF16, BF16, "head"),   # 32 rows of 16 new tokens
+    ([140, 33], 17, 2, 1, 128, 16, F16, F16, "head"),
+    ([2300, 700], 4, 16, 1, 256, 32, BF16, BF16, "head"),        # 64 rows, 256 wide
+    ([i * 37 % 900 for i in range(90)], 2, 24, 4, 128, 16, BF16, BF16, "place"),
 ]
 
 
@@ -503,6 +510,30 @@ def test_attention_scores_of_any_size():
     got, lse = run_attention(s, scale=1e-3)  # equal scores of -3.4e35: the mean of the values
     out, _, av, _ = attention_reference(s, 1e-3)
     check_rounded(got, out, BF16, "equal scores", (300 * 2.0 ** -23 + 2.0 ** -16) * av)
+
+
+@pytest.mark.parametrize("width", [None, 50000])
+@pytest.mark.parametrize("cache, d", [(BF16, 128), (BF16, 256), (F16, 64), (E4M3, 128)])
+def test_attention_scores_that_grow_and_that_begin_at_minus_infinity(cache, d, width):
+    """A maximum that moves with every tile; and requests whose first keys give every row -infinity."""
+    s = attention_inputs([1500, 300, 1], 2, 6, 1, d, 16, F16 if cache is F16 else BF16, cache, seed=21, poison=False, max_pages=width)
+    for b, n in enumerate([1500, 300, 1]):
+        p = torch.arange(n, device=DEV)
+        at = s["table"][b].long()[p // 16], slice(None), p % 16
+        s["k"][at] = (s["k"][at].float() * (p / 400)[:, None, None]).to(cache)
+    got, lse = run_attention(s, scale=0.5)
+    check_attention(s, got, lse, 0.5, "growing")
+    if cache is E4M3:
+        return  # no infinity in that type
+    s["q"][..., 0] = 1.0
+    at = s["table"][0].long()[torch.arange(400, device=DEV) // 16], slice(None), torch.arange(400, device=DEV) % 16, 0
+    s["k"][at] = float("-inf")
+    s["k"][s["table"][2, 0].long(), :, 0, 0] = float("-inf")  # the request of one key: nothing is left of it
+    got, lse = run_attention(s, scale=0.5)
+    assert (got[2] == 0).all() and (lse[2] == -math.inf).all()
+    out, l64, av, _ = attention_reference(s, 0.5)
+    check_rounded(got[:2], out[:2], s["q"].dtype, "minus infinity", 2.0 ** -10 * av[:2])
+    assert (lse[:2].double() - l64[:2]).abs().max() < 2.0 ** -9
 
 
 def test_attention_lengths_and_pages_out_of_range():

@@ -84,7 +84,8 @@ REFUSALS = [
         dict(head_dim=8), dict(head_dim=100), dict(head_dim=288), dict(dtype=2), dict(cache_dtype=1), dict(cache_dtype=2),
         dict(max_pages=1 << 20, page_size=1 << 11, table_stride=1 << 20)]),
     ("mk_logit_controls", logits, BAD, [
-        dict(logits=0), dict(out=0), dict(history=0), dict(bias_ids=0), dict(bias_vals=0), dict(rows=-1), dict(vocab=0),
+        dict(logits=0), dict(out=0), dict(history=0), dict(bias_ids=0), dict(bias_vals=0), dict(rows=-1), dict(vocab=0), dict(rows=(1 << 20) + 1),
+        dict(vocab=(1 << 24) + 1, logits_stride=1 << 25, out_stride=1 << 25, allowed_stride=1 << 20),
         dict(logits_stride=99), dict(out_stride=99), dict(history_stride=9), dict(bias_stride=2), dict(allowed_stride=3),
         dict(out=P, out_stride=104), dict(out=P, dtype=0), dict(logits=P + 2), dict(out=P + 1)]),
     ("mk_logit_controls", logits, UNSUPPORTED, [
@@ -116,6 +117,11 @@ def test_nothing_to_do(lib):
 
 def test_workspace_refusals(lib):
     n = C.c_uint64(0)
+    fn = lib.mk_logit_controls_workspace
+    assert fn(None, 0, C.byref(n)) == BAD
+    assert fn(C.byref(logits()), 0, None) == BAD
+    assert fn(C.byref(logits(dtype=3)), 0, C.byref(n)) == UNSUPPORTED
+    assert fn(C.byref(logits()), -1, C.byref(n)) == BAD
     fn = lib.mk_paged_attention_workspace
     assert fn(None, 0, C.byref(n)) == BAD
     assert fn(C.byref(attention()), 0, None) == BAD
