@@ -231,7 +231,7 @@ struct TcShape {
   static constexpr int kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
-constexpr float kNoBase = -1e30f;
+constexpr float kNoBase = -3.402823466e38f;  // the lowest finite value: what a row's base begins with
 constexpr int kTcMaxRows = 16;   // query rows of a request (of its block of new tokens)
 
 struct TcBars {
@@ -559,35 +559,30 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
           if (late) tail[(key - all_see) * 64 + r0 + r] = s[r];
         }
       }
-      // from here on s is the score less the base, in exp2's units
+      // The base is subtracted once it is known to stay: added back it would not give the score again (base kNoBase).
       float big = -INFINITY;
       if (!first) {
 #pragma unroll
         for (int r = 0; r < RH; r += 4) {
           const float4 base = *reinterpret_cast<const float4*>(base_of + r0 + r);
-          s[r] -= base.x, s[r + 1] -= base.y, s[r + 2] -= base.z, s[r + 3] -= base.w;
-          big = fmaxf(big, fmaxf(fmaxf(s[r], s[r + 1]), fmaxf(s[r + 2], s[r + 3])));
+          big = fmaxf(big, fmaxf(fmaxf(s[r] - base.x, s[r + 1] - base.y), fmaxf(s[r + 2] - base.z, s[r + 3] - base.w)));
         }
       }
       bool waited = false;
       if (any_of(1, S::kSoftmax, first || big > 8.0f)) {
 #pragma unroll
         for (int r = 0; r < RH; ++r) {
-          if (!first) s[r] += base_of[r0 + r];
           const float x = warp_largest(s[r]);
           if (lane == 0) warp_max[wq * 64 + r0 + r] = x;
         }
         named_sync(1, S::kSoftmax);
         if (tid < R) {
-          // no score above -infinity yet: a base that any finite score passes
           const float old = first ? kNoBase : base_of[tid];
           const float base = fmaxf(fmaxf(fmaxf(warp_max[tid], warp_max[64 + tid]), fmaxf(warp_max[128 + tid], warp_max[192 + tid])), old);
           base_of[tid] = base;
           shrink[tid] = exp2_fast(old - base);
         }
         named_sync(1, S::kSoftmax);
-#pragma unroll
-        for (int r = 0; r < RH; ++r) s[r] -= base_of[r0 + r];
         if (!first) {
           ok = bar_wait(&bars.p_empty, static_cast<uint32_t>(j - 1) & 1, dead) && ok;  // the last tile's sums are complete
           waited = true;
@@ -604,6 +599,11 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
             tc_st(at, v);
           }
         }
+      }
+#pragma unroll
+      for (int r = 0; r < RH; r += 4) {
+        const float4 base = *reinterpret_cast<const float4*>(base_of + r0 + r);
+        s[r] -= base.x, s[r + 1] -= base.y, s[r + 2] -= base.z, s[r + 3] -= base.w;
       }
       if (j > 0 && !waited) ok = bar_wait(&bars.p_empty, static_cast<uint32_t>(j - 1) & 1, dead) && ok;  // the buffer is free
       unsigned char* to = smem + S::kOffP + t * 128;

@@ -536,6 +536,36 @@ def test_attention_scores_that_grow_and_that_begin_at_minus_infinity(cache, d, w
     assert (lse[:2].double() - l64[:2]).abs().max() < 2.0 ** -9
 
 
+@pytest.mark.parametrize("width", [None, 50000])
+@pytest.mark.parametrize("dtype, d", [(BF16, 128), (F16, 128), (BF16, 256)])
+def test_attention_whole_tiles_of_minus_infinity_before_the_first_score(dtype, d, width):
+    """Tiles whose keys give every row -infinity, with the only finite scores behind them."""
+    s = attention_inputs([512, 256, 200], 2, 12, 2, d, 16, dtype, dtype, seed=31, poison=False, max_pages=width)
+    s["q"][..., 0] = 1.0
+    qk = attention_reference(s, 0.1)[3]  # at least that of the keys that are left
+    for b, tiles in enumerate([(0, 2), (0,), (0,)]):
+        for t in tiles:
+            p = 128 * t + torch.arange(128, device=DEV)
+            s["k"][s["table"][b].long()[p // 16], :, p % 16, 0] = -math.inf
+    got, lse = run_attention(s, scale=0.1)
+    out, l64, av, _ = attention_reference(s, 0.1)
+    ds = qk * (d + 4) * 2.0 ** -23  # the bounds of check_attention
+    check_rounded(got, out, dtype, "out", (2 * (ds + 2.0 ** -21 + 512 * 2.0 ** -23) + 2.0 ** -16)[..., None] * av)
+    assert ((lse.double() - l64).abs() <= ds + 2.0 ** -20 + 512 * 2.0 ** -23 + l64.abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("width", [None, 50000])
+def test_attention_of_the_lowest_scores(width):
+    """Equal scores of -3.4e35 in long and short calls: the mean of the values."""
+    s = attention_inputs([300, 65], 2, 6, 1, 128, 16, BF16, BF16, seed=33, poison=False, max_pages=width)
+    s["k"].fill_(torch.finfo(BF16).min)
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    got, _ = run_attention(s, scale=1e-3)
+    out, _, av, _ = attention_reference(s, 1e-3)
+    check_rounded(got, out, BF16, "equal scores", (300 * 2.0 ** -23 + 2.0 ** -16) * av)
+
+
 def test_attention_lengths_and_pages_out_of_range():
     s = attention_inputs([40, 30, 20, 10], 1, 4, 2, 64, 8, BF16, BF16, seed=6, max_pages=5, poison=False)
     good, gl = run_attention(s)
