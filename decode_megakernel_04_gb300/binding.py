@@ -300,13 +300,16 @@ class Megakernel:
         in place on the same stream and argmax is the greedy token of what is left (-1: nothing is allowed)."""
         B, R = tokens.shape
         if controls is not None:
-            from .serving import logit_controls
+            from .serving import _call, prepare_logit_controls
             z = None if logits is None else logits.view(-1, self.cfg.vocab)
             if z is None or z.shape[0] != B * R or z.get_device() != self.device:
                 raise ValueError("controls need logits [batch * rows, vocab] on the handle's device")
+            # what does not fit is refused before the step, which cannot be taken back
+            call, workspace = prepare_logit_controls(z, z, token=None if argmax is None else argmax.view(-1),
+                                                     stream=stream or 0, **controls)
             self._check(self.lib.mk_decode_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R, z.data_ptr(),
                                                  None, stream))
-            logit_controls(z, z, token=None if argmax is None else argmax.view(-1), stream=stream or 0, **controls)
+            _call(*call)
             return
         self._check(self.lib.mk_decode_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R,
                                              _ptr(logits), _ptr(argmax), stream))

@@ -249,6 +249,15 @@ def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None
     bias_ids int32 / bias_vals fp32 [rows, m] (pad ids with -1; the last entry of a token counts); allowed: int32
     [rows, ceil(vocab / 32)] bit mask; token: int32 [rows], -1 where nothing is allowed. workspace: a uint8 tensor of
     what mk_logit_controls_workspace says; None allocates what the call needs from torch's allocator."""
+    call, workspace = prepare_logit_controls(logits, out, history, prompt_len, total_len, repetition, presence, frequency,
+                                             bias_ids, bias_vals, allowed, token, workspace, stream)
+    _call(*call)
+
+
+def prepare_logit_controls(logits, out, history=None, prompt_len=None, total_len=None, repetition=None, presence=None,
+                           frequency=None, bias_ids=None, bias_vals=None, allowed=None, token=None, workspace=None,
+                           stream=None):
+    """logit_controls' checks without its launch: (_call's arguments, the workspace, to be kept until the call)."""
     dev = logits.get_device()
     _need(dev >= 0 and logits.dim() == 2, "logit_controls needs logits [rows, vocab] on a CUDA device")
     n, vocab = logits.shape
@@ -261,6 +270,7 @@ def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None
     bp, bs, nb = _rows(bias_ids, _I32, n, dev, "bias_ids")
     bvp, bvs, nbv = _rows(bias_vals, _F32, n, dev, "bias_vals")
     _need(nb == nbv and bs == bvs, "bias_ids and bias_vals have one layout")
+    _need(history is not None or (repetition is None and presence is None and frequency is None), "penalties need a history")
     ap, as_, words = _rows(allowed, _I32, n, dev, "allowed")
     _need(allowed is None or words >= (vocab + 31) // 32, "allowed holds a bit for each token")
     head = (lp, op, _vector(token, _I32, n, dev, "token"), hp, _vector(prompt_len, _I32, n, dev, "prompt_len"),
@@ -274,4 +284,4 @@ def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None
             workspace = _workspace(size, logits.device, dev, stream)
     if workspace is not None:
         packed = _pack_logits(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), workspace.numel(), *tail)
-    _call(load().mk_logit_controls, packed, dev, stream, "logit_controls")
+    return (load().mk_logit_controls, packed, dev, stream, "logit_controls"), workspace

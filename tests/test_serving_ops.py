@@ -158,6 +158,21 @@ def test_packed_arguments_are_the_structs():
     assert serving._pack_attention(*vals) == bytes(a)
 
 
+def test_controls_that_do_not_fit_are_refused_before_the_step():
+    """A step cannot be taken back, so nothing of it is enqueued when its controls are wrong."""
+    class Lib:
+        def mk_decode_step(self, *args):
+            raise AssertionError("the step ran")
+
+    m = binding.Megakernel.__new__(binding.Megakernel)
+    m.lib, m.device, m.h = Lib(), -1, None
+    m.cfg = type("Cfg", (), {"vocab": 8})
+    tok = torch.zeros(2, 1, dtype=torch.int32)
+    for z in (None, torch.zeros(3, 8), torch.zeros(2, 8)):  # none, another number of rows, not on a GPU
+        with pytest.raises(ValueError):
+            m.step(tok, tok[:, 0], z, controls=dict(bias_ids=tok))
+
+
 def test_wrappers_refuse_cpu_tensors():
     i = torch.zeros(2, dtype=torch.int32)
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
