@@ -515,7 +515,9 @@ extern "C" mk_status mk_logit_controls(const mk_logit_controls_args* args, int d
     return refuse(MK_ERR_INVALID_ARG, me, "a row stride is shorter than its row");
   if (a.logits == a.out && (a.dtype != MK_F32 || a.logits_stride != a.out_stride))
     return refuse(MK_ERR_INVALID_ARG, me, "out may be logits only in fp32 with one stride");
-  if (!aligned(a.logits, a.dtype == MK_F32 ? 4 : 2) || !aligned(a.out, 4) || !aligned(a.allowed, 4))
+  if (!aligned(a.logits, a.dtype == MK_F32 ? 4 : 2) || 
+      !aligned({a.out, a.token, a.history, a.prompt_len, a.total_len, a.repetition, a.presence, a.frequency, a.bias_ids, a.bias_vals,
+                a.allowed}, 4))
     return refuse(MK_ERR_INVALID_ARG, me, "a misaligned pointer");
   DeviceGuard guard(device);
   if (guard.err != cudaSuccess) return launched(me, guard.err);

@@ -4,6 +4,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -68,6 +69,11 @@ inline cudaError_t allow_smem(int device, int bytes) {
 }
 
 inline bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline bool aligned(std::initializer_list<const void*> ps, unsigned n) {
+  for (const void* p : ps)
+    if (!aligned(p, n)) return false;
+  return true;
+}
 
 inline mk_status check_device(const char* call, int device) {
   return device < 0 || device >= kMaxDevices ? refuse(MK_ERR_INVALID_ARG, call, "device %d", device) : MK_OK;

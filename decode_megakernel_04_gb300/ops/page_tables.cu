@@ -6,8 +6,6 @@
 // end; with n_free + returned <= ring_size (checked) the two never touch one entry, so they need no order between
 // them. What is read by all and may be written in place (the ring's state, lens over the lengths) is the one hazard:
 // a call of one CTA writes it behind a barrier, a larger one in place takes a second launch for it.
-#include <initializer_list>
-
 #include "mk_ops.cuh"
 
 namespace mkop {
@@ -192,6 +190,9 @@ extern "C" mk_status mk_page_tables(const mk_page_tables_args* p, int device, vo
   if (!a.table || !a.held || !a.start || !a.count || !a.ring || !a.ring_state || !a.ring_state_out ||
       (!a.slots && a.n_tokens > 0))
     return refuse(MK_ERR_INVALID_ARG, me, "a required pointer is NULL");
+  if (!aligned({a.table, a.held, a.start, a.count, a.ring, a.ring_state, a.ring_state_out, a.positions, a.owners, a.starts,
+                a.lens, a.status}, 4) || !aligned(a.slots, 8))
+    return refuse(MK_ERR_INVALID_ARG, me, "a misaligned pointer");
   if (a.batch < 1 || a.batch > MK_PAGE_TABLES_MAX_BATCH)
     return refuse(MK_ERR_INVALID_ARG, me, "batch %d outside 1..%d", a.batch, MK_PAGE_TABLES_MAX_BATCH);
   if (a.max_pages < 1 || a.page_size < 1 || a.n_pages < 1 || a.n_tokens < 0)

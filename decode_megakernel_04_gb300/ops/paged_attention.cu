@@ -227,7 +227,7 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
   using namespace mkop;
   using namespace mkop::attn;
   if (!args) return MK_ERR_INVALID_ARG;
-  Params p;
+  Params p{};
   p.a = *args;
   const mk_paged_attention_args& a = p.a;
   const bool e4m3 = a.cache_dtype == MK_E4M3;
@@ -242,8 +242,10 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
   if (!a.q || !a.k_pages || !a.v_pages || !a.table || !a.lens || !a.out || (e4m3 && (!a.k_scale || !a.v_scale)))
     return refuse(MK_ERR_INVALID_ARG, kMe, "a required pointer is NULL");
   if (a.table_stride < a.max_pages) return refuse(MK_ERR_INVALID_ARG, kMe, "table rows shorter than max_pages");
-  if (!aligned(a.q, 16) || !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) || !aligned(a.out, 16) || !aligned(a.workspace, 16))
+  if (!aligned({a.q, a.k_pages, a.v_pages, a.out, a.workspace}, 16))
     return refuse(MK_ERR_INVALID_ARG, kMe, "a pointer is not 16-byte aligned");
+  if (!aligned({a.table, a.lens, a.k_scale, a.v_scale, a.lse, a.status}, 4))
+    return refuse(MK_ERR_INVALID_ARG, kMe, "a misaligned pointer");
   // the stride of a dimension of one element is never used
   const int q_size[3] = {a.batch, a.rows, a.n_q_heads}, page_dims[3] = {a.n_pages, a.n_kv_heads, a.page_size};
   for (int i = 0; i < 3; ++i) {
@@ -251,6 +253,12 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
       return refuse(MK_ERR_INVALID_ARG, kMe, "a stride is not a multiple of 8 elements");
     if (page_dims[i] > 1 && (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8)))
       return refuse(MK_ERR_INVALID_ARG, kMe, "a cache stride is not a multiple of 16 bytes");
+    const int64_t k = page_dims[i] > 1 ? a.k_page_stride[i] : 0, v = page_dims[i] > 1 ? a.v_page_stride[i] : 0;
+    const int64_t unit = e4m3 ? 16 : 8;  // elements of 16 bytes
+    if (k < 0 || k / unit > UINT32_MAX || v < 0 || v / unit > UINT32_MAX)
+      return refuse(MK_ERR_UNSUPPORTED, kMe, "a cache stride is negative or 64 GB and more");
+    p.k_step[i] = static_cast<uint32_t>(k / unit);
+    p.v_step[i] = static_cast<uint32_t>(v / unit);
   }
   DeviceGuard guard(device);
   if (guard.err != cudaSuccess) return launched(kMe, guard.err);
@@ -259,14 +267,6 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
   if (pl.bytes && (!a.workspace || a.workspace_bytes < static_cast<int64_t>(pl.bytes)))
     return refuse(MK_ERR_INVALID_ARG, kMe, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), pl.bytes);
   char* ws = static_cast<char*>(a.workspace);
-  for (int i = 0; i < 3; ++i) {
-    const int64_t k = page_dims[i] > 1 ? a.k_page_stride[i] * (e4m3 ? 1 : 2) / 16 : 0;
-    const int64_t v = page_dims[i] > 1 ? a.v_page_stride[i] * (e4m3 ? 1 : 2) / 16 : 0;
-    if (k < 0 || k > UINT32_MAX || v < 0 || v > UINT32_MAX)
-      return refuse(MK_ERR_UNSUPPORTED, kMe, "a cache stride is negative or 64 GB and more");
-    p.k_step[i] = static_cast<uint32_t>(k);
-    p.v_step[i] = static_cast<uint32_t>(v);
-  }
   p.page = div_by(a.page_size);
   p.group_div = div_by(pl.group);
   p.group = pl.group;

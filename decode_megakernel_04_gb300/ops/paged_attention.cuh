@@ -139,7 +139,7 @@ struct Shape {
   static constexpr int kTile = E4M3 ? (DP == 64 ? 128 : DP == 128 && MT == 1 ? 128 : 64) : (DP == 256 && MT > 1 ? 32 : 64);
   static constexpr int kWarpKeys = kTile / WK;
   static constexpr int kBlock = kWarpKeys < 32 ? kWarpKeys : 32;  // keys of one softmax step
-    static constexpr int kStages = MT > 2 && (DP == 256 || E4M3) ? 3 : 2;
+  static constexpr int kStages = MT > 2 && (DP == 256 || E4M3) ? 3 : 2;
   static constexpr int kKeyBytes = kTile * kRowBytes;  // of a tile's keys (as many of values)
   static constexpr int kStageBytes = 2 * kKeyBytes;
   static constexpr int kQBytes = kRows * DP * 2;

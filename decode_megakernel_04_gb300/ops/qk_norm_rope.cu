@@ -46,7 +46,7 @@ struct Work {
 
 template <typename T, int L, bool E4M3>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) qk_kernel(const __grid_constant__ Work w) {
-    const mk_qk_norm_rope_args& a = w.a;
+  const mk_qk_norm_rope_args& a = w.a;
   constexpr int H = 32 / L;  // heads a warp holds at once
   const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
   const int half = a.rope_dim / 2;
@@ -226,9 +226,10 @@ extern "C" mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* p, int device, 
   if (!a.q || !a.k || !a.q_out || (a.rope_dim && (!a.inv_freq || !a.positions)) || (cache && (!a.v || !a.slots)) ||
       (cache && e4m3 && (!a.k_scale || !a.v_scale)))
     return refuse(MK_ERR_INVALID_ARG, me, "a required pointer is NULL");
-  const void* ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out, a.q_gain, a.k_gain, a.k_pages, a.v_pages};
-  for (const void* q : ptrs)
-    if (!aligned(q, 16)) return refuse(MK_ERR_INVALID_ARG, me, "a pointer is not 16-byte aligned");
+  if (!aligned({a.q, a.k, a.v, a.q_out, a.k_out, a.q_gain, a.k_gain, a.k_pages, a.v_pages}, 16))
+    return refuse(MK_ERR_INVALID_ARG, me, "a pointer is not 16-byte aligned");
+  if (!aligned({a.inv_freq, a.slots}, 8) || !aligned({a.positions, a.k_scale, a.v_scale, a.status}, 4))
+    return refuse(MK_ERR_INVALID_ARG, me, "a misaligned pointer");
   // the stride of a dimension of one element is never used
   const int tokens_heads[2][2] = {{a.n_tokens, a.n_q_heads}, {a.n_tokens, a.n_kv_heads}};
   for (int i = 0; i < 2; ++i) {

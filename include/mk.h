@@ -404,7 +404,7 @@ mk_status mk_decode_step_static(const mk_model_desc* desc, const mk_weights* wei
  * or a length out of range) never leads to an access out of bounds: the call's text says what happens
  * instead, and, where `status` is not NULL, the mk_op_flag bits are OR-ed into that device int32.
  * Calls from several host threads, and calls on several streams, may overlap as long as the memory they
- * write does not. Strides are in elements.
+ * write does not. Strides are in elements; pointers are aligned to their element where nothing more is said.
  *
  * A paged cache is one tensor for the keys and one for the values, [n_pages][n_kv_heads][page_size]
  * [head_dim] by any strides with the innermost contiguous; request b's position p lives on page
@@ -470,7 +470,7 @@ mk_status mk_page_tables(const mk_page_tables_args* args, int device, void* stre
  * is reduced in 64-bit integers), and each value is rounded once, to its output type (e4m3: value / scale,
  * nearest even, saturating at 448). q_out may be q, k_out may be k (same strides).
  * Token t's key and value go to slots[t] of the paged cache; a negative slot stores nothing, one outside
- * the cache stores nothing and sets MK_OP_BAD_PAGE. Two tokens with one slot: either may stay.
+ * the cache stores nothing and sets MK_OP_BAD_PAGE. Two tokens with one slot: its place holds parts of either.
  * Errors: head_dim not a multiple of 16 in 16..256, rope_dim not a multiple of 8 in 0..head_dim, pointers
  * not 16-byte aligned or strides not multiples of 8 elements (16 for an e4m3 cache). One launch. */
 typedef struct mk_qk_norm_rope_args {
@@ -504,7 +504,8 @@ mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* args, int device, void* st
  *   s = scale * q . k,  p = softmax(s),  out = sum p v,  lse = log(sum exp(s)) (natural)
  * A row that sees nothing gives out = 0 and lse = -infinity. Values in the cache that a row does not see
  * (positions from lens[b] on, later rows' keys) do not reach it, whatever they hold (NaN included).
- * Scores, softmax statistics and sums are fp32; out is rounded once.
+ * Scores, softmax statistics and sums are fp32; out is rounded once. An infinite value that a row sees makes that column
+ * of the row NaN or infinite; a score of +infinity or NaN makes the row NaN.
  * A length below 0 counts as 0, one beyond max_pages * page_size as that (MK_OP_BAD_LENGTH); keys and
  * values of a page outside 0 .. n_pages - 1 read as zeros (MK_OP_BAD_PAGE). Table entries of pages a
  * request does not reach are not read.
@@ -512,7 +513,8 @@ mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* args, int device, void* st
  * in a fixed order: the result does not depend on timing. `workspace` is device scratch of
  * mk_paged_attention_workspace bytes, 16-byte aligned, with any contents; calls that may overlap need one each.
  * Errors: head_dim not a multiple of 16 in 16..256; n_q_heads not a multiple of n_kv_heads; pointers not
- * 16-byte aligned or strides not multiples of 8 elements (16 for an e4m3 cache); too small a workspace.
+ * 16-byte aligned or strides not multiples of 8 elements (16 for an e4m3 cache); cache strides negative or of 64 GB and
+ * more; too small a workspace.
  * One launch without a workspace for small calls, else two (the second joins the splits). */
 typedef struct mk_paged_attention_args {
   const void* q;               /* device [batch][rows][n_q_heads][head_dim], dtype                  */

@@ -61,7 +61,8 @@ REFUSALS = [
     ("mk_page_tables", tables, BAD, [
         dict(table=0), dict(held=0), dict(start=0), dict(count=0), dict(ring=0), dict(ring_state=0), dict(ring_state_out=0),
         dict(slots=0), dict(batch=0), dict(batch=4097), dict(max_pages=0), dict(page_size=0), dict(n_pages=0),
-        dict(n_tokens=-1), dict(table_stride=7), dict(ring_size=31)]),
+        dict(n_tokens=-1), dict(table_stride=7), dict(ring_size=31), dict(table=P + 2), dict(held=P + 1), dict(slots=P + 4),
+        dict(starts=P + 2), dict(ring_state_out=P + 2), dict(status=P + 1)]),
     ("mk_page_tables", tables, UNSUPPORTED, [
         dict(max_pages=1 << 20, page_size=1 << 11, table_stride=1 << 20), dict(n_pages=1 << 20, page_size=1 << 11, ring_size=1 << 20)]),
     ("mk_qk_norm_rope", qk, BAD, [
@@ -70,7 +71,8 @@ REFUSALS = [
         dict(page_size=0), dict(eps=-1.0), dict(eps=float("nan")), dict(q=P + 8), dict(k_out=P + 2), dict(q_gain=P + 4),
         dict(q_stride=(512, 124)), dict(k_stride=(508, 128)), dict(v_stride=(512, 4)), dict(q_out_stride=(512, 127)),
         dict(k_out=P, k_out_stride=(512, 1)), dict(k_page_stride=(4096, 2048, 132)),
-        dict(v_page_stride=(4096, 2048, 136), cache_dtype=3, k_scale=P, v_scale=P)]),
+        dict(v_page_stride=(4096, 2048, 136), cache_dtype=3, k_scale=P, v_scale=P), dict(positions=P + 2), dict(slots=P + 4),
+        dict(inv_freq=P + 4), dict(status=P + 2), dict(cache_dtype=3, k_scale=P + 2, v_scale=P)]),
     ("mk_qk_norm_rope", qk, UNSUPPORTED, [
         dict(head_dim=8), dict(head_dim=72), dict(head_dim=272), dict(rope_dim=136), dict(rope_dim=12), dict(rope_dim=-8),
         dict(dtype=2), dict(dtype=3), dict(cache_dtype=1), dict(cache_dtype=2), dict(n_pages=1 << 20, page_size=1 << 11)]),
@@ -79,15 +81,19 @@ REFUSALS = [
         dict(cache_dtype=3), dict(batch=-1), dict(rows=0), dict(n_q_heads=0), dict(n_kv_heads=0), dict(n_kv_heads=3),
         dict(n_pages=0), dict(page_size=0), dict(max_pages=0), dict(table_stride=7), dict(q=P + 8), dict(out=P + 2),
         dict(workspace=P + 4), dict(q_stride=(512, 512, 4)), dict(out_stride=(4, 512, 128)),
-        dict(k_page_stride=(4096, 2048, 100)), dict(v_page_stride=(4096, 8, 128), cache_dtype=3, k_scale=P, v_scale=P)]),
+        dict(k_page_stride=(4096, 2048, 100)), dict(v_page_stride=(4096, 8, 128), cache_dtype=3, k_scale=P, v_scale=P),
+        dict(table=P + 2), dict(lens=P + 1), dict(lse=P + 2), dict(status=P + 2), dict(cache_dtype=3, k_scale=P, v_scale=P + 1)]),
     ("mk_paged_attention", attention, UNSUPPORTED, [
         dict(head_dim=8), dict(head_dim=100), dict(head_dim=288), dict(dtype=2), dict(cache_dtype=1), dict(cache_dtype=2),
-        dict(max_pages=1 << 20, page_size=1 << 11, table_stride=1 << 20)]),
+        dict(max_pages=1 << 20, page_size=1 << 11, table_stride=1 << 20), dict(k_page_stride=(-4096, 2048, 128)),
+        dict(v_page_stride=(4096, 2048, -128)), dict(v_page_stride=(1 << 35, 2048, 128)),
+        dict(k_page_stride=(1 << 36, 2048, 128), cache_dtype=3, k_scale=P, v_scale=P)]),
     ("mk_logit_controls", logits, BAD, [
         dict(logits=0), dict(out=0), dict(history=0), dict(bias_ids=0), dict(bias_vals=0), dict(rows=-1), dict(vocab=0), dict(rows=(1 << 20) + 1),
         dict(vocab=(1 << 24) + 1, logits_stride=1 << 25, out_stride=1 << 25, allowed_stride=1 << 20),
         dict(logits_stride=99), dict(out_stride=99), dict(history_stride=9), dict(bias_stride=2), dict(allowed_stride=3),
-        dict(out=P, out_stride=104), dict(out=P, dtype=0), dict(logits=P + 2), dict(out=P + 1)]),
+        dict(out=P, out_stride=104), dict(out=P, dtype=0), dict(logits=P + 2), dict(out=P + 1),
+        dict(history=P + 2), dict(token=P + 1), dict(bias_vals=P + 2), dict(total_len=P + 2), dict(frequency=P + 2)]),
     ("mk_logit_controls", logits, UNSUPPORTED, [
         dict(dtype=3), dict(max_history=1 << 20, history_stride=1 << 20), dict(n_biases=2048, bias_stride=2048),
         dict(max_history=-1)]),
