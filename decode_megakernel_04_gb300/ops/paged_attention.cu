@@ -151,7 +151,10 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
   const int tiles = (pl.n_rows + 15) / 16;
   pl.blocks = (tiles + 3) / 4;
   const int mt = (tiles + pl.blocks - 1) / pl.blocks;
-  pl.build = a.cache_dtype == MK_E4M3 ? pick_e4m3(pl.dp, mt) : a.dtype == MK_BF16 ? pick_bf16(pl.dp, mt) : pick_f16(pl.dp, mt);
+  auto pick = [&](bool longer) {
+    return a.cache_dtype == MK_E4M3 ? pick_e4m3(pl.dp, mt, longer) : a.dtype == MK_BF16 ? pick_bf16(pl.dp, mt, longer) : pick_f16(pl.dp, mt, longer);
+  };
+  pl.build = pick(false);
   int sms, per_sm;
   cudaError_t e = sm_count(device, &sms);
   if (e == cudaSuccess) e = pl.build->occupancy(device, &per_sm);
@@ -179,9 +182,11 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
       a.cache_dtype != MK_E4M3 && (a.head_dim == 128 || a.head_dim == 256) && a.rows <= kTcMaxRows) {
     const int block_rows = pl.blocks == 1 ? pl.n_rows : 16 * mt;
     pl.build = a.dtype == MK_BF16 ? pick_tc_bf16(pl.dp, block_rows) : pick_tc_f16(pl.dp, block_rows);
-    if ((e = pl.build->occupancy(device, &per_sm)) != cudaSuccess) return e;
-    pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+  } else {
+    pl.build = pick(true);
   }
+  if ((e = pl.build->occupancy(device, &per_sm)) != cudaSuccess) return e;
+  pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
   const size_t slots = 2 * static_cast<size_t>(pl.ctas);
   pl.ml_at = slots * pl.build->rows * pl.dp * sizeof(float);
   pl.piece_at = pl.ml_at + slots * pl.build->rows * sizeof(float2);

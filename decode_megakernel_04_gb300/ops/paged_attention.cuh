@@ -128,7 +128,7 @@ __device__ inline float exp2_fast(float x) {
 }
 
 // ---- the shape of one build -----------------------------------------------------------------------------------------
-template <int DP, int MT, bool E4M3>
+template <int DP, int MT, bool E4M3, bool LONG>
 struct Shape {
   static constexpr int WM = MT, WK = MT == 1 ? 4 : 2, kWarps = WM * WK, kThreads = 32 * kWarps;
   static constexpr int kRows = 16 * MT;
@@ -136,7 +136,7 @@ struct Shape {
   static constexpr int kRowBytes = DP * kElt;         // of a key in shared memory
   static constexpr int kChunks = kRowBytes / 16;
   // 16 to 32 KB of keys and values a tile (64 KB at 256 wide and 16 rows, where four warps take 16 keys each)
-  static constexpr int kTile = E4M3 ? (DP == 64 ? 128 : DP == 128 && MT == 1 ? 128 : 64) : (DP == 256 && MT > 1 ? 32 : 64);
+  static constexpr int kTile = E4M3 ? (DP == 64 ? 128 : DP == 128 && MT == 1 ? 128 : 64) : (DP == 256 && MT > 1 ? 32 : DP == 64 && LONG ? 128 : 64);
   static constexpr int kWarpKeys = kTile / WK;
   static constexpr int kBlock = kWarpKeys < 32 ? kWarpKeys : 32;  // keys of one softmax step
   static constexpr int kStages = MT > 2 && (DP == 256 || E4M3) ? 3 : 2;
@@ -180,10 +180,10 @@ __device__ inline uint32_t place(int row, int chunk) {  // byte offset of a 16-b
   return row * (kChunks * 16) + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-template <typename T, int DP, int MT, bool E4M3>
-__global__ void __launch_bounds__(Shape<DP, MT, E4M3>::kThreads, Shape<DP, MT, E4M3>::kCtas)
+template <typename T, int DP, int MT, bool E4M3, bool LONG>
+__global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP, MT, E4M3, LONG>::kCtas)
     attention_kernel(const __grid_constant__ Params p) {
-  using S = Shape<DP, MT, E4M3>;
+  using S = Shape<DP, MT, E4M3, LONG>;
   extern __shared__ __align__(128) unsigned char smem[];
   const mk_paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -735,10 +735,10 @@ struct Build {
   cudaError_t (*launch)(const Params& p, cudaStream_t s);
 };
 
-template <typename T, int DP, int MT, bool E4M3>
+template <typename T, int DP, int MT, bool E4M3, bool LONG = false>
 struct Make {
-  using S = Shape<DP, MT, E4M3>;
-  static constexpr auto kKernel = attention_kernel<T, DP, MT, E4M3>;
+  using S = Shape<DP, MT, E4M3, LONG>;
+  static constexpr auto kKernel = attention_kernel<T, DP, MT, E4M3, LONG>;
   static cudaError_t occupancy(int device, int* n) {
     static std::atomic<int> known[kMaxDevices];
     *n = known[device].load(std::memory_order_relaxed);
@@ -788,8 +788,15 @@ struct Make {
   static constexpr Build build() { return {S::kRows, S::kTile, occupancy, clusters, launch}; }
 };
 
+// longer: the call's tiles are one line. 16-bit caches 64 wide then have tiles of 128 keys up to 32 rows (64 requests of 1 to
+// 16384 positions, 32 / 8 heads: 212 us against 242 with 64 keys; 64 / 2 heads: 265, 336), of 64 with more (48 rows: 367
+// against 442, fewer CTAs on an SM); a cluster wants more tiles to share (129 requests of up to 700: 8.7 against 10.4).
 template <typename T, bool E4M3>
-inline const Build* pick(int dp, int mt) {
+inline const Build* pick(int dp, int mt, bool longer) {
+  if constexpr (!E4M3) {
+    static constexpr Build narrow[2] = {Make<T, 64, 1, false, true>::build(), Make<T, 64, 2, false, true>::build()};
+    if (longer && dp == 64 && mt <= 2) return &narrow[mt - 1];
+  }
   static constexpr Build all[3][4] = {
       {Make<T, 64, 1, E4M3>::build(), Make<T, 64, 2, E4M3>::build(), Make<T, 64, 3, E4M3>::build(), Make<T, 64, 4, E4M3>::build()},
       {Make<T, 128, 1, E4M3>::build(), Make<T, 128, 2, E4M3>::build(), Make<T, 128, 3, E4M3>::build(), Make<T, 128, 4, E4M3>::build()},
@@ -797,9 +804,9 @@ inline const Build* pick(int dp, int mt) {
   return &all[dp == 64 ? 0 : dp == 128 ? 1 : 2][mt - 1];
 }
 
-const Build* pick_bf16(int dp, int mt);
-const Build* pick_f16(int dp, int mt);
-const Build* pick_e4m3(int dp, int mt);
+const Build* pick_bf16(int dp, int mt, bool longer);
+const Build* pick_f16(int dp, int mt, bool longer);
+const Build* pick_e4m3(int dp, int mt, bool longer);
 
 }  // namespace attn
 }  // namespace mkop

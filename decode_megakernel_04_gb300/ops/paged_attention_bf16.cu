@@ -3,6 +3,6 @@
 
 namespace mkop {
 namespace attn {
-const Build* pick_bf16(int dp, int mt) { return pick<__nv_bfloat16, false>(dp, mt); }
+const Build* pick_bf16(int dp, int mt, bool longer) { return pick<__nv_bfloat16, false>(dp, mt, longer); }
 }  // namespace attn
 }  // namespace mkop

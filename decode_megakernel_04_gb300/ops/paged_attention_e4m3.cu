@@ -3,6 +3,6 @@
 
 namespace mkop {
 namespace attn {
-const Build* pick_e4m3(int dp, int mt) { return pick<__half, true>(dp, mt); }
+const Build* pick_e4m3(int dp, int mt, bool longer) { return pick<__half, true>(dp, mt, longer); }
 }  // namespace attn
 }  // namespace mkop

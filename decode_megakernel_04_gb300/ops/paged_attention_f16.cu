@@ -3,6 +3,6 @@
 
 namespace mkop {
 namespace attn {
-const Build* pick_f16(int dp, int mt) { return pick<__half, false>(dp, mt); }
+const Build* pick_f16(int dp, int mt, bool longer) { return pick<__half, false>(dp, mt, longer); }
 }  // namespace attn
 }  // namespace mkop

@@ -433,6 +433,8 @@ CASES_ATT = [  # lens, R, hq, hkv, d, page, dtype, cache, layout
     ([777, 1023, 5], 1, 36, 2, 128, 32, BF16, BF16, "head"),     # 18 rows of a kv head: two 16-row tiles
     ([900, 2], 1, 40, 1, 64, 256, F16, F16, "head"),             # 40 rows
     ([500, 70], 1, 72, 1, 128, 16, BF16, BF16, "head"),          # 72 rows: two blocks
+    ([900, 128, 5], 1, 32, 1, 64, 16, BF16, BF16, "place"),      # 64 wide, 32 and 64 rows
+    ([600, 129], 4, 16, 1, 64, 16, F16, F16, "head"),
     ([500, 70], 1, 100, 1, 256, 16, BF16, BF16, "head"),         # 100 rows, 256 wide
     ([8, 1, 64, 71, 0, 3, 1000], 8, 6, 1, 128, 16, BF16, BF16, "head"),
     ([9, 130, 64, 2], 5, 24, 4, 256, 64, BF16, BF16, "place"),
