@@ -11,8 +11,8 @@
 //   vocabulary, one word for each of its tokens, and joins the greedy token through distributed shared memory: one launch.
 //   Every CTA reads the whole history.
 // - Many rows: that would read histories as often as logits (64 rows with 4 to 8 thousand tokens of history: 82 us against
-//   17 for the pass alone). So a plain pass masks and leaves each chunk's largest logit, and a second kernel, one CTA a
-//   row, gathers the words in a hash table, computes the named tokens, and joins the largest: a chunk whose largest is a
+//   17 for the pass alone). So a plain pass masks and leaves each chunk's largest logit, and a second kernel, one CTA or
+//   more a row, gathers the words in a hash table, computes the named tokens, and joins the largest: a chunk whose largest is a
 //   named token is looked through again without these. (The other order, words sorted by chunk first and computed in
 //   the pass, was slower: 48 against 39 us for these rows, 77 against 70 for 256 rows of 163841 bf16 logits.)
 #include <cooperative_groups.h>
@@ -300,7 +300,8 @@ struct Table {
   int* tokens;
   uint32_t* words;
   int mask;
-  __device__ int first(int v) const { return static_cast<int>(static_cast<uint32_t>(v) * 2654435769u >> 8) & mask; }
+  static __device__ uint32_t hash(int v) { return static_cast<uint32_t>(v) * 2654435769u; }
+  __device__ int first(int v) const { return static_cast<int>(hash(v) >> 8) & mask; }
   __device__ uint32_t* word_of(int v) {
     for (int i = first(v);; i = (i + 1) & mask) {
       int old = *reinterpret_cast<volatile int*>(tokens + i);
@@ -316,13 +317,18 @@ struct Table {
   }
 };
 
+// A cluster of `split` CTAs (1, 2 or 4) has a row, each the tokens whose hash says so.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constant__ mk_logit_controls_args a, int places,
+__global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constant__ mk_logit_controls_args a, int split, int places,
                                                            int chunk_bits, int chunks, const unsigned long long* largest) {
   extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ unsigned long long cta_best;
+  cg::cluster_group cluster = cg::this_cluster();
   Table table{reinterpret_cast<int*>(smem), smem + places, places - 1};
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x / split;
+  const uint32_t rank = blockIdx.x % split;
+  auto owner = [&](int v) { return Table::hash(v) >> 30 & (split - 1); };
   const T* z = static_cast<const T*>(a.logits) + row * a.logits_stride;
   float* out = a.out + row * a.out_stride;
   const int32_t* mask = a.allowed ? a.allowed + row * a.allowed_stride : nullptr;
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
     __syncthreads();
     for (int e = tid; ids && e < a.n_biases; e += kThreads) {
       const int v = ids[e];
-      if (v >= 0 && v < V) atomicMax(table.word_of(v), static_cast<uint32_t>(e + 1));
+      if (v >= 0 && v < V && owner(v) == rank) atomicMax(table.word_of(v), static_cast<uint32_t>(e + 1));
     }
     __syncthreads();
     if (a.history && (a.repetition || a.presence || a.frequency)) {
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
         for (int i = 0; i < kAhead; ++i) v[i] = h0 + i * kThreads < total ? hist[h0 + i * kThreads] : -1;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          if (v[i] < 0 || v[i] >= V) continue;
+          if (v[i] < 0 || v[i] >= V || owner(v[i]) != rank) continue;
           uint32_t* word = table.word_of(v[i]);
           if (h0 + i * kThreads >= prompt) atomicAdd(word, 1u << 11);
           else atomicOr(word, kSeen);
@@ -369,9 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {  // out may be the logits, where a masked one is -infinity by now
       v[i] = i0 + i * kThreads < places ? table.tokens[i0 + i * kThreads] : -1;
-      const int at = max(v[i], 0);
-      y[i] = static_cast<float>(z[at]);
-      ok[i] = v[i] >= 0 && bit_set(mask, at);
+      ok[i] = v[i] >= 0;
+      if (!ok[i]) continue;
+      y[i] = static_cast<float>(z[v[i]]);
+      ok[i] = bit_set(mask, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -382,7 +389,21 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
     }
   }
   if (!a.token) return;
-  const unsigned long long named = block_largest<kWarps>(best_v < 0 ? 0 : key_of(best_z, best_v));
+  unsigned long long named = block_largest<kWarps>(best_v < 0 ? 0 : key_of(best_z, best_v));
+  if (tid == 0) cta_best = named;
+  if (split > 1) {
+    cluster.sync();
+    if (rank) {
+      cluster.sync();  // this CTA's table stays until it has been read
+      return;
+    }
+    for (int r = 1; r < split; ++r) named = larger(named, *cluster.map_shared_rank(&cta_best, r));
+  }
+  auto is_named = [&](int v) {
+    if (!places) return false;
+    const Table of{split > 1 ? cluster.map_shared_rank(table.tokens, owner(v)) : table.tokens, nullptr, table.mask};
+    return of.has(v);
+  };
   // The largest of the chunks' largest that is not a named token. A chunk is looked through again at most once.
   const int lead = lead_of(z, out, V);
   unsigned long long best = 0;
@@ -392,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
       const unsigned long long top = block_largest<kWarps>(mine);
       if (top <= larger(best, named)) break;
       const int v = token_of(top);
-      if (!places || !table.has(v)) {
+      if (!is_named(v)) {
         best = top;
         break;
       }
@@ -411,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const int u = u0 + i * kThreads;
-          if (ok[i] && y[i] > best_z && !table.has(u)) best_z = y[i], best_v = u;
+          if (ok[i] && y[i] > best_z && !is_named(u)) best_z = y[i], best_v = u;
         }
       }
       const unsigned long long again = block_largest<kWarps>(best_v < 0 ? 0 : key_of(best_z, best_v));
@@ -419,12 +440,13 @@ __global__ void __launch_bounds__(kThreads, 1) named_kernel(const __grid_constan
     }
   }
   if (tid == 0) a.token[row] = token_of(larger(best, named));
+  if (split > 1) cluster.sync();
 }
 
 // ---- host -------------------------------------------------------------------------------------------------------------
 struct Plan {
   bool clusters;
-  int places, chunk_bits, chunks;
+  int split, places, chunk_bits, chunks;
   size_t bytes;
 };
 
@@ -436,6 +458,9 @@ Plan plan(const mk_logit_controls_args& a, int sms) {
   if (p.clusters) return p;
   if (entries)
     for (p.places = 256; p.places / 4 * 3 < entries;) p.places *= 2;
+  // CTAs of a row's named tokens, while every cluster has SMs: 64 rows of 151936 fp32 logits, 8192 tokens of history 37.9 us with
+  // one, 32.7 with two; 2048: 24.6, 23.8; 256: 20.4, 20.9; 32 rows, 8192: 30.5, 24.9, 23.3 with four; 100 rows, 4096: 34.6, 43.7.
+  p.split = entries <= 1024 || a.rows * 2 > sms ? 1 : a.rows * 4 > sms ? 2 : 4;
   p.chunk_bits = a.dtype == MK_F32 ? kChunkBits : kChunkBits + 1;
   p.chunks = (a.vocab + (1 << p.chunk_bits) - 1) >> p.chunk_bits;
   p.bytes = sizeof(unsigned long long) * p.chunks * a.rows;
@@ -472,16 +497,19 @@ cudaError_t launch_pass(const mk_logit_controls_args& a, const Plan& p, int devi
   if (e != cudaSuccess || (!p.places && !a.token)) return e;
   if ((e = allow_smem<named_kernel<T>>(device, 8 * kPlaces)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.rows);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * p.split);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 8 * static_cast<size_t>(p.places);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = p.split;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, named_kernel<T>, a, p.places, p.chunk_bits, p.chunks, static_cast<const unsigned long long*>(largest));
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, named_kernel<T>, a, p.split, p.places, p.chunk_bits, p.chunks, static_cast<const unsigned long long*>(largest));
 }
 
 mk_status check_shape(const mk_logit_controls_args& a, const char* me, int device) {

@@ -719,7 +719,10 @@ CASES_LOGITS = [  # rows, vocab, history, biases, dtype, mask, row padding
     (1, 1, 3, 1, F32, True, 0), (2, 3, 5, 2, F32, True, 1), (3, 31, 8, 0, BF16, True, 0), (2, 33, 0, 3, F32, True, 2),
     (4, 1000, 64, 5, F32, True, 0), (3, 1001, 700, 17, BF16, True, 0), (5, 4097, 33, 0, F16, False, 3), (2, 32000, 2000, 300, F32, True, 4),
     (1, 151936, 5000, 40, F32, True, 0), (2, 163841, 300, 2047, BF16, True, 0), (1, 229121, 900, 9, F32, True, 1),
-    (1, 262145, 3000, 50, F16, True, 0), (2, 500001, 100, 5, BF16, False, 0), (700, 130, 9, 4, F32, True, 0), (40, 5003, 50, 0, F32, False, 0)]
+    (1, 262145, 3000, 50, F16, True, 0), (2, 500001, 100, 5, BF16, False, 0), (700, 130, 9, 4, F32, True, 0), (40, 5003, 50, 0, F32, False, 0),
+    # long histories of many rows: a row's named tokens over 4, 2 and 1 CTAs
+    (30, 5000, 3000, 20, F32, True, 0), (60, 9001, 1500, 2047, BF16, True, 1), (33, 40000, 12000, 40, F32, False, 0),
+    (90, 3001, 2000, 3, F16, True, 0)]
 
 
 def logit_inputs(rows, vocab, hist, biases, dtype, mask, pad, seed=0):
@@ -817,11 +820,12 @@ def test_logit_controls_special_values():
     check_controls(*many(z, kw))
 
 
-def test_logit_controls_largest_logits_are_in_the_history():
+@pytest.mark.parametrize("n, repeats", [(30, 1), (30, 6), (50, 6)])
+def test_logit_controls_largest_logits_are_in_the_history(n, repeats):
     """The chunks' largest logits are mostly named tokens, so that the join has to look for others."""
-    n, V = 30, 20011
+    V = 20011
     z = torch.randn(n, V, generator=gen(5), device=DEV)
-    top = z.topk(200, dim=1).indices.to(torch.int32)
+    top = z.topk(200, dim=1).indices.to(torch.int32).repeat(1, repeats)
     for pen in (1.0, 1.02, 5.0):
         kw = dict(history=top, total_len=i32([7 * i for i in range(n)]), frequency=torch.full((n,), pen, device=DEV))
         check_controls(z, kw)
