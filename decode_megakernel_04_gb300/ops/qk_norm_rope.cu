@@ -4,8 +4,10 @@
 // L = 8, 16 or 32 lanes, 8 elements a lane, so a warp works on 32 / L heads at a time. A lane of the rotated part holds
 // the 4 elements 4l.. and their partners 4l + rope_dim / 2.., so that the rotation needs no exchange; the other lanes
 // hold 8 elements in a row. The mean square is log2(L) shuffles. A warp loads the heads of kBatch rounds before it
-// works on the first (64 bytes a lane in flight); a token's angles are computed once per warp and token and serve
-// every head the warp has of it.
+// works on the first, and the next kBatch while it does (128 bytes a lane in flight; 63 us without, 51 with); a token's
+// angles are computed once per warp and token and serve every head the warp has of it.
+// Measured: 8190 tokens of 48 / 8 heads x 128 with the append, fp16: 51 us, 5.3 TB/s, 79 % of the measured copy rate,
+// bound by the instructions issued (66 % of the slots); one token 3.9 us.
 //
 // Angles: inv_freq / (2 pi) is turned into a 64-bit binary fraction of a turn; position x fraction mod 2^64 is then the
 // exact phase whatever the position, and its upper 32 bits (as a signed half-turn count) go to sincospif. An fp32
