@@ -124,11 +124,14 @@ struct Plan {
   size_t piece_at, ml_at, bytes;
 };
 
-// Small calls: a cluster of up to 16 CTAs per (request, kv head, row block) splits its keys evenly and joins through
-// distributed shared memory: no workspace, no second launch, no sums over the batch first. It does not balance ragged
-// requests against each other, so it is for calls whose CTAs are all resident and have at most this much to read each.
-// Measured both ways (one request, 48 / 8 heads x 128, bf16; time on the GPU, and the host's per call): 4096 positions
-// 10.9 us (10) as clusters, 15.0 (21) as pieces of the line; 8192 (256 KB a CTA) 18.0 and 18; 16384 (512 KB) 30 and 22.
+// Small calls: a cluster of up to 16 CTAs, all resident, per (request, kv head, row block) splits its keys evenly and
+// joins through distributed shared memory; where there are too many for two CTAs each, one CTA has it alone. No workspace,
+// no second launch, no sums over the batch first. It does not balance ragged requests against each other, so it is for
+// calls whose CTAs have at most this much to read each, twice that where they are more than fit at once.
+// Measured both ways (GPU us, and the host's per call), 128 wide, bf16. One request, 48 / 8 heads: 4096 positions 10.9 (10)
+// as clusters, 15.0 (21) as pieces of the line; 8192 (256 KB a CTA) 18.0 and 18; 16384 (512 KB) 30 and 22. One CTA each, 32
+// / 8 heads, 60 requests of 10 to 256 positions 18 and 36, to 700 (352 KB) 31 and 49, to 1500 (768 KB) 53 and 62; 150 of
+// these 103 and 133; 60 of 8 rows to 700 57 and 102; 256 wide to 700 (704 KB) 42 and 40.
 constexpr size_t kClusterBytes = 384 * 1024;
 
 mk_status check_shape(const mk_paged_attention_args& a, int device) {
@@ -172,7 +175,8 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
       if ((e = pl.build->clusters(device, parts, &resident)) != cudaSuccess) return e;
       if (items <= resident) break;
     }
-  if ((parts > 1 || key_tiles <= kMinTiles) && items * parts < 1 << 24 && (key_tiles + parts - 1) / parts * tile_bytes <= kClusterBytes) {
+  const size_t most = parts == 1 && items >= pl.ctas ? 2 * kClusterBytes : kClusterBytes;
+  if (items * parts < 1 << 24 && (key_tiles + parts - 1) / parts * tile_bytes <= most) {
     pl.parts = parts;
     pl.ctas = static_cast<int>(items) * parts;
     return cudaSuccess;

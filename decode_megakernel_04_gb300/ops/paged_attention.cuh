@@ -329,19 +329,28 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
   constexpr int kLoaders = S::kThreads & (S::kThreads - 1) ? 128 : S::kThreads;
   constexpr int kLoadRows = kLoaders / S::kChunks;
   static_assert(S::kTile % kLoadRows == 0, "whole rounds");
-  auto load = [&](int stage, int ring) {
+  // The first tile of a piece may be all there is (a short request), so only its keys that the products read (whole 32) are
+  // copied: 129 to 200 requests of a few keys 1.5 to 3.5 times faster. In the loop the second copy of the code costs 2 %.
+  auto load = [&](auto begins, int stage, int ring) {
     const Tile m = meta[ring];
     const uint32_t kd = s0 + S::kOffKV + stage * S::kStageBytes, vd = kd + S::kKeyBytes;
     if (kLoaders == S::kThreads || tid < kLoaders) {
       const int chunk = tid % S::kChunks, row0 = tid / S::kChunks;
       const bool in = chunk * 16 < a.head_dim * S::kElt;
       const unsigned char* const* at = addr + (ring * 2) * S::kTile + row0;
-#pragma unroll 8
-      for (int i = 0; i < S::kTile / kLoadRows; ++i) {
+      auto round = [&](int i) {
         const uint32_t to = place<S::kChunks>(row0 + i * kLoadRows, chunk);
         const unsigned char *k = at[i * kLoadRows], *v = at[S::kTile + i * kLoadRows];
         cp16(kd + to, in ? k + chunk * 16 : kZeros);
         cp16(vd + to, in ? v + chunk * 16 : kZeros);
+      };
+      const int rows = (m.len - m.key0 + 31) & ~31;
+      if (!decltype(begins)::value || rows >= S::kTile) {
+#pragma unroll 8
+        for (int i = 0; i < S::kTile / kLoadRows; ++i) round(i);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i * kLoadRows < rows; ++i) round(i);
       }
     }
     if (m.first) {
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) {
-    if (i < count) load(i, i);
+    if (i < count) load(std::bool_constant<!LONG>{}, i, i);
     cp_commit();
   }
 
@@ -430,7 +439,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
     if (d >= a.head_dim) return;
     const int mrow = block * S::kRows + row, r = p.group_div(mrow), h = head * p.group + mrow - r * p.group;
     const float f = sum == 0.0f ? 0.0f : (E4M3 ? a.v_scale[head] : 1.0f) / sum;
-    const uint2 u = a.dtype == MK_BF16
+    const uint2 u = (E4M3 ? a.dtype == MK_BF16 : std::is_same<T, __nv_bfloat16>::value)
                         ? make_uint2(pack2<__nv_bfloat16>(y.x * f, y.y * f), pack2<__nv_bfloat16>(y.z * f, y.w * f))
                         : make_uint2(pack2<__half>(y.x * f, y.y * f), pack2<__half>(y.z * f, y.w * f));
     uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2] + d;
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
     __syncthreads();  // tile j is there for every warp; tile j - 1's buffer and description are free
     {
       const int ahead = S::kStages - 1;
-      if (j + ahead < count) load((stage + ahead) % S::kStages, (ring + ahead) % S::kRing);
+      if (j + ahead < count) load(std::false_type{}, (stage + ahead) % S::kStages, (ring + ahead) % S::kRing);
       cp_commit();
     }
     const int next = look_up();
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
       }
     }
 
-    if (m.last && !p.parts) {  // the end of this CTA's part of the request
+    if (m.last && p.parts <= 1) {  // the end of this CTA's part of the request
       const long long slot = 2ll * blockIdx.x + m.slot;
       join_warps(reinterpret_cast<float*>(smem + S::kOffKV + stage * S::kStageBytes),
                  min(S::kRows, p.n_rows - m.block * S::kRows), [&](int row, int d, float4 y, float top, float sum) {
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
     ring = ring + 1 == S::kRing ? 0 : ring + 1;
   }
   cp_wait<0>();
-  if (!p.parts) return;
+  if (p.parts <= 1) return;
 
   // ---- a cluster's join: each CTA's rows in its own shared memory, then each CTA sums its share of the columns ------------
   cg::cluster_group cluster = cg::this_cluster();
