@@ -7,11 +7,11 @@
 // What bounds it: each cached byte is read once and meets rows x group query rows, 2 x rows x group flops a byte at 16
 // bits (6 to 96 for the models here) where the tensor cores' bound begins at 284. So the design keeps bytes in flight:
 // - Work: a tile is kTile keys of one (request, kv head, block of 16 MT rows). Small calls: a cluster of up to 16 CTAs
-//   shares the tiles of one and joins through distributed shared memory. Else all tiles of the call, request after
-//   request, are one line that is cut into equal pieces, one per resident CTA. A piece may begin and end inside a
-//   request; ragged lengths balance by themselves and nothing depends on the host knowing the lengths. A part of a
-//   request that a CTA did not cover alone goes to the workspace (at most two per CTA: its first and its last) and is
-//   joined by the second kernel.
+//   shares the tiles of one and joins through distributed shared memory, or one CTA has it alone. Else all tiles of the
+//   call, request after request, are one line that is cut into equal pieces, one per resident CTA. A piece may begin and
+//   end inside a request; ragged lengths balance by themselves and nothing depends on the host knowing the lengths. A
+//   part of a request that a CTA did not cover alone goes to the workspace (at most two per CTA: its first and its last)
+//   and is joined by the second kernel.
 // - Loads: cp.async in a ring of kStages tiles that runs on across requests, so the next request's keys (and its query
 //   rows, in a ring of their own) are in flight while the current one is finished. Page ids are looked up one tile
 //   further ahead; a key's address is made once, by one thread. Two stages and more CTAs on an SM measured faster
