@@ -23,6 +23,9 @@
 //   would cost as much accuracy as the final rounding; the second product costs 5 % of the time. e4m3 caches: keys and
 //   values become fp16 (exact) and the queries fp16 scaled per row by a power of two (bf16 mantissas fit; what falls under
 //   2^-24 of a row's largest is rounded); probabilities are one fp16 (2^-11), an eighth of a bf16 result's rounding.
+//   fp16 has few exponents, and many weak keys behind one strong key of a small value make the whole result: so fp16
+//   probabilities are taken against a base 15 under the running maximum (2^15 at it): off by 2^-11 (a pair: 2^-22) or by 2^-40
+//   of the largest. The sums are against the same base, which is what parts are joined by.
 // What bounds it now: warps x instructions in flight (IPC 1.8 of 4 at 12 warps on an SM); 64 requests of 1 to 16384
 // positions, 48 / 8 heads x 128, e4m3: 229 us, 70 % of the measured copy rate.
 #pragma once
@@ -128,11 +131,13 @@ __device__ inline float exp2_fast(float x) {
 }
 
 // ---- the shape of one build -----------------------------------------------------------------------------------------
-template <int DP, int MT, bool E4M3, bool LONG>
+template <typename T, int DP, int MT, bool E4M3, bool LONG>
 struct Shape {
   static constexpr int WM = MT, WK = MT == 1 ? 4 : 2, kWarps = WM * WK, kThreads = 32 * kWarps;
   static constexpr int kRows = 16 * MT;
   static constexpr int kElt = E4M3 ? 1 : 2;
+  // fp16 probabilities are 2^15 at the largest score, so that what falls under fp16's range is 2^-40 of it, not 2^-25
+  static constexpr float kLift = std::is_same<T, __half>::value ? 15.0f : 0.0f;
   static constexpr int kRowBytes = DP * kElt;         // of a key in shared memory
   static constexpr int kChunks = kRowBytes / 16;
   // 16 to 32 KB of keys and values a tile (64 KB at 256 wide and 16 rows, where four warps take 16 keys each)
@@ -181,9 +186,9 @@ __device__ inline uint32_t place(int row, int chunk) {  // byte offset of a 16-b
 }
 
 template <typename T, int DP, int MT, bool E4M3, bool LONG>
-__global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP, MT, E4M3, LONG>::kCtas)
+__global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<T, DP, MT, E4M3, LONG>::kCtas)
     attention_kernel(const __grid_constant__ Params p) {
-  using S = Shape<DP, MT, E4M3, LONG>;
+  using S = Shape<T, DP, MT, E4M3, LONG>;
   extern __shared__ __align__(128) unsigned char smem[];
   const mk_paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
   }
 
   float o[DP / 8][4];
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0, 0};
+  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0, 0};  // the base (largest score - kLift) and the sum against it
   uint32_t qf[DP / 16][4];
   float row_scale[2];
   int limit[2];
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (key + 8 * n + 2 * t4 + (i & 1) >= limit[i >> 1]) s[n][i] = -INFINITY;
-      float top[2] = {m_run[0], m_run[1]};
+      float top[2] = {S::kLift ? -INFINITY : m_run[0], S::kLift ? -INFINITY : m_run[1]};
 #pragma unroll
       for (int n = 0; n < S::kBlock / 8; ++n)
 #pragma unroll
@@ -571,6 +576,7 @@ __global__ void __launch_bounds__(Shape<DP, MT, E4M3, LONG>::kThreads, Shape<DP,
       for (int h = 0; h < 2; ++h) {
         top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
         top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
+        if (S::kLift) top[h] = fmaxf(m_run[h], __fadd_ru(top[h], -S::kLift));  // upwards: no more than 2^kLift
         base[h] = top[h] == -INFINITY ? 0.0f : top[h];
         grew |= top[h] > m_run[h];
       }
@@ -746,7 +752,7 @@ struct Build {
 
 template <typename T, int DP, int MT, bool E4M3, bool LONG = false>
 struct Make {
-  using S = Shape<DP, MT, E4M3, LONG>;
+  using S = Shape<T, DP, MT, E4M3, LONG>;
   static constexpr auto kKernel = attention_kernel<T, DP, MT, E4M3, LONG>;
   static cudaError_t occupancy(int device, int* n) {
     static std::atomic<int> known[kMaxDevices];

@@ -10,12 +10,12 @@
 //   scores  S [128 keys x R rows] = K Q^T         A = the tile's keys (K-major), B = the query rows
 //   sums    O [128 of D x 2 R] += V^T [P hi, P lo]  A = the tile's values as they lie (M-major), B = the probabilities
 // R = 8, 16, 32, 48 or 64 rows. Probabilities are 16-bit pairs hi + lo, side by side in one product (an instruction takes
-// about 50 cycles whatever its width, so two narrow ones cost twice); the halves are added at the end.
+// about 50 cycles whatever its width, so two narrow ones cost twice); the halves are added at the end (kLowScale).
 // Roles: warps 0-7 softmax (a thread is a key of the scores and one of the D of the sums; warps 0-3 have the first half
 // of the rows, 4-7 the second), warp 8 one thread that issues, warps 9-11 load keys and 12-14 values (cp.async, page by
 // page) into a ring of 32 KB slots, 128 keys x 128 wide each. The scores of the next tile are computed while this one's
 // probabilities are made (two score buffers).
-// The running maximum is the same for all threads of a row and grows only when a score passes it by 2^8 (in the
+// The running maximum is the same for all threads of a row and grows only when a score passes it by kGrow (in the
 // exponent's units): then the sums are rescaled in tensor memory; else nothing is exchanged but two votes per tile.
 // Code that runs once per request is kept short: it comes from memory every time (an unrolled end of a request took
 // 11 us).
@@ -232,6 +232,14 @@ struct TcShape {
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 constexpr float kNoBase = -3.402823466e38f;  // the lowest finite value: what a row's base begins with
+// fp16 has few exponents, and many weak keys behind one strong key of a small value make the whole result. So fp16
+// probabilities are taken against a base 7 under the maximum (up to 2^15 before the sums are rescaled) and the lower half
+// of a pair is 2^11 times what is left: off by 2^-22, or by 2^-43 of the largest.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+template <typename T>
+constexpr float kLowScale = std::is_same<T, __half>::value ? 2048.0f : 1.0f;
+constexpr float kGrow = 8.0f;  // a score above the maximum by this (in the exponent's units) moves the base
 constexpr int kTcMaxRows = 16;   // query rows of a request (of its block of new tokens)
 
 struct TcBars {
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
         }
       }
       bool waited = false;
-      if (any_of(1, S::kSoftmax, first || big > 8.0f)) {
+      if (any_of(1, S::kSoftmax, first || big > kLift<T> + kGrow)) {
 #pragma unroll
         for (int r = 0; r < RH; ++r) {
           const float x = warp_largest(s[r]);
@@ -578,7 +586,8 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
         named_sync(1, S::kSoftmax);
         if (tid < R) {
           const float old = first ? kNoBase : base_of[tid];
-          const float base = fmaxf(fmaxf(fmaxf(warp_max[tid], warp_max[64 + tid]), fmaxf(warp_max[128 + tid], warp_max[192 + tid])), old);
+          const float top = fmaxf(fmaxf(warp_max[tid], warp_max[64 + tid]), fmaxf(warp_max[128 + tid], warp_max[192 + tid]));
+          const float base = fmaxf(kLift<T> ? __fadd_ru(top, -kLift<T>) : top, old);  // upwards: the lift is no more than that
           base_of[tid] = base;
           shrink[tid] = exp2_fast(old - base);
         }
@@ -621,7 +630,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
           l[r] += x, l[r + 1] += y;
           hi[i] = pack2<T>(x, y);
           const float2 u = unpack2<T>(hi[i]);
-          lo[i] = pack2<T>(x - u.x, y - u.y);
+          lo[i] = pack2<T>((x - u.x) * kLowScale<T>, (y - u.y) * kLowScale<T>);
         }
         if (kAtOnce == 8) {
           *reinterpret_cast<uint4*>(column(r0 + c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -688,7 +697,7 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
           tc_ld(v, sums_at(h) + lanes + r0);
           tc_ld(u, sums_at(h) + lanes + R + r0);
 #pragma unroll
-          for (int r = 0; r < RH; ++r) v[r] += u[r];
+          for (int r = 0; r < RH; ++r) v[r] += u[r] * (1.0f / kLowScale<T>);
 #pragma unroll 2
           for (int x = 0; x < late_n; ++x) {
             const float value = late_at[x] ? static_cast<float>(late_at[x][h * 128 + t]) : 0.0f;

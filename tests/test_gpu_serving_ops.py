@@ -568,6 +568,43 @@ def test_attention_of_the_lowest_scores(width):
     check_rounded(got, out, BF16, "equal scores", (300 * 2.0 ** -23 + 2.0 ** -16) * av)
 
 
+def sink_inputs(lens, hq, hkv, d, dtype, cache, max_pages, seed=41):
+    """One key 14 to 18 above all the others of its request (natural units), with a value of zero: the result is what
+    the others' small probabilities give. It comes first, or in the middle."""
+    s = attention_inputs(lens, 1, hq, hkv, d, 16, dtype, cache, seed=seed, poison=False, max_pages=max_pages)
+    if cache is E4M3:
+        s["ks"].fill_(1.0), s["vs"].fill_(0.5)
+    s["q"].mul_(0.125)
+    s["q"][..., 0] = 4.0
+    s["k"][..., 0] = 0.0
+    s["v"].copy_((s["v"].float() * 0.25 + 1.0).to(cache))
+    for b, n in enumerate(lens):
+        p = n // 2 if b % 2 else 0
+        at = s["table"][b, p // 16].long()
+        s["k"][at, :, p % 16] = 0.0
+        s["k"][at, :, p % 16, 0] = 14.0 + b % 5
+        s["v"][at, :, p % 16] = 0.0
+    return s
+
+
+@pytest.mark.parametrize("lens, width", [([1500, 300, 1000, 700, 1301], None), ([4000] * 40 + [1300], 50000)], ids=["short", "long"])
+@pytest.mark.parametrize("dtype, cache, d", [(F16, F16, 64), (F16, F16, 128), (F16, F16, 256), (F16, E4M3, 64), (BF16, E4M3, 128),
+                                             (F16, E4M3, 128), (BF16, E4M3, 256), (BF16, BF16, 128)])
+def test_attention_of_many_weak_keys_behind_a_strong_one(dtype, cache, d, lens, width):
+    """Probabilities far below the largest count. The bound is check_attention's, without its absolute share for e4m3: a
+    probability is off by a relative 2^-16 (e4m3: 2^-11) or by 2^-40 of the largest one."""
+    s = sink_inputs(lens, 24, 8, d, dtype, cache, width)
+    got, lse = run_attention(s, scale=0.25)
+    out, l64, av, qk = attention_reference(s, 0.25)
+    n = s["lens"].double()[:, None, None]
+    e4 = cache is E4M3
+    ds = qk * ((d + 4) * 2.0 ** -23 + (2.0 ** -20 if e4 else 0))
+    rel = 2 * (ds + 2.0 ** -21 + n * 2.0 ** -23) + (2.0 ** -11 if e4 else 2.0 ** -16)
+    v_max = s["v"].float().abs().max().double() * (0.5 if e4 else 1.0)
+    check_rounded(got, out, dtype, "weak keys", rel[..., None] * av + (n * 2.0 ** -40)[..., None] * v_max)
+    assert ((lse.double() - l64).abs() <= ds + 2.0 ** -20 + n * 2.0 ** -23 + l64.abs() * 2.0 ** -22).all()
+
+
 def test_attention_lengths_and_pages_out_of_range():
     s = attention_inputs([40, 30, 20, 10], 1, 4, 2, 64, 8, BF16, BF16, seed=6, max_pages=5, poison=False)
     good, gl = run_attention(s)
