@@ -113,7 +113,7 @@ EXPORTS = ["mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host"
            "mk_fork_sequence", "mk_plan", "mk_set_wait_limit",
            "mk_set_routing_override", "mk_decode_steps", "mk_decode_steps_host", "mk_verify_step",
            "mk_packed_weight_bytes", "mk_pack_weights", "mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention",
-           "mk_paged_attention_workspace", "mk_logit_controls", "mk_logit_controls_workspace"]
+           "mk_paged_attention_workspace", "mk_logit_controls", "mk_logit_controls_workspace", "mk_logit_controls_check"]
 
 _lib = None
 
@@ -159,6 +159,8 @@ def load(path: str | None = None) -> C.CDLL:
     for f in ("mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention", "mk_logit_controls"):
         getattr(lib, f).argtypes = [_P, C.c_int, _P]
         getattr(lib, f).restype = C.c_int
+    lib.mk_logit_controls_check.argtypes = [_P, C.c_int]
+    lib.mk_logit_controls_check.restype = C.c_int
     for f in ("mk_paged_attention_workspace", "mk_logit_controls_workspace"):
         getattr(lib, f).argtypes = [_P, C.c_int, C.POINTER(C.c_uint64)]
         getattr(lib, f).restype = C.c_int
@@ -300,13 +302,14 @@ class Megakernel:
         in place on the same stream and argmax is the greedy token of what is left (-1: nothing is allowed)."""
         B, R = tokens.shape
         if controls is not None:
-            from .serving import _call, prepare_logit_controls
+            from .serving import _call, check_logit_controls, prepare_logit_controls
             z = None if logits is None else logits.view(-1, self.cfg.vocab)
             if z is None or z.shape[0] != B * R or z.get_device() != self.device:
                 raise ValueError("controls need logits [batch * rows, vocab] on the handle's device")
             # what does not fit is refused before the step, which cannot be taken back
             call, workspace = prepare_logit_controls(z, z, token=None if argmax is None else argmax.view(-1),
                                                      stream=stream or 0, **controls)
+            check_logit_controls(call)
             self._check(self.lib.mk_decode_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R, z.data_ptr(),
                                                  None, stream))
             _call(*call)

@@ -524,14 +524,8 @@ mk_status check_shape(const mk_logit_controls_args& a, const char* me, int devic
   return check_device(me, device);
 }
 
-}  // namespace
-}  // namespace mkop
-
-extern "C" mk_status mk_logit_controls(const mk_logit_controls_args* args, int device, void* stream) {
-  using namespace mkop;
-  static const char* me = "mk_logit_controls";
-  if (!args) return MK_ERR_INVALID_ARG;
-  const mk_logit_controls_args a = *args;
+// Everything that a call of at least one row can be refused for before the device is touched.
+mk_status check(const mk_logit_controls_args& a, const char* me, int device) {
   if (mk_status s = check_shape(a, me, device)) return s;
   if (a.rows == 0) return MK_OK;
   if (!a.logits || !a.out) return refuse(MK_ERR_INVALID_ARG, me, "a required pointer is NULL");
@@ -547,13 +541,45 @@ extern "C" mk_status mk_logit_controls(const mk_logit_controls_args* args, int d
       !aligned({a.out, a.token, a.history, a.prompt_len, a.total_len, a.repetition, a.presence, a.frequency, a.bias_ids, a.bias_vals,
                 a.allowed}, 4))
     return refuse(MK_ERR_INVALID_ARG, me, "a misaligned pointer");
-  DeviceGuard guard(device);
-  if (guard.err != cudaSuccess) return launched(me, guard.err);
+  return MK_OK;
+}
+
+// The plan on the current device `device`, and whether the workspace holds what it needs.
+mk_status plan_within(const mk_logit_controls_args& a, const char* me, int device, Plan* p) {
   int sms;
   if (const cudaError_t e = sm_count(device, &sms)) return launched(me, e);
-  const Plan p = plan(a, sms);
-  if (p.bytes && (!a.workspace || !aligned(a.workspace, 8) || a.workspace_bytes < static_cast<int64_t>(p.bytes)))
-    return refuse(MK_ERR_INVALID_ARG, me, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), p.bytes);
+  *p = plan(a, sms);
+  if (p->bytes && (!a.workspace || !aligned(a.workspace, 8) || a.workspace_bytes < static_cast<int64_t>(p->bytes)))
+    return refuse(MK_ERR_INVALID_ARG, me, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), p->bytes);
+  return MK_OK;
+}
+
+}  // namespace
+}  // namespace mkop
+
+extern "C" mk_status mk_logit_controls_check(const mk_logit_controls_args* args, int device) {
+  using namespace mkop;
+  static const char* me = "mk_logit_controls_check";
+  if (!args) return MK_ERR_INVALID_ARG;
+  if (mk_status s = check(*args, me, device)) return s;
+  if (args->rows == 0) return MK_OK;
+  DeviceGuard guard(device);
+  if (guard.err != cudaSuccess) return launched(me, guard.err);
+  Plan p;
+  return plan_within(*args, me, device, &p);
+}
+
+extern "C" mk_status mk_logit_controls(const mk_logit_controls_args* args, int device, void* stream) {
+  using namespace mkop;
+  static const char* me = "mk_logit_controls";
+  if (!args) return MK_ERR_INVALID_ARG;
+  const mk_logit_controls_args a = *args;
+  if (mk_status s = check(a, me, device)) return s;
+  if (a.rows == 0) return MK_OK;
+  DeviceGuard guard(device);
+  if (guard.err != cudaSuccess) return launched(me, guard.err);
+  Plan p;
+  if (mk_status s = plan_within(a, me, device, &p)) return s;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p.clusters)
     return launched(me, a.dtype == MK_F32 ? launch_clusters<float>(a, device, s)

@@ -257,7 +257,7 @@ def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None
 def prepare_logit_controls(logits, out, history=None, prompt_len=None, total_len=None, repetition=None, presence=None,
                            frequency=None, bias_ids=None, bias_vals=None, allowed=None, token=None, workspace=None,
                            stream=None):
-    """logit_controls' checks without its launch: (_call's arguments, the workspace, to be kept until the call)."""
+    """logit_controls' marshalling without its launch: (_call's arguments, the workspace, to be kept until the call)."""
     dev = logits.get_device()
     _need(dev >= 0 and logits.dim() == 2, "logit_controls needs logits [rows, vocab] on a CUDA device")
     n, vocab = logits.shape
@@ -285,3 +285,11 @@ def prepare_logit_controls(logits, out, history=None, prompt_len=None, total_len
     if workspace is not None:
         packed = _pack_logits(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), workspace.numel(), *tail)
     return (load().mk_logit_controls, packed, dev, stream, "logit_controls"), workspace
+
+
+def check_logit_controls(call) -> None:
+    """Raises what the library would refuse of a prepared call, without enqueueing it."""
+    _, packed, dev, _, what = call
+    rc = load().mk_logit_controls_check(packed, dev)
+    if rc != MK_OK:
+        raise MKError(rc, f"{what} (details on stderr)")

@@ -587,6 +587,10 @@ mk_status mk_logit_controls(const mk_logit_controls_args* args, int device, void
  * NULL). Which pointers are NULL and the sizes decide; nothing is read through a pointer. */
 mk_status mk_logit_controls_workspace(const mk_logit_controls_args* args, int device, uint64_t* bytes);
 
+/* What mk_logit_controls would return for these arguments, short of enqueueing anything: every host-side argument error,
+ * the workspace's among them. For callers that must know before they enqueue the step whose logits are controlled. */
+mk_status mk_logit_controls_check(const mk_logit_controls_args* args, int device);
+
 #ifdef __cplusplus
 }
 #endif

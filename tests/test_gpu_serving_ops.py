@@ -1049,3 +1049,36 @@ def test_step_with_controls():
         mks[1].step(tok, pos, None, am, controls=kw)
     for m in mks:
         m.close()
+
+
+def stepless():
+    """A Megakernel of 2 sequences and 8 tokens of vocabulary whose step must not run, and its tokens and positions."""
+    from decode_megakernel_04_gb300 import binding
+
+    class Lib:
+        def mk_decode_step(self, *args):
+            raise AssertionError("the step ran")
+
+    m = binding.Megakernel.__new__(binding.Megakernel)
+    m.lib, m.device, m.h = Lib(), 0, None
+    m.cfg = type("Cfg", (), {"vocab": 8})
+    return m, i32([[1], [2]]), i32([0, 0])
+
+
+def test_controls_that_the_library_refuses_are_refused_before_the_step():
+    """Strides, alignment, list lengths and the workspace: what only the library checks."""
+    from decode_megakernel_04_gb300 import MKError
+    m, tok, pos = stepless()
+    z = torch.zeros(2, 8, device=DEV)
+    ids = i32([[1, 2]] * 2)
+    pen = torch.ones(2, device=DEV)
+    spare = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    many = torch.zeros(400, 8, device=DEV)
+    for kw in (dict(allowed=i32([[-1]]).expand(2, -1)), dict(history=i32([[1, 2]]).expand(2, -1), repetition=pen),
+               dict(bias_ids=ids.repeat(1, 1024), bias_vals=torch.zeros(2, 2048, device=DEV), workspace=spare)):
+        with pytest.raises(MKError):
+            m.step(tok, pos, z, controls=kw)
+    # many rows need a workspace: one that is too short, and one that is not aligned
+    for ws in (spare[:8], spare[1:]):
+        with pytest.raises(MKError):
+            m.step(i32([[1]] * 400), i32([0] * 400), many, controls=dict(bias_ids=i32([[1]] * 400), bias_vals=torch.zeros(400, 1, device=DEV), workspace=ws))

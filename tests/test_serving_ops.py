@@ -179,6 +179,17 @@ def test_controls_that_do_not_fit_are_refused_before_the_step():
             m.step(tok, tok[:, 0], z, controls=dict(bias_ids=tok))
 
 
+@pytest.mark.parametrize("code, change", [(c, k) for n, m, c, ks in REFUSALS if n == "mk_logit_controls" for k in ks])
+def test_logit_controls_check_refuses_what_the_call_refuses(lib, code, change):
+    assert lib.mk_logit_controls_check(C.byref(logits(**change)), 0) == code
+
+
+def test_logit_controls_check_without_rows_arguments_or_a_device(lib):
+    fn = lib.mk_logit_controls_check
+    assert fn(None, 0) == BAD and fn(C.byref(logits()), -1) == BAD and fn(C.byref(logits()), 64) == BAD
+    assert fn(C.byref(logits(rows=0)), 0) == 0
+
+
 def test_wrappers_refuse_cpu_tensors():
     i = torch.zeros(2, dtype=torch.int32)
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
