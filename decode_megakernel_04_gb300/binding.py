@@ -304,8 +304,9 @@ class Megakernel:
         if controls is not None:
             from .serving import _call, check_logit_controls, prepare_logit_controls
             z = None if logits is None else logits.view(-1, self.cfg.vocab)
-            if z is None or z.shape[0] != B * R or z.get_device() != self.device:
-                raise ValueError("controls need logits [batch * rows, vocab] on the handle's device")
+            # (the step writes its rows one after the other)
+            if z is None or z.shape[0] != B * R or z.get_device() != self.device or not z.is_contiguous():
+                raise ValueError("controls need contiguous logits [batch * rows, vocab] on the handle's device")
             # what does not fit is refused before the step, which cannot be taken back
             call, workspace = prepare_logit_controls(z, z, token=None if argmax is None else argmax.view(-1),
                                                      stream=stream or 0, **controls)

@@ -1082,3 +1082,12 @@ def test_controls_that_the_library_refuses_are_refused_before_the_step():
     for ws in (spare[:8], spare[1:]):
         with pytest.raises(MKError):
             m.step(i32([[1]] * 400), i32([0] * 400), many, controls=dict(bias_ids=i32([[1]] * 400), bias_vals=torch.zeros(400, 1, device=DEV), workspace=ws))
+
+
+def test_controls_refuse_logits_with_gaps_between_rows():
+    """The step writes contiguous rows, so controls at another row stride would work on the wrong values."""
+    m, tok, pos = stepless()
+    for z in (torch.zeros(2, 12, device=DEV)[:, :8], torch.zeros(4, 8, device=DEV)[::2], torch.zeros(2, 1, 9, device=DEV)[..., :8],
+              torch.zeros(1, 8, device=DEV).expand(2, 8)):
+        with pytest.raises(ValueError):
+            m.step(tok, pos, z, controls=dict(bias_ids=i32([[1], [2]]), bias_vals=torch.ones(2, 1, device=DEV)))
