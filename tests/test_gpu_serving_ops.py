@@ -279,6 +279,59 @@ def test_qk_norm_rope(case):
         check_rounded(flat[s["slots"][keep]], want[keep], cache, "cache", slack[keep])
 
 
+@pytest.mark.parametrize("case", [c for c in CASES_QK if c[6] is not None], ids=str)
+def test_qk_cached_values_are_exact(case):
+    """Values are not normed or turned: a 16-bit cache holds them bit for bit, an e4m3 cache the code of the fp32 quotient."""
+    from decode_megakernel_04_gb300 import qk_norm_rope
+    n, hq, hkv, d, rope, dtype, cache, page, gains = case
+    s = qk_inputs(*case, seed=1)
+    qk_norm_rope(s["q"], s["k"], s["pos"], s["inv"], torch.empty(n, hq, d, dtype=dtype, device=DEV), q_gain=s["qg"], k_gain=s["kg"],
+                 v=s["v"], k_pages=s["pages"][0], v_pages=s["pages"][1], slots=s["slots"], k_scale=s["scales"][0], v_scale=s["scales"][1])
+    keep = (s["slots"] >= 0).cpu()
+    got = s["pages"][1].float().cpu().transpose(1, 2).reshape(-1, hkv, d)[s["slots"].cpu()[keep]]
+    want = s["v"].float().cpu()[keep]
+    if cache is E4M3:
+        want = (want / s["scales"][1].cpu()[:, None]).clamp(-448, 448).to(E4M3).float()
+    assert torch.equal(got, want)
+
+
+def test_qk_e4m3_values_halfway_between_two_codes():
+    """value / scale exactly between two e4m3 codes goes to the even one. (17 .. 31) / 16 x 2^e are such, for odd numerators,
+    and their products with 3, 5 and 7 are bf16 values."""
+    from decode_megakernel_04_gb300 import qk_norm_rope
+    half = torch.tensor([(m if e % 2 else -m) / 16 * 2.0 ** e for e in range(-5, 8) for m in range(17, 32, 2)])
+    n, hkv, d = -(-half.numel() // 16), 3, 16
+    half = torch.cat([half, half.new_ones(n * d - half.numel())]).view(n, 1, d)
+    scale = torch.tensor([3.0, 5.0, 7.0]) / 64
+    v = (half * scale[:, None]).to(BF16)
+    assert torch.equal(v.double(), half.double() * scale.double()[:, None])
+    kp, vp = (torch.zeros(n, hkv, 1, d, device=DEV).to(E4M3) for _ in range(2))
+    q = torch.zeros(n, 1, d, dtype=BF16, device=DEV)
+    qk_norm_rope(q, v.to(DEV), None, None, q, v=v.to(DEV), k_pages=kp, v_pages=vp, slots=torch.arange(n, device=DEV),
+                 k_scale=scale.to(DEV), v_scale=scale.to(DEV))
+    want = half.expand(n, hkv, d).to(E4M3).float()
+    for got in (kp, vp):  # (without norm and rotation keys are stored as they come too)
+        assert torch.equal(got[:, :, 0].float().cpu(), want)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-44, 3e-5, 0.7, 1e25, -2.0])
+def test_qk_e4m3_scales_and_values_of_any_size(scale):
+    """Quotients of every size: past 448 (infinite ones too) 448, NaN NaN, down to 0; scales that fp32 has no reciprocal of."""
+    from decode_megakernel_04_gb300 import qk_norm_rope
+    x = torch.tensor([0.0, -0.0, 1.0, -1.0, 447.0, 448.0, 463.0, 465.0, -480.0, 511.0, 512.0, 1e4, 3e38, float("inf"), float("-inf"),
+                      float("nan"), 2.0 ** -6, 2.0 ** -9, 2.0 ** -10, 1.5 * 2.0 ** -10, 2.0 ** -11, 1e-20, 1e-38, 1e-40])
+    x = torch.cat([x, x * 0.3, x * 1e-3, x * scale, x * scale * 0.7, (x.double() * scale * 1.1).float()]).to(BF16)
+    n, d = x.numel() // 16, 16
+    v = x.view(n, 1, d)
+    kp, vp = (torch.zeros(n, 1, 1, d, device=DEV).to(E4M3) for _ in range(2))
+    q, sc = torch.zeros(n, 1, d, dtype=BF16, device=DEV), torch.tensor([scale])
+    qk_norm_rope(q, v.to(DEV), None, None, q, v=v.to(DEV), k_pages=kp, v_pages=vp, slots=torch.arange(n, device=DEV),
+                 k_scale=sc.to(DEV), v_scale=sc.to(DEV))
+    want = (v.float() / sc[:, None]).clamp(-448, 448).to(E4M3).float()
+    for got in (kp, vp):
+        assert torch.equal(got[:, :, 0].float().cpu().nan_to_num(1000.0), want.nan_to_num(1000.0))
+
+
 def test_qk_in_place_and_streams():
     from decode_megakernel_04_gb300 import qk_norm_rope
     s = qk_inputs(300, 24, 4, 128, 128, BF16, None, 1, True)
