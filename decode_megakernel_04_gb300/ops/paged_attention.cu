@@ -121,8 +121,20 @@ const char* const kMe = "mk_paged_attention";
 struct Plan {
   const Build* build;
   int dp, group, n_rows, blocks, ctas, parts;
-  size_t piece_at, ml_at, bytes;
+  size_t piece_at, ml_at;
+  size_t bytes;   // what this call uses
+  size_t offer;   // what mk_paged_attention_workspace says: `bytes` or more, so that the largest call's fits smaller ones
 };
+
+// The line's grid and workspace with a build.
+size_t lay_out(Plan& pl, const Build* build, int sms, int per_sm) {
+  pl.build = build;
+  pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+  const size_t slots = 2 * static_cast<size_t>(pl.ctas);
+  pl.ml_at = slots * build->rows * pl.dp * sizeof(float);
+  pl.piece_at = pl.ml_at + slots * build->rows * sizeof(float2);
+  return pl.piece_at + pl.ctas * sizeof(Piece);
+}
 
 // Small calls: a cluster of up to 16 CTAs, all resident, per (request, kv head, row block) splits its keys evenly and
 // joins through distributed shared memory; where there are too many for two CTAs each, one CTA has it alone. No workspace,
@@ -164,7 +176,7 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
   if (e != cudaSuccess) return e;
   pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
   pl.parts = 0;
-  pl.ml_at = pl.piece_at = pl.bytes = 0;
+  pl.ml_at = pl.piece_at = pl.bytes = pl.offer = 0;
   const int64_t items = static_cast<int64_t>(a.batch) * a.n_kv_heads * pl.blocks;
   const int64_t key_tiles = (static_cast<int64_t>(a.max_pages) * a.page_size + pl.build->tile - 1) / pl.build->tile;
   const size_t tile_bytes = 2 * static_cast<size_t>(pl.build->tile) * pl.dp * (a.cache_dtype == MK_E4M3 ? 1 : 2);
@@ -175,26 +187,32 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
       if ((e = pl.build->clusters(device, parts, &resident)) != cudaSuccess) return e;
       if (items <= resident) break;
     }
+  const size_t each = static_cast<size_t>((key_tiles + parts - 1) / parts) * tile_bytes;  // a CTA's keys and values
   const size_t most = parts == 1 && items >= pl.ctas ? 2 * kClusterBytes : kClusterBytes;
-  if (items * parts < 1 << 24 && (key_tiles + parts - 1) / parts * tile_bytes <= most) {
-    pl.parts = parts;
-    pl.ctas = static_cast<int>(items) * parts;
-    return cudaSuccess;
+  const bool small = items * parts < 1 << 24 && each <= most;
+  if (!small || each > kClusterBytes) {  // the line, or a batch that would be one with fewer requests
+    Plan line = pl;
+    const Build* build = pick(true);
+    if ((e = build->occupancy(device, &per_sm)) != cudaSuccess) return e;
+    pl.offer = line.bytes = lay_out(line, build, sms, per_sm);
+    if (a.cache_dtype != MK_E4M3 && (a.head_dim == 128 || a.head_dim == 256) && a.rows <= kTcMaxRows) {
+      const int block_rows = pl.blocks == 1 ? pl.n_rows : 16 * mt;
+      build = a.dtype == MK_BF16 ? pick_tc_bf16(pl.dp, block_rows) : pick_tc_f16(pl.dp, block_rows);
+      if ((e = build->occupancy(device, &per_sm)) != cudaSuccess) return e;
+      Plan tc = pl;
+      tc.bytes = lay_out(tc, build, sms, per_sm);
+      pl.offer = tc.bytes > line.bytes ? tc.bytes : line.bytes;
+      // (its CTAs count their tiles in 32 bits)
+      if (items * ((static_cast<int64_t>(a.max_pages) * a.page_size >> 7) + 1) < INT32_MAX) line = tc;
+    }
+    if (!small) {
+      line.offer = pl.offer;
+      pl = line;
+      return cudaSuccess;
+    }
   }
-  // (its CTAs count their tiles in 32 bits)
-  if (items * ((static_cast<int64_t>(a.max_pages) * a.page_size >> 7) + 1) < INT32_MAX &&
-      a.cache_dtype != MK_E4M3 && (a.head_dim == 128 || a.head_dim == 256) && a.rows <= kTcMaxRows) {
-    const int block_rows = pl.blocks == 1 ? pl.n_rows : 16 * mt;
-    pl.build = a.dtype == MK_BF16 ? pick_tc_bf16(pl.dp, block_rows) : pick_tc_f16(pl.dp, block_rows);
-  } else {
-    pl.build = pick(true);
-  }
-  if ((e = pl.build->occupancy(device, &per_sm)) != cudaSuccess) return e;
-  pl.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
-  const size_t slots = 2 * static_cast<size_t>(pl.ctas);
-  pl.ml_at = slots * pl.build->rows * pl.dp * sizeof(float);
-  pl.piece_at = pl.ml_at + slots * pl.build->rows * sizeof(float2);
-  pl.bytes = pl.piece_at + pl.ctas * sizeof(Piece);
+  pl.parts = parts;
+  pl.ctas = static_cast<int>(items) * parts;
   return cudaSuccess;
 }
 
@@ -228,7 +246,7 @@ extern "C" mk_status mk_paged_attention_workspace(const mk_paged_attention_args*
   if (guard.err != cudaSuccess) return launched(kMe, guard.err);
   Plan pl;
   if (const cudaError_t e = plan(*p, device, &pl)) return launched(kMe, e);
-  *bytes = pl.bytes;
+  *bytes = pl.offer;
   return MK_OK;
 }
 

@@ -749,6 +749,38 @@ def test_attention_in_graphs_and_on_streams(width):
     assert torch.equal(got[0], want[0][0])
 
 
+@pytest.mark.parametrize("rows, hq, hkv, d, dtype, cache", [
+    (1, 32, 8, 128, 0, 0), (8, 48, 8, 128, 0, 0), (1, 24, 4, 256, 1, 1), (1, 32, 8, 64, 0, 0), (1, 48, 8, 128, 0, 3), (1, 2, 1, 128, 1, 1), (17, 4, 2, 256, 0, 0)])
+def test_attention_workspace_of_the_largest_call_fits_all(rows, hq, hkv, d, dtype, cache):
+    """0 or one size for the heads, rows and types; more requests or a wider table never need less."""
+    import ctypes as C
+
+    from decode_megakernel_04_gb300 import binding
+    lib = binding.load()
+
+    def size(batch, pages):
+        a = binding.PagedAttentionArgs(batch=batch, rows=rows, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, n_pages=1 << 20,
+                                       page_size=16, max_pages=pages, dtype=dtype, cache_dtype=cache)
+        n = C.c_uint64(0)
+        assert lib.mk_paged_attention_workspace(C.byref(a), 0, C.byref(n)) == 0
+        return n.value
+
+    got = np.array([[size(b, w) for w in (1, 4, 16, 32, 60, 94, 128, 300, 5000, 1 << 20, (1 << 27) - 64)]
+                    for b in (1, 2, 7, 16, 30, 40, 60, 150, 400, 5000, 1 << 20)], np.int64)
+    assert len(np.unique(got[got > 0])) == 1
+    assert (np.diff(got, axis=0) >= 0).all() and (np.diff(got, axis=1) >= 0).all()
+
+
+def test_attention_of_fewer_requests_in_the_largest_calls_workspace():
+    from decode_megakernel_04_gb300 import paged_attention_workspace
+    s = attention_inputs([7 + 10 * i for i in range(150)], 1, 32, 8, 128, 16, BF16, BF16, seed=13, poison=False)
+    ws = torch.empty(paged_attention_workspace(s["q"], s["k"], s["table"]), dtype=torch.uint8, device=DEV)
+    for n in (150, 60, 40, 30, 22, 5, 1):
+        t = dict(s, q=s["q"][-n:], table=s["table"][-n:], lens=s["lens"][-n:].contiguous())
+        got, lse = run_attention(t, workspace=ws)
+        check_attention(t, got, lse, 128 ** -0.5)
+
+
 def test_attention_refuses():
     from decode_megakernel_04_gb300 import MKError, paged_attention
     s = attention_inputs([20], 1, 4, 2, 64, 16, BF16, BF16)
