@@ -194,12 +194,12 @@ def _workspace_size(fn, packed, dev, what) -> int:
 
 def _workspace(size, device, dev, stream):
     """Scratch for one call, from torch's allocator (inside a graph capture: from the graph's pool)."""
-    workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    if stream is not None and stream != _raw_stream(dev):
-        # torch may hand this memory out again on its own stream while the call still runs on the other
-        workspace.record_stream(torch.cuda.ExternalStream(stream, device=device) if stream else
-                                torch.cuda.default_stream(device))
-    return workspace
+    if stream is None or stream == _raw_stream(dev):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    # The memory has to be the other stream's: what torch has free for its current stream may be in use there until the work
+    # enqueued on it so far has run, and nothing orders the two.
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)):
+        return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def paged_attention_workspace(q, k_pages, table) -> int:

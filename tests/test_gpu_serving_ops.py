@@ -797,6 +797,34 @@ def test_attention_refuses():
             paged_attention(**{**ok, **change})
 
 
+def test_workspaces_for_another_stream_are_not_the_current_streams_memory():
+    """What torch holds free for the current stream may still be read and written by work enqueued there."""
+    from decode_megakernel_04_gb300 import serving
+    size = 3 << 20
+    dev = torch.device(DEV, 0)
+    side = torch.cuda.Stream()
+
+    def fresh(current, stream):
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(current):
+            x = torch.empty(size, dtype=torch.uint8, device=dev)
+            at = x.data_ptr()
+            del x  # free for `current` from here on
+            w = serving._workspace(size, dev, 0, stream)
+            same = w.data_ptr() == at
+            del w
+            return not same, serving._workspace(size, dev, 0, stream).data_ptr()
+
+    main = torch.cuda.default_stream()
+    for current, stream in ((main, side.cuda_stream), (side, 0)):
+        own, at = fresh(current, stream)
+        assert own
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if stream else main):  # it goes back to its stream
+            assert torch.empty(size, dtype=torch.uint8, device=dev).data_ptr() == at
+    for current, stream in ((main, 0), (main, None), (side, side.cuda_stream), (side, None)):
+        assert not fresh(current, stream)[0]
+
+
 # ---- logit controls ---------------------------------------------------------------------------------------------------
 
 def controls_reference(z, history, prompt, total, rep, pres, freq, ids, vals, allowed):
