@@ -492,8 +492,7 @@ cudaError_t launch_clusters(const mk_logit_controls_args& a, int device, cudaStr
 template <typename T>
 cudaError_t launch_pass(const mk_logit_controls_args& a, const Plan& p, int device, cudaStream_t s) {
   unsigned long long* largest = static_cast<unsigned long long*>(a.workspace);
-  pass_kernel<T><<<static_cast<unsigned>(a.rows) * p.chunks, kPassThreads, 0, s>>>(a, p.chunk_bits, p.chunks, largest);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = start(pass_kernel<T>, static_cast<unsigned>(a.rows) * p.chunks, kPassThreads, 0, s, a, p.chunk_bits, p.chunks, largest);
   if (e != cudaSuccess || (!p.places && !a.token)) return e;
   if ((e = allow_smem<named_kernel<T>>(device, 8 * kPlaces)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <initializer_list>
+#include <utility>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -79,8 +80,22 @@ inline mk_status check_device(const char* call, int device) {
   return device < 0 || device >= kMaxDevices ? refuse(MK_ERR_INVALID_ARG, call, "device %d", device) : MK_OK;
 }
 
+// What the call returns. An error does not stay behind as the runtime's last one, which a later call would take for its own.
 inline mk_status launched(const char* call, cudaError_t e) {
-  return e == cudaSuccess ? MK_OK : refuse(MK_ERR_CUDA, call, "%s", cudaGetErrorString(e));
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  return refuse(MK_ERR_CUDA, call, "%s", cudaGetErrorString(e));
+}
+
+// A plain launch. Its status is that of this launch, not of what an earlier call left behind.
+template <typename... Params, typename... Args>
+cudaError_t start(void (*kernel)(Params...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // n / d for 0 <= n < 2^31 by a product: with 2^(k-1) < d <= 2^k, mul = floor(2^(31+k) / d) + 1 is off by at most 1 from

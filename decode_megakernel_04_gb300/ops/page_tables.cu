@@ -227,11 +227,7 @@ extern "C" mk_status mk_page_tables(const mk_page_tables_args* p, int device, vo
   in_place |= overlap(a.lens, a.batch, a.ring_state, 2) || overlap(a.starts, a.batch + 1, a.ring_state, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool split = in_place && ctas > 1;
-  page_tables_kernel<<<ctas, kThreads, smem, s>>>(a, true, !split);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && split) {
-    page_tables_kernel<<<1, kThreads, smem, s>>>(a, false, true);
-    e = cudaGetLastError();
-  }
+  cudaError_t e = start(page_tables_kernel, ctas, kThreads, smem, s, a, true, !split);
+  if (e == cudaSuccess && split) e = start(page_tables_kernel, 1, kThreads, smem, s, a, false, true);
   return launched(me, e);
 }

@@ -739,8 +739,7 @@ struct TcMake {
     return allow_smem<kKernel>(device, S::kSmem);
   }
   static cudaError_t launch(const Params& p, cudaStream_t s) {
-    kKernel<<<p.ctas, S::kThreads, S::kSmem, s>>>(p);
-    return cudaGetLastError();
+    return start(kKernel, p.ctas, S::kThreads, S::kSmem, s, p);
   }
   static constexpr Build build() { return {R, S::kTile, occupancy, nullptr, launch}; }
 };

@@ -209,9 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) qk_kernel(const __grid_con
 
 template <typename T, int L>
 cudaError_t launch(const Work& w, bool e4m3, int grid, cudaStream_t s) {
-  if (e4m3) qk_kernel<T, L, true><<<grid, kWarps * 32, 0, s>>>(w);
-  else qk_kernel<T, L, false><<<grid, kWarps * 32, 0, s>>>(w);
-  return cudaGetLastError();
+  return start(e4m3 ? qk_kernel<T, L, true> : qk_kernel<T, L, false>, grid, kWarps * 32, 0, s, w);
 }
 
 template <typename T>

@@ -1204,3 +1204,34 @@ def test_controls_refuse_logits_with_gaps_between_rows():
               torch.zeros(1, 8, device=DEV).expand(2, 8)):
         with pytest.raises(ValueError):
             m.step(tok, pos, z, controls=dict(bias_ids=i32([[1], [2]]), bias_vals=torch.ones(2, 1, device=DEV)))
+
+
+def test_a_failed_call_leaves_nothing_for_the_next_one():
+    """A device that is not there is an error of that call alone: the operators and the step after it succeed."""
+    import ctypes as C
+
+    from decode_megakernel_04_gb300 import Megakernel, binding, logit_controls, page_tables, paged_attention, qk_norm_rope
+    from synthetic import config, make_tokens, make_weights
+    lib = binding.load()
+    cfg = config("tiny_dense")
+    m = Megakernel(cfg, make_weights(cfg, seed=5, device=torch.device(DEV)), max_batch=1, max_rows=8, max_ctx=64)
+    m.prefill(make_tokens(5, "ctx", (1, 20), cfg.vocab, device=DEV).contiguous())
+    tok, z = make_tokens(5, "t", (1, 1), cfg.vocab, device=DEV).contiguous(), torch.empty(1, cfg.vocab, device=DEV)
+    few, many = torch.zeros(2, 50, device=DEV), torch.zeros(500, 50, device=DEV)
+    s = attention_inputs([40, 30], 1, 4, 2, 128, 16, BF16, BF16, seed=6, poison=False)
+    wide = dict(s, table=s["table"].repeat(1, 4000))
+    out = torch.empty_like(s["q"].contiguous())
+    x = torch.zeros(3, 2, 64, dtype=BF16, device=DEV)
+    t = i32([[0, -1], [1, -1]])
+    args = binding.LogitControlsArgs(logits=few.data_ptr(), out=few.data_ptr(), logits_stride=50, out_stride=50, rows=2, vocab=50, dtype=2)
+    calls = [lambda: page_tables(t, i32([4, 2]), i32([4, 2]), i32([0, 0]), i32([2, 3, 0, 0]), i32([0, 2]), 4, 4, slots=torch.empty(3, dtype=torch.int64, device=DEV)),
+             lambda: qk_norm_rope(x, x, None, None, x), lambda: logit_controls(few, few), lambda: logit_controls(many, many),
+             lambda: paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], out),
+             lambda: paged_attention(wide["q"], wide["k"], wide["v"], wide["table"], wide["lens"], out), lambda: m.step(tok, i32([20]), z)]
+    for call in calls:
+        call()
+        assert lib.mk_logit_controls(C.byref(args), 63, None) == 4  # MK_ERR_CUDA
+        call()
+    torch.cuda.synchronize()
+    assert m.status() == 0
+    m.close()
