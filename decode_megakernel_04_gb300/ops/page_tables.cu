@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const __grid_cons
   const int step = gridDim.x * kThreads, id = blockIdx.x * kThreads + tid;
   state = state && blockIdx.x == 0;
   if (why) {  // the same decision in every CTA
-    for (int t = id; tokens && t < a.n_tokens; t += step) {
+    for (unsigned t = id; tokens && t < static_cast<unsigned>(a.n_tokens); t += step) {  // (t + step passes 2^31)
       a.slots[t] = -1;
       if (a.positions) a.positions[t] = 0;
       if (a.owners) a.owners[t] = -1;
@@ -217,7 +217,7 @@ extern "C" mk_status mk_page_tables(const mk_page_tables_args* p, int device, vo
   int sms;
   if (const cudaError_t e = sm_count(device, &sms)) return launched(me, e);
   // One CTA up to 1024 places (two tokens a thread): a second CTA would gain less than the second launch in place costs.
-  const int want = a.n_tokens <= 2 * kThreads ? 1 : (a.n_tokens + kThreads - 1) / kThreads;
+  const int want = a.n_tokens <= 2 * kThreads ? 1 : a.n_tokens / kThreads + 1;
   const int ctas = want < 2 * sms ? want : 2 * sms;
   bool in_place = overlap(a.ring_state_out, 2, a.ring_state, 2);
   for (const int32_t* in : {a.held, a.start, a.count}) {

@@ -102,6 +102,7 @@ def page_tables(table, held, start, count, ring, ring_state, page_size: int, n_p
     n = held.numel()
     tp, ts, max_pages = _rows(table, _I32, n, dev, "table")
     places = slots.numel()
+    _need(places < 2 ** 31 and ring.numel() < 2 ** 31, "slots and ring have less than 2^31 entries")
     packed = _pack_tables(
         tp, ts, _vector(held, _I32, n, dev, "held"), _vector(start, _I32, n, dev, "start"),
         _vector(count, _I32, n, dev, "count"), _vector(ring, _I32, None, dev, "ring"),

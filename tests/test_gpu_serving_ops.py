@@ -172,6 +172,23 @@ def test_page_tables_refused_step_changes_nothing(change, why):
         assert (got["starts"] == 0).all()
 
 
+def test_page_tables_with_the_most_places():
+    """2^31 - 1 places (17 GB of slots), in a step that is taken and in one that is refused."""
+    from decode_megakernel_04_gb300 import page_tables
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 20 GB")
+    slots = torch.empty(2 ** 31 - 1, dtype=torch.int64, device=DEV)
+    for count, why, first in ((3, 0, [0, 1, 2, -1]), (-1, 2, [-1] * 4)):
+        slots.fill_(7)
+        t, status, starts = i32([[-1, -1]]), i32([0]), i32([9, 9])
+        page_tables(t, i32([0]), i32([0]), i32([count]), i32([0, 1, 2, 3]), i32([0, 4]), 4, 4, slots=slots, starts=starts, status=status)
+        assert status.item() == why and slots[:4].tolist() == first and starts.tolist() == [0, max(0, count)]
+        for part in slots[4:].split(1 << 28):
+            assert (part == -1).all()
+    with pytest.raises(ValueError):
+        page_tables(t, i32([0]), i32([0]), i32([0]), i32([0, 1, 2, 3]), i32([0, 4]), 4, 4, slots=slots[:1].expand(2 ** 31))
+
+
 def test_page_tables_bad_page_ids():
     table = np.array([[3, 77, -1], [4, 5, -1]], np.int32)
     ring = np.array([6, -2, 8, 9, 10, 11, 12, 13], np.int32)
