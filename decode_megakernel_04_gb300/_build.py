@@ -13,8 +13,8 @@ OPS = os.path.join(PKG, "ops")
 SOURCES = [os.path.join(CSRC, f) for f in ("mk_host.cu", "mk_kernel_dense.cu", "mk_kernel_full.cu")]
 SOURCES += [os.path.join(OPS, f) for f in ("page_tables.cu", "qk_norm_rope.cu", "logit_controls.cu", "paged_attention.cu",
                                            "paged_attention_bf16.cu", "paged_attention_f16.cu",
-                                           "paged_attention_e4m3.cu", "paged_attention_tc_bf16.cu",
-                                           "paged_attention_tc_f16.cu")]
+                                           "paged_attention_e4m3_bf16.cu", "paged_attention_e4m3_f16.cu",
+                                           "paged_attention_tc_bf16.cu", "paged_attention_tc_f16.cu")]
 HEADERS = [os.path.join(CSRC, "mk_internal.h"), os.path.join(CSRC, "mk_kernel.cuh"), os.path.join(INCLUDE, "mk.h")]
 HEADERS += [os.path.join(OPS, "mk_ops.cuh"), os.path.join(OPS, "paged_attention.cuh"),
             os.path.join(OPS, "paged_attention_tc.cuh")]

@@ -167,7 +167,9 @@ cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
   pl.blocks = (tiles + 3) / 4;
   const int mt = (tiles + pl.blocks - 1) / pl.blocks;
   auto pick = [&](bool longer) {
-    return a.cache_dtype == MK_E4M3 ? pick_e4m3(pl.dp, mt, longer) : a.dtype == MK_BF16 ? pick_bf16(pl.dp, mt, longer) : pick_f16(pl.dp, mt, longer);
+    const bool bf = a.dtype == MK_BF16;
+    if (a.cache_dtype == MK_E4M3) return bf ? pick_e4m3_bf16(pl.dp, mt, longer) : pick_e4m3_f16(pl.dp, mt, longer);
+    return bf ? pick_bf16(pl.dp, mt, longer) : pick_f16(pl.dp, mt, longer);
   };
   pl.build = pick(false);
   int sms, per_sm;

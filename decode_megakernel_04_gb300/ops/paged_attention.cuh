@@ -22,11 +22,13 @@
 // - 16-bit caches: probabilities enter the product as a pair hi + lo of 16-bit values (16 mantissa bits): rounded to one they
 //   would cost as much accuracy as the final rounding; the second product costs 5 % of the time. e4m3 caches: keys and
 //   values become fp16 (exact) and the queries fp16 scaled per row by a power of two (bf16 mantissas fit; what falls under
-//   2^-24 of a row's largest is rounded); probabilities are one fp16 (2^-11), an eighth of a bf16 result's rounding.
+//   2^-24 of a row's largest is rounded); probabilities are one fp16 (2^-11), an eighth of a bf16 result's rounding, for bf16
+//   queries, and a pair for fp16 ones (64 requests of 1 to 16384 positions 246 us, with one 235, while an fp16 result then is as far
+//   off again as its own rounding; 8 requests x 8 rows of 8192 85, 76).
 //   fp16 has few exponents, and many weak keys behind one strong key of a small value make the whole result: so fp16
 //   probabilities are taken against a base 15 under the running maximum (2^15 at it): off by 2^-11 (a pair: 2^-22) or by 2^-40
 //   of the largest. The sums are against the same base, which is what parts are joined by.
-// What bounds it now: warps x instructions in flight (IPC 1.8 of 4 at 12 warps on an SM); 64 requests of 1 to 16384
+// What bounds it now: warps x instructions in flight (IPC 1.8 of 4 at 8 warps on an SM); 64 requests of 1 to 16384
 // positions, 48 / 8 heads x 128, e4m3: 229 us, 70 % of the measured copy rate.
 #pragma once
 #include <type_traits>
@@ -185,10 +187,12 @@ __device__ inline uint32_t place(int row, int chunk) {  // byte offset of a 16-b
   return row * (kChunks * 16) + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-template <typename T, int DP, int MT, bool E4M3, bool LONG>
+// PAIRS: probabilities as hi + lo (over e4m3 caches with fp16 queries and not with bf16 ones)
+template <typename T, int DP, int MT, bool E4M3, bool LONG, bool PAIRS>
 __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<T, DP, MT, E4M3, LONG>::kCtas)
     attention_kernel(const __grid_constant__ Params p) {
   using S = Shape<T, DP, MT, E4M3, LONG>;
+  using Out = std::conditional_t<E4M3 && !PAIRS, __nv_bfloat16, T>;  // of the queries and the results
   extern __shared__ __align__(128) unsigned char smem[];
   const mk_paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -444,9 +448,7 @@ __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<
     if (d >= a.head_dim) return;
     const int mrow = block * S::kRows + row, r = p.group_div(mrow), h = head * p.group + mrow - r * p.group;
     const float f = sum == 0.0f ? 0.0f : (E4M3 ? a.v_scale[head] : 1.0f) / sum;
-    const uint2 u = (E4M3 ? a.dtype == MK_BF16 : std::is_same<T, __nv_bfloat16>::value)
-                        ? make_uint2(pack2<__nv_bfloat16>(y.x * f, y.y * f), pack2<__nv_bfloat16>(y.z * f, y.w * f))
-                        : make_uint2(pack2<__half>(y.x * f, y.y * f), pack2<__half>(y.z * f, y.w * f));
+    const uint2 u = make_uint2(pack2<Out>(y.x * f, y.y * f), pack2<Out>(y.z * f, y.w * f));
     uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2] + d;
     *reinterpret_cast<uint2*>(out) = u;
     if (d == 0 && a.lse)
@@ -484,12 +486,11 @@ __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<
           auto piece = [&](int k) {
             return *reinterpret_cast<const uint2*>(q + place<DP / 8>(row, 2 * k + (t4 >> 1)) + (t4 & 1) * 8);
           };
-          const bool bf = a.dtype == MK_BF16;
           float big = 0;
           for (int k = 0; k < DP / 16; ++k) {
             const uint2 u = piece(k);
-            const float2 x = bf ? unpack2<__nv_bfloat16>(u.x) : unpack2<__half>(u.x);
-            const float2 y = bf ? unpack2<__nv_bfloat16>(u.y) : unpack2<__half>(u.y);
+            const float2 x = unpack2<Out>(u.x);
+            const float2 y = unpack2<Out>(u.y);
             big = fmaxf(big, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
           }
           big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
@@ -501,8 +502,8 @@ __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
             const uint2 u = piece(k);
-            const float2 x = bf ? unpack2<__nv_bfloat16>(u.x) : unpack2<__half>(u.x);
-            const float2 y = bf ? unpack2<__nv_bfloat16>(u.y) : unpack2<__half>(u.y);
+            const float2 x = unpack2<Out>(u.x);
+            const float2 y = unpack2<Out>(u.y);
             qf[k][h] = pack2<__half>(x.x * down, x.y * down);
             qf[k][2 + h] = pack2<__half>(y.x * down, y.y * down);
           }
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<
           for (int i = 0; i < 4; ++i) {
             const float x = s[2 * q + (i >> 1)][2 * (i & 1)], y = s[2 * q + (i >> 1)][2 * (i & 1) + 1];
             hi[i] = pack2<T>(x, y);
-            if (!E4M3) {
+            if (PAIRS) {
               const float2 r = unpack2<T>(hi[i]);
               lo[i] = pack2<T>(x - r.x, y - r.y);
             }
@@ -646,6 +647,10 @@ __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<
                 if (kMixed) u[0] &= keep[0], u[1] &= keep[0], v[0] &= keep[1], v[1] &= keep[1];
                 mma<T>(o[4 * d + 2 * i], hi, u[0], v[0]);
                 mma<T>(o[4 * d + 2 * i + 1], hi, u[1], v[1]);
+                if (PAIRS) {
+                  mma<T>(o[4 * d + 2 * i], lo, u[0], v[0]);
+                  mma<T>(o[4 * d + 2 * i + 1], lo, u[1], v[1]);
+                }
               }
             }
           }
@@ -750,10 +755,10 @@ struct Build {
   cudaError_t (*launch)(const Params& p, cudaStream_t s);
 };
 
-template <typename T, int DP, int MT, bool E4M3, bool LONG = false>
+template <typename T, int DP, int MT, bool E4M3, bool LONG = false, bool PAIRS = !E4M3>
 struct Make {
   using S = Shape<T, DP, MT, E4M3, LONG>;
-  static constexpr auto kKernel = attention_kernel<T, DP, MT, E4M3, LONG>;
+  static constexpr auto kKernel = attention_kernel<T, DP, MT, E4M3, LONG, PAIRS>;
   static cudaError_t occupancy(int device, int* n) {
     static std::atomic<int> known[kMaxDevices];
     *n = known[device].load(std::memory_order_relaxed);
@@ -806,22 +811,26 @@ struct Make {
 // longer: the call's tiles are one line. 16-bit caches 64 wide then have tiles of 128 keys up to 32 rows (64 requests of 1 to
 // 16384 positions, 32 / 8 heads: 212 us against 242 with 64 keys; 64 / 2 heads: 265, 336), of 64 with more (48 rows: 367
 // against 442, fewer CTAs on an SM); a cluster wants more tiles to share (129 requests of up to 700: 8.7 against 10.4).
-template <typename T, bool E4M3>
+template <typename T, bool E4M3, bool PAIRS = !E4M3>
 inline const Build* pick(int dp, int mt, bool longer) {
   if constexpr (!E4M3) {
     static constexpr Build narrow[2] = {Make<T, 64, 1, false, true>::build(), Make<T, 64, 2, false, true>::build()};
     if (longer && dp == 64 && mt <= 2) return &narrow[mt - 1];
   }
   static constexpr Build all[3][4] = {
-      {Make<T, 64, 1, E4M3>::build(), Make<T, 64, 2, E4M3>::build(), Make<T, 64, 3, E4M3>::build(), Make<T, 64, 4, E4M3>::build()},
-      {Make<T, 128, 1, E4M3>::build(), Make<T, 128, 2, E4M3>::build(), Make<T, 128, 3, E4M3>::build(), Make<T, 128, 4, E4M3>::build()},
-      {Make<T, 256, 1, E4M3>::build(), Make<T, 256, 2, E4M3>::build(), Make<T, 256, 3, E4M3>::build(), Make<T, 256, 4, E4M3>::build()}};
+      {Make<T, 64, 1, E4M3, false, PAIRS>::build(), Make<T, 64, 2, E4M3, false, PAIRS>::build(),
+       Make<T, 64, 3, E4M3, false, PAIRS>::build(), Make<T, 64, 4, E4M3, false, PAIRS>::build()},
+      {Make<T, 128, 1, E4M3, false, PAIRS>::build(), Make<T, 128, 2, E4M3, false, PAIRS>::build(),
+       Make<T, 128, 3, E4M3, false, PAIRS>::build(), Make<T, 128, 4, E4M3, false, PAIRS>::build()},
+      {Make<T, 256, 1, E4M3, false, PAIRS>::build(), Make<T, 256, 2, E4M3, false, PAIRS>::build(),
+       Make<T, 256, 3, E4M3, false, PAIRS>::build(), Make<T, 256, 4, E4M3, false, PAIRS>::build()}};
   return &all[dp == 64 ? 0 : dp == 128 ? 1 : 2][mt - 1];
 }
 
 const Build* pick_bf16(int dp, int mt, bool longer);
 const Build* pick_f16(int dp, int mt, bool longer);
-const Build* pick_e4m3(int dp, int mt, bool longer);
+const Build* pick_e4m3_bf16(int dp, int mt, bool longer);
+const Build* pick_e4m3_f16(int dp, int mt, bool longer);
 
 }  // namespace attn
 }  // namespace mkop

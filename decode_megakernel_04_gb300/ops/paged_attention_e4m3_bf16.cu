@@ -1,0 +1,8 @@
+// The attention kernels over e4m3 caches with bf16 queries.
+#include "paged_attention.cuh"
+
+namespace mkop {
+namespace attn {
+const Build* pick_e4m3_bf16(int dp, int mt, bool longer) { return pick<__half, true, false>(dp, mt, longer); }
+}  // namespace attn
+}  // namespace mkop

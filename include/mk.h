@@ -504,7 +504,10 @@ mk_status mk_qk_norm_rope(const mk_qk_norm_rope_args* args, int device, void* st
  *   s = scale * q . k,  p = softmax(s),  out = sum p v,  lse = log(sum exp(s)) (natural)
  * A row that sees nothing gives out = 0 and lse = -infinity. Values in the cache that a row does not see
  * (positions from lens[b] on, later rows' keys) do not reach it, whatever they hold (NaN included).
- * Scores, softmax statistics and sums are fp32; out is rounded once. An infinite value that a row sees makes that column
+ * Scores, softmax statistics and sums are fp32; out is rounded once. Probabilities enter the product with the values as pairs
+ * of 16-bit numbers (to 2^-16 and better), over e4m3 caches with bf16 queries as one fp16 (2^-11, an eighth of out's own
+ * rounding); ones far below a row's largest to 2^-40 of that. Over e4m3 caches queries are taken in fp16 against a power of two near
+ * their row's largest element: bf16 elements are exact down to 2^-16 of that, fp16 ones to 2^-13, smaller ones to 2^-25 of it. An infinite value that a row sees makes that column
  * of the row NaN or infinite; a score of +infinity or NaN makes the row NaN.
  * A length below 0 counts as 0, one beyond max_pages * page_size as that (MK_OP_BAD_LENGTH); keys and
  * values of a page outside 0 .. n_pages - 1 read as zeros (MK_OP_BAD_PAGE). Table entries of pages a

@@ -675,6 +675,25 @@ def test_attention_of_many_weak_keys_behind_a_strong_one(dtype, cache, d, lens, 
     assert ((lse.double() - l64).abs() <= ds + 2.0 ** -20 + n * 2.0 ** -23 + l64.abs() * 2.0 ** -22).all()
 
 
+@pytest.mark.parametrize("width", [None, 50000])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("R, hq", [(1, 24), (6, 48)])
+def test_attention_over_e4m3_with_fp16_results_is_rounded_once(R, hq, d, width):
+    """Scores of one exact product each, so that what is left is the rounding of the probabilities: a pair of fp16 values
+    (2^-22), not one (2^-11, as much as the result's own). Scores, exponentials and sums as in check_attention."""
+    lens = [1, 2, 3, 7, 12, 20, 33, 40, 130, 200]
+    s = attention_inputs(lens, R, hq, 8, d, 16, F16, E4M3, seed=45, max_pages=width)
+    s["ks"].fill_(1.0)
+    one = torch.zeros_like(s["q"])
+    one[..., 3] = s["q"][..., 3]
+    s["q"].copy_(one)
+    got, _ = run_attention(s, scale=0.5)
+    out, l64, av, qk = attention_reference(s, 0.5)
+    n = s["lens"].double()[:, None, None]
+    rel = 2 * (qk * 2.0 ** -21 + 2.0 ** -21 + n * 2.0 ** -23) + 2.0 ** -22
+    check_rounded(got, out, F16, "out", rel[..., None] * av)
+
+
 def test_attention_lengths_and_pages_out_of_range():
     s = attention_inputs([40, 30, 20, 10], 1, 4, 2, 64, 8, BF16, BF16, seed=6, max_pages=5, poison=False)
     good, gl = run_attention(s)
