@@ -1271,3 +1271,219 @@ def test_a_failed_call_leaves_nothing_for_the_next_one():
     torch.cuda.synchronize()
     assert m.status() == 0
     m.close()
+
+
+# ---- the ends of the documented ranges ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens, R, hq, hkv, d, dtype, cache", [
+    ([70, 200, 64, 3], 64, 6, 1, 128, BF16, BF16), ([65, 130], 65, 4, 2, 64, F16, F16), ([1000, 1500, 999], 1000, 4, 2, 128, BF16, BF16),
+    ([4096], 4096, 2, 1, 64, BF16, BF16), ([300], 100, 8, 1, 256, F16, F16), ([500, 90], 100, 6, 2, 128, BF16, E4M3),
+    ([700], 65, 4, 1, 256, F16, E4M3)])
+@pytest.mark.parametrize("width", [None, 50000])
+def test_attention_of_many_new_tokens(lens, R, hq, hkv, d, dtype, cache, width):
+    """A prompt's tokens at once; then the newest two keys become NaN, which the rows before them do not see."""
+    s = attention_inputs(lens, R, hq, hkv, d, 16, dtype, cache, seed=51, max_pages=width)
+    got, lse = run_attention(s)
+    check_attention(s, got, lse, d ** -0.5)
+    for x in (s["k"], s["v"]):  # the newest two keys of each request: every row before them as it was
+        for b, n in enumerate(lens):
+            for p in (n - 1, n - 2):
+                at = s["table"][b, p // 16].long()
+                x[at, :, p % 16] = torch.full((hkv, d), float("nan"), device=DEV).to(cache)
+    bad, bl = run_attention(s)
+    assert torch.equal(bad[:, :R - 2], got[:, :R - 2]) and torch.equal(bl[:, :R - 2], lse[:, :R - 2])
+    assert bad[:, -1].isnan().all()
+
+
+def test_attention_of_more_requests_than_a_cta_has_threads():
+    for d, cache in ((128, BF16), (64, BF16), (128, E4M3)):
+        s = attention_inputs([i * 11 % 90 for i in range(1300)], 1, 4, 1, d, 16, BF16, cache, seed=52, max_pages=50000)
+        got, lse = run_attention(s)
+        check_attention(s, got, lse, d ** -0.5)
+
+
+def test_attention_of_one_very_long_request():
+    """Positions, tiles and pieces of 3 million keys; all scores equal, so that the result is the mean of the values."""
+    n, page, d = 3_000_001, 256, 64
+    pages = -(-n // page)
+    g = gen(53)
+    k = torch.zeros(pages, 1, page, d, dtype=F16, device=DEV)
+    v = torch.randint(0, 3, (pages, 1, page, d), generator=g, device=DEV).to(F16)
+    s = dict(q=torch.ones(1, 2, 4, d, dtype=F16, device=DEV), k=k, v=v, table=torch.randperm(pages, generator=g, device=DEV).to(torch.int32)[None],
+             lens=i32([n]), ks=None, vs=None, page=page)
+    v[s["table"][0, -1].long(), :, n % page:] = float("nan")
+    got, lse = run_attention(s)
+    x = v[s["table"][0].long()].reshape(-1, d)
+    for r in range(2):
+        m = n - 1 + r
+        # sums of whole numbers times a power of two: exact in fp32 within a piece while below 2^24; joined in 1 rounding each
+        want = x[:m].double().mean(0)
+        check_rounded(got[0, r], want.expand(4, d), F16, "mean", 2.0 ** -16 * want)
+        assert (lse[0, r].double() - math.log(m)).abs().max() < 2.0 ** -18
+
+
+def test_logit_controls_of_a_million_rows_and_of_the_longest_rows():
+    from decode_megakernel_04_gb300 import logit_controls
+    g = gen(54)
+    for rows, vocab in ((1 << 20, 5), (1, 1 << 24), (40, 1 << 24), (3, (1 << 24) - 5)):
+        z = torch.randn(rows, vocab, generator=g, device=DEV)
+        bits = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, -(-vocab // 32)), generator=g, device=DEV).to(torch.int32)
+        hist = torch.randint(0, vocab, (rows, 3), generator=g, device=DEV).to(torch.int32)
+        pen = 0.5 + torch.rand(rows, generator=g, device=DEV)
+        out, tok = torch.empty_like(z), torch.empty(rows, dtype=torch.int32, device=DEV)
+        logit_controls(z, out, history=hist, presence=pen, allowed=bits, token=tok)
+        ids = hist.long()
+        z.scatter_(1, ids, z.gather(1, ids) - pen[:, None])  # (an id named twice: both write the same)
+        v = torch.arange(vocab, device=DEV)
+        for r0 in range(0, rows, 1 << 18 if vocab < 100 else 4):
+            part = slice(r0, r0 + (1 << 18 if vocab < 100 else 4))
+            ok = (bits[part][:, v >> 5] >> (v & 31)) & 1 == 1
+            want = torch.where(ok, z[part], -math.inf)
+            assert torch.equal(out[part], want)
+            first = torch.where(want == want.amax(1, keepdim=True), v, vocab).amin(1)
+            assert torch.equal(tok[part].long(), torch.where(ok.any(1), first, -1))
+
+
+def test_logit_controls_longest_history():
+    """2^20 - 1 entries of one token: the count fills its bits; with the most biases."""
+    V, n = 1000, 2 ** 20 - 1
+    z = torch.full((2, V), 2.0, device=DEV)
+    kw = dict(history=torch.full((2, n), 17, dtype=torch.int32, device=DEV), prompt_len=i32([0, 1]), repetition=torch.tensor([2.0, 4.0], device=DEV),
+              frequency=torch.tensor([0.5, 2.0], device=DEV), bias_ids=i32([[17] * 2047] * 2), bias_vals=torch.arange(4094, device=DEV).view(2, 2047).float())
+    check_controls(z, kw)
+
+
+def test_qk_most_heads_and_any_position():
+    from decode_megakernel_04_gb300 import qk_norm_rope
+    g = gen(55)
+    n, hq, hkv, d = 5, 4096, 4096, 16
+    q, k = (torch.randn(n, h, d, generator=g, device=DEV).to(BF16) for h in (hq, hkv))
+    pos = i32([-2 ** 31, -1, 0, 2 ** 31 - 1, -12345678])
+    inv = (1e4 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).to(DEV)
+    gain = (1 + 0.2 * torch.randn(d, generator=g, device=DEV)).to(BF16)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    qk_norm_rope(q, k, pos, inv, qo, k_out=ko, q_gain=gain, k_gain=gain)
+    for x, y in ((q, qo), (k, ko)):
+        want = rotate(x, gain, 1e-6, pos, inv)
+        check_rounded(y, want, BF16, "heads", qk_slack(want))
+
+
+@pytest.mark.parametrize("over", ["held", "start", "count"])
+@pytest.mark.parametrize("chunk", [3, 2000])
+def test_page_tables_lens_over_each_of_the_lengths(over, chunk):
+    """lens may be held, start or count itself, for a step that is taken and one that is refused, of one CTA and of more."""
+    from decode_megakernel_04_gb300 import page_tables
+    rng = np.random.default_rng(5)
+    B, page, max_pages = 20, 16, 400
+    held = [int(x) for x in rng.integers(0, 4000, B)]
+    start = [max(0, h - i % 3) for i, h in enumerate(held)]
+    count = [1 + (chunk if i % 7 == 0 else 0) for i in range(B)]
+    n_pages = 2 * B * max_pages
+    table, ring, state = make_pool(rng, held, page, max_pages, n_pages, 0)
+    for bad in (False, True):
+        places = sum(count) - bad
+        t = dict(held=i32(held), start=i32(start), count=i32(count))
+        tab, rg = torch.from_numpy(table).to(DEV), torch.from_numpy(ring).to(DEV)
+        st, slots, status = i32(state), torch.empty(places, dtype=torch.int64, device=DEV), i32([0])
+        page_tables(tab, t["held"], t["start"], t["count"], rg, st, page, n_pages, slots=slots, lens=t[over], status=status)
+        want = tables_reference(table, held, start, count, ring, state, page, n_pages, places)
+        if bad:
+            assert want == 8 == status.item() and t[over].tolist() == held and st.tolist() == state
+        else:
+            assert t[over].tolist() == want["lens"].tolist() and np.array_equal(slots.cpu().numpy(), want["slots"])
+            assert st.tolist() == want["ring_state_out"].tolist() and np.array_equal(tab.cpu().numpy(), want["table"])
+
+
+def test_calls_without_rows():
+    from decode_megakernel_04_gb300 import logit_controls, paged_attention, qk_norm_rope
+    x = torch.empty(0, 2, 64, dtype=BF16, device=DEV)
+    qk_norm_rope(x, x, i32([]), torch.ones(32, dtype=torch.float64, device=DEV), x)
+    kv = torch.zeros(3, 2, 16, 64, dtype=BF16, device=DEV)
+    qk_norm_rope(x, x, None, None, x, v=x, k_pages=kv, v_pages=kv, slots=torch.empty(0, dtype=torch.int64, device=DEV))
+    q = torch.empty(0, 1, 4, 64, dtype=BF16, device=DEV)
+    paged_attention(q, kv, kv, torch.empty(0, 5, dtype=torch.int32, device=DEV), i32([]), q)
+    z = torch.empty(0, 9, device=DEV)
+    logit_controls(z, z, token=i32([]))
+    torch.cuda.synchronize()
+
+
+FIRST_CALL = """
+import torch
+from decode_megakernel_04_gb300 import logit_controls, page_tables, paged_attention, qk_norm_rope
+D = "cuda"
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=D)
+t, h, st, ring, slots = i32([[0, -1], [1, -1]]), i32([4, 2]), i32([0, 2]), i32([2, 3, 0, 0]), torch.empty(3, dtype=torch.int64, device=D)
+one, so, lens = i32([1, 1]), i32([0, 0]), i32([0, 0])
+x = torch.randn(2, 4, 128, device=D).bfloat16()
+xo = torch.empty_like(x)
+kv = torch.randn(4, 2, 16, 128, device=D).bfloat16()
+q = torch.randn(2, 1, 4, 128, device=D).bfloat16()
+tab, wide, al = i32([[0, 1], [2, 3]]), i32([[0, 1] + [0] * 5000, [2, 3] + [0] * 5000]), i32([20, 31])
+o1, o2 = torch.zeros_like(q), torch.zeros_like(q)
+few, many = torch.randn(2, 70, device=D), torch.randn(400, 70, device=D)
+f2, m2 = torch.zeros_like(few), torch.zeros_like(many)
+ids, vals = i32([[5]] * 400), torch.ones(400, 1, device=D)
+def calls():
+    page_tables(t, h, h, one, ring, st, 4, 4, slots=slots, lens=lens, ring_state_out=so)
+    qk_norm_rope(x, x, None, None, xo)
+    paged_attention(q, kv, kv, tab, al, o1)
+    paged_attention(q, kv, kv, wide, al, o2)
+    logit_controls(few, f2)
+    logit_controls(many, m2, bias_ids=ids, bias_vals=vals)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    calls()
+g.replay()
+torch.cuda.synchronize()
+got = [v.clone() for v in (slots, lens, so, xo, o1, o2, f2, m2)]
+t.copy_(i32([[0, -1], [1, -1]])), o1.zero_(), o2.zero_(), f2.zero_(), m2.zero_(), xo.zero_()
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (slots, lens, so, xo, o1, o2, f2, m2)))
+assert torch.equal(xo, x) and torch.equal(f2, few) and o1.abs().sum() > 0 and (o1.float() - o2.float()).abs().max() < 0.02
+print("same")
+"""
+
+
+def test_a_process_first_calls_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+def test_calls_from_several_threads_at_once():
+    """Each thread on a stream of its own, scratch from torch's allocator: every result as alone."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    from decode_megakernel_04_gb300 import logit_controls, paged_attention, qk_norm_rope
+    sets = [attention_inputs([2000 + 77 * i, 40, 900], 1 + i % 2, 8, 2, 128, 16, BF16, BF16, seed=60 + i, poison=False,
+                             max_pages=50000 if i % 3 else None) for i in range(6)]
+    logits = [logit_inputs(100, 5003, 300, 9, F32, True, 0, seed=60 + i) for i in range(6)]
+    norms = [qk_inputs(50 + i, 12, 2, 128, 128, BF16, None, 1, True, seed=60 + i) for i in range(6)]
+
+    def work(i, stream):
+        with torch.cuda.stream(stream):
+            s, (z, kw), n = sets[i], logits[i], norms[i]
+            outs = []
+            for _ in range(20):
+                o, l, y = torch.empty_like(s["q"].contiguous()), torch.empty(s["q"].shape[:3], device=DEV), torch.empty_like(z)
+                tok, qo = i32([0] * 100), torch.empty_like(n["q"].contiguous())
+                paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], o, lse=l)
+                logit_controls(z, y, token=tok, **kw)
+                qk_norm_rope(n["q"], n["k"], n["pos"], n["inv"], qo, q_gain=n["qg"], k_gain=n["kg"])
+                outs.append((o, l, y, tok, qo))
+            stream.synchronize()
+        return outs
+
+    torch.cuda.synchronize()
+    want = [work(i, torch.cuda.current_stream())[0] for i in range(6)]
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(6) as pool:
+        got = list(pool.map(work, range(6), streams))
+    for w, outs in zip(want, got):
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(w, o))
