@@ -182,3 +182,40 @@ def test_static_entry_point_rejects_oversized_step():
     assert rc == 0
     assert torch.isfinite(lg1).all()
     mk.close()
+
+
+def test_paged_attention_reads_the_caches_a_static_step_wrote():
+    """The caller's KV cache after mk_decode_step_static, one layer at a time, as the paged cache include/mk.h describes: the
+    step has written the positions it committed or holds pending and no others, and attention over the pages is that over them."""
+    from decode_megakernel_04_gb300 import Megakernel, _build, binding, paged_attention
+    _build.build()
+    lib = binding.load()
+    cfg = config("tiny_dense", n_kv_heads=2)
+    dev = torch.device("cuda")
+    w = make_weights(cfg, seed=8, device=dev)
+    B, R, ctx, page = 2, 8, 64, 16
+    mk = Megakernel(cfg, w, max_batch=B, max_rows=R, max_ctx=ctx)
+    keep, sb = _state_buffers(cfg, mk.desc, dev)
+    calls = [(make_tokens(8, "a", (B, R), cfg.vocab, device=dev), [0, 0]), (make_tokens(8, "b", (B, R), cfg.vocab, device=dev), [R, R]),
+             (make_tokens(8, "c", (B, 1), cfg.vocab, device=dev), [2 * R, 2 * R])]
+    _compare_calls(lib, mk, sb, cfg, calls, dev)
+    n, hkv, d, layers = 2 * R + 1, cfg.n_kv_heads, cfg.head_dim, sum(1 for m in cfg.mixers if m == "gqa")
+    kc, vc = (x.view(layers, B, hkv, ctx, d) for x in keep[:2])
+    assert (kc[:, :, :, :n].float().abs().amax(-1) > 0).all() and (kc[:, :, :, n:] == 0).all() and (vc[:, :, :, n:] == 0).all()
+    per = ctx // page
+    table = (torch.arange(B)[:, None] * hkv * per + torch.arange(per)).to(torch.int32).to(dev)
+    lens = torch.full((B,), n, dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev)
+    g.manual_seed(8)
+    q = torch.randn(B, 1, cfg.n_q_heads, d, generator=g, device=dev).to(torch.bfloat16)
+    for k, v in zip(kc, vc):
+        as_pages = [x.as_strided(((B - 1) * hkv * per + per, hkv, page, d), (page * d, ctx * d, d, 1)) for x in (k, v)]
+        out = torch.empty_like(q)
+        paged_attention(q, *as_pages, table, lens, out)
+        x = q.double().view(B, hkv, -1, d)
+        p = torch.softmax(torch.matmul(x, k[:, :, :n].double().transpose(2, 3)) * d ** -0.5, -1)
+        want = torch.matmul(p, v[:, :, :n].double()).view_as(q)
+        mass = torch.matmul(p, v[:, :, :n].double().abs()).view_as(q)
+        # one rounding to bf16, and 2^-12 of the terms for fp32 scores (d + 4 roundings of 2^-23 of sums up to 2^4) and sums
+        assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -8 + mass * 2.0 ** -12).all()
+    mk.close()
