@@ -468,7 +468,8 @@ mk_status mk_page_tables(const mk_page_tables_args* args, int device, void* stre
  *   elements from rope_dim on pass.
  * Norm and rotation are held in fp32, the angles are exact to fp32 at any int32 position (the turn count
  * is reduced in 64-bit integers), and each value is rounded once, to its output type (e4m3: the fp32 quotient value / scale,
- * nearest even, saturating at 448). Values in a 16-bit cache are the inputs bit for bit. q_out may be q, k_out may be k (same strides).
+ * nearest even, saturating at 448). Values in a 16-bit cache are the inputs bit for bit.
+ * (bf16 elements of 2^60 and more have squares beyond fp32: such a head norms to zeros.) q_out may be q, k_out may be k (same strides).
  * Token t's key and value go to slots[t] of the paged cache; a negative slot stores nothing, one outside
  * the cache stores nothing and sets MK_OP_BAD_PAGE. Two tokens with one slot: its place holds parts of either.
  * Errors: head_dim not a multiple of 16 in 16..256, rope_dim not a multiple of 8 in 0..head_dim, pointers
