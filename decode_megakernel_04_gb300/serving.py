@@ -4,7 +4,8 @@ and marshalling only; every result is computed by the library's kernels.
 
 Tensors live on one CUDA device and outputs are preallocated, as in ``Megakernel``; each call enqueues and returns.
 ``stream`` is a raw CUDA stream (an int, 0 = the legacy default stream); None takes torch's current stream of the
-tensors' device, so a call inside ``torch.cuda.stream`` or a graph capture lands there. Tensors that do not fit
+tensors' device, so a call inside ``torch.cuda.stream`` or a graph capture lands there. On any other stream than that the
+caller orders the call with the work that makes and frees its tensors, as for every use of torch on two streams. Tensors that do not fit
 together raise ValueError; what the library refuses raises MKError. ``status``, where given, is an int32 tensor of one
 element that collects the OP_* flags of what only the device can see.
 """

@@ -1487,3 +1487,35 @@ def test_calls_from_several_threads_at_once():
     for w, outs in zip(want, got):
         for o in outs:
             assert all(torch.equal(a, b) for a, b in zip(w, o))
+
+
+def test_captured_calls_on_a_forked_stream_and_with_rows_over_several_ctas():
+    """Inside one capture: attention with scratch of its own on a second stream, and logit controls whose rows take 1, 2 and 4
+    CTAs; replayed with other inputs, twice."""
+    from decode_megakernel_04_gb300 import logit_controls, paged_attention
+    s = attention_inputs([3000, 40, 700], 2, 8, 1, 128, 16, BF16, BF16, seed=71, poison=False, max_pages=50000)
+    sets = [logit_inputs(*case, seed=72) for case in ((30, 5000, 3000, 20, F32, True, 0), (60, 9001, 1500, 40, F32, True, 1), (90, 3001, 2000, 3, F32, True, 0))]
+    outs = [torch.empty_like(z) for z, _ in sets]
+    toks = [i32([0] * z.shape[0]) for z, _ in sets]
+    o, l = torch.empty_like(s["q"].contiguous()), torch.empty(s["q"].shape[:3], device=DEV)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], o, lse=l, stream=side.cuda_stream)
+        for (z, kw), out, tok in zip(sets, outs, toks):
+            logit_controls(z, out, token=tok, **kw)
+        main.wait_stream(side)
+    for turn in range(2):
+        s["q"].mul_(0.8)
+        for z, kw in sets:
+            z.mul_(-0.7)
+            kw["history"].add_(1)
+        graph.replay()
+        want, wl = run_attention(s)
+        assert torch.equal(o, want) and torch.equal(l, wl)
+        for (z, kw), out, tok in zip(sets, outs, toks):
+            y, token = controls_reference(z, *(kw.get(k) for k in ("history", "prompt_len", "total_len", "repetition", "presence",
+                                                                  "frequency", "bias_ids", "bias_vals", "allowed")))
+            assert np.array_equal(out.cpu().numpy(), y) and np.array_equal(tok.cpu().numpy(), token)
