@@ -5,7 +5,8 @@ its sources, the build step and a thin ctypes binding with the same entry points
 """
 from .binding import Megakernel, MKError, load, lib_path, EXPORTS  # noqa: F401
 
-_SERVING = ("page_tables", "qk_norm_rope", "paged_attention", "paged_attention_workspace", "logit_controls")
+_SERVING = ("page_tables", "rms_norm", "qk_norm_rope", "paged_attention", "paged_attention_workspace", "prefix_attention",
+            "prefix_attention_workspace", "logit_controls", "verify_drafts", "verify_drafts_workspace")
 
 
 def __getattr__(name):

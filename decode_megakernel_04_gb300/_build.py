@@ -11,7 +11,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmk.so")
 OPS = os.path.join(PKG, "ops")
 SOURCES = [os.path.join(CSRC, f) for f in ("mk_host.cu", "mk_kernel_dense.cu", "mk_kernel_full.cu")]
-SOURCES += [os.path.join(OPS, f) for f in ("page_tables.cu", "qk_norm_rope.cu", "logit_controls.cu", "paged_attention.cu",
+SOURCES += [os.path.join(OPS, f) for f in ("page_tables.cu", "rms_norm.cu", "qk_norm_rope.cu", "logit_controls.cu", "verify_drafts.cu", "prefix_attention.cu", "paged_attention.cu",
                                            "paged_attention_bf16.cu", "paged_attention_f16.cu",
                                            "paged_attention_e4m3_bf16.cu", "paged_attention_e4m3_f16.cu",
                                            "paged_attention_tc_bf16.cu", "paged_attention_tc_f16.cu")]

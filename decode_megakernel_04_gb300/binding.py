@@ -108,12 +108,37 @@ class LogitControlsArgs(C.Structure):
                 ("dtype", _I)]
 
 
+class RmsNormArgs(C.Structure):
+    _fields_ = [("x", _P), ("residual", _P), ("gain", _P), ("residual_out", _P), ("out", _P), ("scales", _P),
+                ("x_stride", _L), ("residual_stride", _L), ("residual_out_stride", _L), ("out_stride", _L),
+                ("scales_stride", _L), ("rows", _I), ("width", _I), ("group", _I), ("dtype", _I), ("out_dtype", _I),
+                ("eps", _F)]
+
+
+class PrefixAttentionArgs(C.Structure):
+    _fields_ = [("q", _P), ("k_pages", _P), ("v_pages", _P), ("prefix_table", _P), ("prefix_len", _P), ("table", _P),
+                ("lens", _P), ("k_scale", _P), ("v_scale", _P), ("out", _P), ("lse", _P), ("workspace", _P), ("status", _P),
+                ("workspace_bytes", _L), ("table_stride", _L), ("q_stride", _L * 3), ("out_stride", _L * 3),
+                ("k_page_stride", _L * 3), ("v_page_stride", _L * 3), ("batch", _I), ("rows", _I), ("n_q_heads", _I),
+                ("n_kv_heads", _I), ("head_dim", _I), ("n_pages", _I), ("page_size", _I), ("max_pages", _I),
+                ("max_prefix_pages", _I), ("dtype", _I), ("cache_dtype", _I), ("scale", _F)]
+
+
+class VerifyDraftsArgs(C.Structure):
+    _fields_ = [("logits", _P), ("draft_logits", _P), ("tokens", _P), ("n_drafts", _P), ("positions", _P),
+                ("temperature", _P), ("uniforms", _P), ("noise", _P), ("accept_out", _P), ("logprobs", _P),
+                ("workspace", _P), ("status", _P), ("workspace_bytes", _L), ("logits_stride", _L), ("draft_stride", _L),
+                ("noise_stride", _L), ("batch", _I), ("rows", _I), ("vocab", _I), ("dtype", _I)]
+
+
 EXPORTS = ["mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host", "mk_get_status",
            "mk_last_error", "mk_get_info", "mk_destroy", "mk_decode_step_static", "mk_set_routing_log",
            "mk_fork_sequence", "mk_plan", "mk_set_wait_limit",
            "mk_set_routing_override", "mk_decode_steps", "mk_decode_steps_host", "mk_verify_step",
            "mk_packed_weight_bytes", "mk_pack_weights", "mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention",
-           "mk_paged_attention_workspace", "mk_logit_controls", "mk_logit_controls_workspace", "mk_logit_controls_check"]
+           "mk_paged_attention_workspace", "mk_logit_controls", "mk_logit_controls_workspace", "mk_logit_controls_check",
+           "mk_rms_norm", "mk_prefix_attention", "mk_prefix_attention_workspace", "mk_verify_drafts",
+           "mk_verify_drafts_workspace", "mk_verify_drafts_check"]
 
 _lib = None
 
@@ -156,12 +181,15 @@ def load(path: str | None = None) -> C.CDLL:
     lib.mk_packed_weight_bytes.argtypes = [C.POINTER(ModelDesc), C.POINTER(Weights), C.c_int, C.POINTER(C.c_uint64)]
     lib.mk_pack_weights.argtypes = [C.POINTER(ModelDesc), C.POINTER(Weights), C.c_int, _P, _P]
     # the argument structs go in by address (a structure's byref or the bytes of one)
-    for f in ("mk_page_tables", "mk_qk_norm_rope", "mk_paged_attention", "mk_logit_controls"):
+    for f in ("mk_page_tables", "mk_rms_norm", "mk_qk_norm_rope", "mk_paged_attention", "mk_prefix_attention",
+              "mk_logit_controls", "mk_verify_drafts"):
         getattr(lib, f).argtypes = [_P, C.c_int, _P]
         getattr(lib, f).restype = C.c_int
-    lib.mk_logit_controls_check.argtypes = [_P, C.c_int]
-    lib.mk_logit_controls_check.restype = C.c_int
-    for f in ("mk_paged_attention_workspace", "mk_logit_controls_workspace"):
+    for f in ("mk_logit_controls_check", "mk_verify_drafts_check"):
+        getattr(lib, f).argtypes = [_P, C.c_int]
+        getattr(lib, f).restype = C.c_int
+    for f in ("mk_paged_attention_workspace", "mk_prefix_attention_workspace", "mk_logit_controls_workspace",
+              "mk_verify_drafts_workspace"):
         getattr(lib, f).argtypes = [_P, C.c_int, C.POINTER(C.c_uint64)]
         getattr(lib, f).restype = C.c_int
     for f in ("mk_packed_weight_bytes", "mk_pack_weights", "mk_create", "mk_prefill_kv", "mk_decode_step", "mk_decode_step_host", "mk_get_status", "mk_get_info",
@@ -326,10 +354,27 @@ class Megakernel:
             None if logits_np is None else logits_np.ctypes.data, argmax_np.ctypes.data, stream)
         self._check(rc)
 
-    def verify(self, tokens, positions, accept_out, logits=None, argmax=None, stream=None):
+    def verify(self, tokens, positions, accept_out, logits=None, argmax=None, stream=None, sampling=None):
         """Verify step with on-device greedy acceptance. tokens: device int32 [B, R] (anchor + drafts);
-        accept_out: device int32 [3, B] (accepted length, bonus token, next position)."""
+        accept_out: device int32 [3, B] (accepted length, bonus token, next position).
+        sampling: a dict of serving.verify_drafts' arguments (noise, uniforms, draft_logits, n_drafts, temperature, logprobs,
+        ...): the drafts are then verified against the step's logits (required: contiguous fp32 [B * R, vocab]) by sampling, on
+        the same stream; R = 1 samples a token."""
         B, R = tokens.shape
+        if sampling is not None:
+            from .serving import _call, check_verify_drafts, prepare_verify_drafts
+            z = None if logits is None else logits.view(-1, self.cfg.vocab)
+            # (the step writes its rows one after the other)
+            if z is None or z.shape[0] != B * R or z.get_device() != self.device or not z.is_contiguous():
+                raise ValueError("sampling needs contiguous logits [batch * rows, vocab] on the handle's device")
+            # what does not fit is refused before the step, which cannot be taken back
+            call, workspace = prepare_verify_drafts(z, tokens, accept_out=accept_out, positions=positions, stream=stream or 0,
+                                                    **sampling)
+            check_verify_drafts(call)
+            self._check(self.lib.mk_decode_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R, z.data_ptr(),
+                                                 _ptr(argmax), stream))
+            _call(*call)
+            return
         self._check(self.lib.mk_verify_step(self.h, tokens.data_ptr(), positions.data_ptr(), B, R, _ptr(logits),
                                              _ptr(argmax), accept_out.data_ptr(), stream))
 

@@ -141,4 +141,32 @@ __device__ inline float2 unpack2<__half>(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// x / scale for an e4m3 result, by a product and one correction. The product with inv = 1 / scale alone is off by up to 1.5
+// steps of fp32, so that a value halfway between two codes could go to either. What it leaves, x - q scale, is exact in one
+// fused multiply-add; the corrected sum is off by 2^-46 before its rounding, so a quotient that is an fp32 value, as
+// halfway ones are, comes out as that value. Nothing overflows or gets too small for that: a scale outside 2^+-60 is brought there
+// with the value (`lift`, a power of two), and quotients past 448, infinite ones among them, are not corrected.
+// mk_qk_norm_rope, 8190 tokens of 48 / 8 heads x 128 with an e4m3 append 63 us (the product alone 60, divisions 67); a verify batch of 512 rows 7.5
+// (7.0, 8.7).
+struct Scale {
+  float scale, inv, lift;
+  __device__ explicit Scale(float s) {
+    lift = fabsf(s) < 0x1p-60f ? 0x1p100f : fabsf(s) > 0x1p60f ? 0x1p-64f : 1.0f;
+    scale = s * lift;
+    inv = 1.0f / scale;
+  }
+  __device__ float quotient(float x) const {
+    x *= lift;
+    const float q = x * inv;
+    return fabsf(q) < 512.0f ? fmaf(fmaf(-q, scale, x), inv, q) : q;
+  }
+};
+
+__device__ inline uint32_t e4m3x4(const float* x, const Scale& s) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(s.quotient(x[1])), "f"(s.quotient(x[0])));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(s.quotient(x[3])), "f"(s.quotient(x[2])));
+  return lo | static_cast<uint32_t>(hi) << 16;
+}
+
 }  // namespace mkop

@@ -57,10 +57,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
           const float g = __shfl_sync(~0u, f, k);
           y.x += g * x.x, y.y += g * x.y, y.z += g * x.z, y.w += g * x.w;
         }
-        if (d < a.head_dim)
+        if (p.raw)
+          *reinterpret_cast<float4*>(p.raw + ((static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h) * dp + d) =
+              make_float4(y.x * scale, y.y * scale, y.z * scale, y.w * scale);
+        else if (d < a.head_dim)
           *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(y.x * scale, y.y * scale), pack2<T>(y.z * scale, y.w * scale));
       }
-      if (lane == 0 && a.lse)
+      if (lane == 0 && p.raw)
+        p.raw_lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] = sum == 0.0f ? -INFINITY : top + log2f(sum);
+      else if (lane == 0 && a.lse)
         a.lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] =
             sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
     }
@@ -106,16 +111,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     for (int d = 2 * tid; d < a.head_dim; d += 2 * kJoinWarps * 32) {
       float x = 0, y = 0;
       for (int w = 0; w < kJoinWarps; ++w) x += sums[w][d], y += sums[w][d + 1];
-      out[d / 2] = pack2<T>(x * f, y * f);
+      if (p.raw)
+        *reinterpret_cast<float2*>(p.raw + ((static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h) * dp + d) = make_float2(x * f, y * f);
+      else
+        out[d / 2] = pack2<T>(x * f, y * f);
     }
-    if (tid == 0 && a.lse)
+    if (tid == 0 && p.raw)
+      p.raw_lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] = sum == 0.0f ? -INFINITY : top + log2f(sum);
+    else if (tid == 0 && a.lse)
       a.lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] =
           sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
     __syncthreads();
   }
 }
-
-const char* const kMe = "mk_paged_attention";
 
 // What follows from the shape fields alone: the build, the grid, the workspace.
 struct Plan {
@@ -145,17 +153,6 @@ size_t lay_out(Plan& pl, const Build* build, int sms, int per_sm) {
 // / 8 heads, 60 requests of 10 to 256 positions 18 and 36, to 700 (352 KB) 31 and 49, to 1500 (768 KB) 53 and 62; 150 of
 // these 103 and 133; 60 of 8 rows to 700 57 and 102; 256 wide to 700 (704 KB) 42 and 40.
 constexpr size_t kClusterBytes = 384 * 1024;
-
-mk_status check_shape(const mk_paged_attention_args& a, int device) {
-  if (a.rows < 1 || a.rows > 4096 || a.n_q_heads < 1 || a.n_q_heads > 4096 || a.n_kv_heads < 1 || a.n_q_heads % a.n_kv_heads)
-    return refuse(MK_ERR_INVALID_ARG, kMe, "rows %d, heads %d / %d", a.rows, a.n_q_heads, a.n_kv_heads);
-  if (a.head_dim < 16 || a.head_dim > 256 || a.head_dim % 16)
-    return refuse(MK_ERR_UNSUPPORTED, kMe, "head_dim %d is not a multiple of 16 in 16..256", a.head_dim);
-  if (a.dtype != MK_BF16 && a.dtype != MK_F16) return refuse(MK_ERR_UNSUPPORTED, kMe, "dtype %d", a.dtype);
-  if (a.cache_dtype != a.dtype && a.cache_dtype != MK_E4M3)
-    return refuse(MK_ERR_UNSUPPORTED, kMe, "cache dtype %d with dtype %d", a.cache_dtype, a.dtype);
-  return check_device(kMe, device);
-}
 
 cudaError_t plan(const mk_paged_attention_args& a, int device, Plan* out) {
   Plan& pl = *out;
@@ -236,65 +233,73 @@ cudaError_t join(const Params& p, const Plan& pl, cudaStream_t s) {
 }
 
 }  // namespace
-}  // namespace attn
-}  // namespace mkop
 
-extern "C" mk_status mk_paged_attention_workspace(const mk_paged_attention_args* p, int device, uint64_t* bytes) {
-  using namespace mkop;
-  using namespace mkop::attn;
-  if (!p || !bytes) return MK_ERR_INVALID_ARG;
-  if (mk_status s = check_shape(*p, device)) return s;
+mk_status check_shape(const char* me, const mk_paged_attention_args& a, int device) {
+  if (a.rows < 1 || a.rows > 4096 || a.n_q_heads < 1 || a.n_q_heads > 4096 || a.n_kv_heads < 1 || a.n_q_heads % a.n_kv_heads)
+    return refuse(MK_ERR_INVALID_ARG, me, "rows %d, heads %d / %d", a.rows, a.n_q_heads, a.n_kv_heads);
+  if (a.head_dim < 16 || a.head_dim > 256 || a.head_dim % 16)
+    return refuse(MK_ERR_UNSUPPORTED, me, "head_dim %d is not a multiple of 16 in 16..256", a.head_dim);
+  if (a.dtype != MK_BF16 && a.dtype != MK_F16) return refuse(MK_ERR_UNSUPPORTED, me, "dtype %d", a.dtype);
+  if (a.cache_dtype != a.dtype && a.cache_dtype != MK_E4M3)
+    return refuse(MK_ERR_UNSUPPORTED, me, "cache dtype %d with dtype %d", a.cache_dtype, a.dtype);
+  return check_device(me, device);
+}
+
+mk_status workspace_of(const char* me, const mk_paged_attention_args& a, int device, uint64_t* bytes) {
+  if (mk_status s = check_shape(me, a, device)) return s;
   DeviceGuard guard(device);
-  if (guard.err != cudaSuccess) return launched(kMe, guard.err);
+  if (guard.err != cudaSuccess) return launched(me, guard.err);
   Plan pl;
-  if (const cudaError_t e = plan(*p, device, &pl)) return launched(kMe, e);
+  if (const cudaError_t e = plan(a, device, &pl)) return launched(me, e);
   *bytes = pl.offer;
   return MK_OK;
 }
 
-extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream) {
-  using namespace mkop;
-  using namespace mkop::attn;
-  if (!args) return MK_ERR_INVALID_ARG;
-  Params p{};
-  p.a = *args;
-  const mk_paged_attention_args& a = p.a;
+mk_status check(const char* me, const mk_paged_attention_args& a, int device) {
   const bool e4m3 = a.cache_dtype == MK_E4M3;
   if (a.batch < 0 || a.batch > 1 << 24 || a.n_pages < 1 || a.page_size < 1 || a.max_pages < 1)
-    return refuse(MK_ERR_INVALID_ARG, kMe, "batch %d, n_pages %d, page_size %d, max_pages %d", a.batch, a.n_pages,
+    return refuse(MK_ERR_INVALID_ARG, me, "batch %d, n_pages %d, page_size %d, max_pages %d", a.batch, a.n_pages,
                   a.page_size, a.max_pages);
   // a tile may end past max_len, so that leaves room below 2^31
   if (static_cast<int64_t>(a.max_pages) * a.page_size > INT32_MAX - 1024)
-    return refuse(MK_ERR_UNSUPPORTED, kMe, "positions beyond 2^31 - 1024");
-  if (mk_status s = check_shape(a, device)) return s;
+    return refuse(MK_ERR_UNSUPPORTED, me, "positions beyond 2^31 - 1024");
+  if (mk_status s = check_shape(me, a, device)) return s;
   if (a.batch == 0) return MK_OK;
   if (!a.q || !a.k_pages || !a.v_pages || !a.table || !a.lens || !a.out || (e4m3 && (!a.k_scale || !a.v_scale)))
-    return refuse(MK_ERR_INVALID_ARG, kMe, "a required pointer is NULL");
-  if (a.table_stride < a.max_pages) return refuse(MK_ERR_INVALID_ARG, kMe, "table rows shorter than max_pages");
+    return refuse(MK_ERR_INVALID_ARG, me, "a required pointer is NULL");
+  if (a.table_stride < a.max_pages) return refuse(MK_ERR_INVALID_ARG, me, "table rows shorter than max_pages");
   if (!aligned({a.q, a.k_pages, a.v_pages, a.out, a.workspace}, 16))
-    return refuse(MK_ERR_INVALID_ARG, kMe, "a pointer is not 16-byte aligned");
+    return refuse(MK_ERR_INVALID_ARG, me, "a pointer is not 16-byte aligned");
   if (!aligned({a.table, a.lens, a.k_scale, a.v_scale, a.lse, a.status}, 4))
-    return refuse(MK_ERR_INVALID_ARG, kMe, "a misaligned pointer");
+    return refuse(MK_ERR_INVALID_ARG, me, "a misaligned pointer");
   // the stride of a dimension of one element is never used
   const int q_size[3] = {a.batch, a.rows, a.n_q_heads}, page_dims[3] = {a.n_pages, a.n_kv_heads, a.page_size};
   for (int i = 0; i < 3; ++i) {
     if (q_size[i] > 1 && (a.q_stride[i] % 8 || a.out_stride[i] % 8))
-      return refuse(MK_ERR_INVALID_ARG, kMe, "a stride is not a multiple of 8 elements");
+      return refuse(MK_ERR_INVALID_ARG, me, "a stride is not a multiple of 8 elements");
     if (page_dims[i] > 1 && (a.k_page_stride[i] % (e4m3 ? 16 : 8) || a.v_page_stride[i] % (e4m3 ? 16 : 8)))
-      return refuse(MK_ERR_INVALID_ARG, kMe, "a cache stride is not a multiple of 16 bytes");
+      return refuse(MK_ERR_INVALID_ARG, me, "a cache stride is not a multiple of 16 bytes");
     const int64_t k = page_dims[i] > 1 ? a.k_page_stride[i] : 0, v = page_dims[i] > 1 ? a.v_page_stride[i] : 0;
     const int64_t unit = e4m3 ? 16 : 8;  // elements of 16 bytes
     if (k < 0 || k / unit > UINT32_MAX || v < 0 || v / unit > UINT32_MAX)
-      return refuse(MK_ERR_UNSUPPORTED, kMe, "a cache stride is negative or 64 GB and more");
-    p.k_step[i] = static_cast<uint32_t>(k / unit);
-    p.v_step[i] = static_cast<uint32_t>(v / unit);
+      return refuse(MK_ERR_UNSUPPORTED, me, "a cache stride is negative or 64 GB and more");
   }
+  return MK_OK;
+}
+
+mk_status attend(const char* me, const mk_paged_attention_args& args, float* raw, float* raw_lse, int device, void* stream) {
+  if (mk_status s = check(me, args, device)) return s;
+  if (args.batch == 0) return MK_OK;
+  Params p{};
+  p.a = args;
+  const mk_paged_attention_args& a = p.a;
+  cache_steps(a.cache_dtype, a.n_pages, a.n_kv_heads, a.page_size, a.k_page_stride, a.v_page_stride, p.k_step, p.v_step);
   DeviceGuard guard(device);
-  if (guard.err != cudaSuccess) return launched(kMe, guard.err);
+  if (guard.err != cudaSuccess) return launched(me, guard.err);
   Plan pl;
-  if (const cudaError_t e = plan(a, device, &pl)) return launched(kMe, e);
+  if (const cudaError_t e = plan(a, device, &pl)) return launched(me, e);
   if (pl.bytes && (!a.workspace || a.workspace_bytes < static_cast<int64_t>(pl.bytes)))
-    return refuse(MK_ERR_INVALID_ARG, kMe, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), pl.bytes);
+    return refuse(MK_ERR_INVALID_ARG, me, "workspace of %lld bytes, %zu needed", static_cast<long long>(a.workspace_bytes), pl.bytes);
   char* ws = static_cast<char*>(a.workspace);
   p.page = div_by(a.page_size);
   p.group_div = div_by(pl.group);
@@ -308,8 +313,21 @@ extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_at);
   p.piece = reinterpret_cast<Piece*>(ws + pl.piece_at);
+  p.raw = raw;
+  p.raw_lse = raw_lse;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pl.build->launch(p, s);
   if (e == cudaSuccess && !pl.parts && pl.ctas > 1) e = a.dtype == MK_BF16 ? join<__nv_bfloat16>(p, pl, s) : join<__half>(p, pl, s);
-  return launched(kMe, e);
+  return launched(me, e);
+}
+
+}  // namespace attn
+}  // namespace mkop
+
+extern "C" mk_status mk_paged_attention_workspace(const mk_paged_attention_args* p, int device, uint64_t* bytes) {
+  return p && bytes ? mkop::attn::workspace_of("mk_paged_attention", *p, device, bytes) : MK_ERR_INVALID_ARG;
+}
+
+extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream) {
+  return args ? mkop::attn::attend("mk_paged_attention", *args, nullptr, nullptr, device, stream) : MK_ERR_INVALID_ARG;
 }

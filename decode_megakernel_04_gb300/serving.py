@@ -1,6 +1,6 @@
 """The serving operators of libmk (include/mk.h, "Serving operators") on torch tensors: page tables and slot maps,
-per-head norms with rotation and cache append, attention over a paged cache, and logit controls. Argument checks
-and marshalling only; every result is computed by the library's kernels.
+RMS norm with the residual's addition, per-head norms with rotation and cache append, attention over a paged cache (with a
+prefix that a batch shares, too), logit controls and verification of drafts by sampling. Argument checks and marshalling only; every result is computed by the library's kernels.
 
 Tensors live on one CUDA device and outputs are preallocated, as in ``Megakernel``; each call enqueues and returns.
 ``stream`` is a raw CUDA stream (an int, 0 = the legacy default stream); None takes torch's current stream of the
@@ -16,9 +16,10 @@ import struct
 
 import torch
 
-from .binding import (MK_OK, LogitControlsArgs, MKError, PagedAttentionArgs, PageTablesArgs, QkNormRopeArgs, load)
+from .binding import (MK_OK, LogitControlsArgs, MKError, PagedAttentionArgs, PageTablesArgs, PrefixAttentionArgs,
+                      QkNormRopeArgs, RmsNormArgs, VerifyDraftsArgs, load)
 
-OP_BAD_PAGE, OP_BAD_LENGTH, OP_NO_PAGES, OP_NO_ROOM, OP_TIMEOUT = 1, 2, 4, 8, 16
+OP_BAD_PAGE, OP_BAD_LENGTH, OP_NO_PAGES, OP_NO_ROOM, OP_TIMEOUT, OP_BAD_TOKEN = 1, 2, 4, 8, 16, 32
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 _I32, _I64, _F32, _F64 = torch.int32, torch.int64, torch.float32, torch.float64
@@ -38,7 +39,10 @@ def _packer(cls):
 _pack_tables = _packer(PageTablesArgs)
 _pack_qk = _packer(QkNormRopeArgs)
 _pack_attention = _packer(PagedAttentionArgs)
+_pack_prefix = _packer(PrefixAttentionArgs)
 _pack_logits = _packer(LogitControlsArgs)
+_pack_norm = _packer(RmsNormArgs)
+_pack_drafts = _packer(VerifyDraftsArgs)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -114,6 +118,33 @@ def page_tables(table, held, start, count, ring, ring_state, page_size: int, n_p
         _vector(lens, _I32, n, dev, "lens"), _vector(status, _I32, 1, dev, "status"), n, max_pages, page_size, n_pages,
         ring.numel(), places)
     _call(load().mk_page_tables, packed, dev, stream, "page_tables")
+
+
+def rms_norm(x, out, *, gain=None, residual=None, residual_out=None, eps: float = 1e-6, scales=None, stream=None) -> None:
+    """mk_rms_norm: h = x + residual, out = h / sqrt(mean(h^2) + eps) * gain, row by row.
+
+    x, residual, residual_out (receives h): [rows, width] bf16, fp16 or fp32, rows contiguous; gain: [width] of x's type.
+    out: [rows, width] of x's type, or float8_e4m3fn with scales float32 [rows, width / group]: each group of columns is
+    stored against its largest value / 448 (group: the whole row or 8, 16, 32, 64, 128, 256 columns). residual_out may be x
+    or residual, a 16- or 32-bit out may be x or residual."""
+    dev = x.get_device()
+    _need(dev >= 0 and x.dim() == 2, "rms_norm needs x [rows, width] on a CUDA device")
+    n, width = x.shape
+    dt, ot = x.dtype, out.dtype
+    _need(dt in _DTYPE and ot in _DTYPE, f"x of {dt}, out of {ot}")
+    xp, xs, _ = _rows(x, dt, n, dev, "x")
+    rp, rs, rw = _rows(residual, dt, n, dev, "residual")
+    hp, hs, hw = _rows(residual_out, dt, n, dev, "residual_out")
+    op, os_, ow = _rows(out, ot, n, dev, "out")
+    _need(ow == width and (residual is None or rw == width) and (residual_out is None or hw == width), "widths differ")
+    sp, ss, groups = _rows(scales, _F32, n, dev, "scales")
+    if ot is torch.float8_e4m3fn:
+        _need(groups > 0 and width % groups == 0, "8-bit results need scales [rows, width / group]")
+    else:
+        _need(scales is None, "scales are for 8-bit results")
+    packed = _pack_norm(xp, rp, _vector(gain, dt, width, dev, "gain"), hp, op, sp, xs, rs, hs, os_, ss, n, width,
+                        width // groups if groups else 0, _DTYPE[dt], _DTYPE[ot], eps)
+    _call(load().mk_rms_norm, packed, dev, stream, "rms_norm")
 
 
 _NO2, _NO3 = (0, 0), (0, 0, 0)
@@ -241,6 +272,49 @@ def paged_attention(q, k_pages, v_pages, table, lens, out, *, scale: float | Non
     _call(load().mk_paged_attention, packed, dev, stream, "paged_attention")
 
 
+def _pack_prefix_args(q, k_pages, v_pages, prefix_table, prefix_len, table, lens, out, scale, lse, k_scale, v_scale, dev):
+    """The argument struct's fields before the workspace's address and those after its size."""
+    head, tail = _pack_attention_args(q, k_pages, v_pages, table, lens, out, scale, lse, k_scale, v_scale, dev)
+    pages = prefix_table.numel()
+    prefix = (_vector(prefix_table, _I32, None, dev, "prefix_table"), _vector(prefix_len, _I32, 1, dev, "prefix_len"))
+    return head[:3] + prefix + head[3:], tail[:-3] + (pages,) + tail[-3:]
+
+
+def prefix_attention_workspace(q, k_pages, prefix_table, table) -> int:
+    """Bytes of device scratch prefix_attention needs for q, k_pages and tables of these shapes and types."""
+    dev = q.get_device()
+    _need(dev >= 0, "prefix_attention needs CUDA tensors")
+    lens = torch.empty(q.shape[0], dtype=_I32, device=q.device)
+    scale = torch.empty(k_pages.shape[1], dtype=_F32, device=q.device)
+    head, tail = _pack_prefix_args(q, k_pages, k_pages, prefix_table, prefix_table[:1], table, lens, q, None, None, scale,
+                                   scale, dev)
+    return _workspace_size(load().mk_prefix_attention_workspace, _pack_prefix(*head, 0, 0, 0, *tail), dev,
+                           "prefix_attention_workspace")
+
+
+def prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, table, lens, out, *, scale: float | None = None,
+                     lse=None, k_scale=None, v_scale=None, workspace=None, status=None, stream=None) -> None:
+    """mk_prefix_attention: attention of each request's newest R tokens over a prefix that all requests share and over the
+    request's own positions behind it; the prefix is read once for the whole batch.
+
+    prefix_table: int32 [pages] with prefix_len int32 [1], the shared positions; table: int32 [B, max_pages] and lens: int32
+    [B], each request's own positions with the R new ones (row r sees the prefix and lens - (R - 1 - r) of them). The rest is
+    paged_attention's. workspace: a uint8 tensor of prefix_attention_workspace bytes that no overlapping call uses; None
+    allocates what the call needs from torch's allocator (inside a graph capture: from the graph's pool)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("prefix_attention needs CUDA tensors")
+    head, tail = _pack_prefix_args(q, k_pages, v_pages, prefix_table, prefix_len, table, lens, out, scale, lse, k_scale,
+                                   v_scale, dev)
+    st = _vector(status, _I32, 1, dev, "status")
+    if workspace is None:
+        size = _workspace_size(load().mk_prefix_attention_workspace, _pack_prefix(*head, 0, st, 0, *tail), dev,
+                               "prefix_attention")
+        workspace = _workspace(size, q.device, dev, stream)
+    packed = _pack_prefix(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), st, workspace.numel(), *tail)
+    _call(load().mk_prefix_attention, packed, dev, stream, "prefix_attention")
+
+
 def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None, repetition=None, presence=None,
                    frequency=None, bias_ids=None, bias_vals=None, allowed=None, token=None, workspace=None,
                    stream=None) -> None:
@@ -293,5 +367,72 @@ def check_logit_controls(call) -> None:
     """Raises what the library would refuse of a prepared call, without enqueueing it."""
     _, packed, dev, _, what = call
     rc = load().mk_logit_controls_check(packed, dev)
+    if rc != MK_OK:
+        raise MKError(rc, f"{what} (details on stderr)")
+
+
+def _pack_drafts_args(logits, tokens, noise, uniforms, accept_out, draft_logits, n_drafts, temperature, positions, logprobs,
+                      dev):
+    """The argument struct's fields before the workspace's address and those after its size."""
+    _need(tokens.dim() == 2 and logits.dim() == 2, "tokens is [batch, rows] and logits [batch * rows, vocab]")
+    b, rows = tokens.shape
+    _need(rows >= 1, "a row at least")
+    dt = logits.dtype
+    _need(dt in _DTYPE, f"logits of {dt}")
+    lp, ls, vocab = _rows(logits, dt, b * rows, dev, "logits")
+    yp, ys, width = _rows(draft_logits, dt, b * (rows - 1), dev, "draft_logits")
+    np_, ns, tokens_of = _rows(noise, _F32, b, dev, "noise")
+    _need(tokens_of == vocab and (draft_logits is None or width == vocab), "vocabularies differ")
+    _need(uniforms is not None or rows == 1, "drafts need uniforms")
+    return ((lp, yp, _vector(tokens, _I32, b * rows, dev, "tokens"), _vector(n_drafts, _I32, b, dev, "n_drafts"),
+             _vector(positions, _I32, b, dev, "positions"), _vector(temperature, _F32, b, dev, "temperature"),
+             _vector(uniforms, _F32, b * (rows - 1), dev, "uniforms"), np_,
+             _vector(accept_out, _I32, 3 * b, dev, "accept_out"), _vector(logprobs, _F32, b * rows, dev, "logprobs")),
+            (ls, ys, ns, b, rows, vocab, _DTYPE[dt]))
+
+
+def verify_drafts_workspace(logits, tokens) -> int:
+    """Bytes of device scratch verify_drafts needs for logits [batch * rows, vocab] and tokens [batch, rows]."""
+    dev = logits.get_device()
+    _need(dev >= 0 and logits.dim() == 2 and tokens.dim() == 2 and logits.dtype in _DTYPE, "verify_drafts needs CUDA tensors")
+    packed = _pack_drafts(*(0,) * 10, 0, 0, 0, 0, 0, 0, *tokens.shape, logits.shape[1], _DTYPE[logits.dtype])
+    return _workspace_size(load().mk_verify_drafts_workspace, packed, dev, "verify_drafts_workspace")
+
+
+def verify_drafts(logits, tokens, noise, uniforms, accept_out, *, draft_logits=None, n_drafts=None, temperature=None,
+                  positions=None, logprobs=None, workspace=None, status=None, stream=None) -> None:
+    """mk_verify_drafts: how many of each request's drafted tokens to keep, and the token after them, by sampling.
+
+    logits: [B * R, vocab] fp32, bf16 or fp16, the target's; tokens: int32 [B, R], an anchor and its drafts; draft_logits: [B *
+    (R - 1), vocab] of the same type that the drafts were sampled from, None: drafts from elsewhere. noise: float32 [B, vocab]
+    from the exponential distribution, uniforms: float32 [B, R - 1] in [0, 1) (None for R = 1). temperature: float32 [B] (0:
+    greedy); n_drafts: int32 [B], drafts that a request has (R - 1 by default); positions: int32 [B]. accept_out: int32 [3, B]:
+    accepted rows, bonus token, next position; logprobs: float32 [B, R] of the emitted tokens. workspace: a uint8 tensor of
+    verify_drafts_workspace bytes that no overlapping call uses; None allocates it from torch's allocator."""
+    call, workspace = prepare_verify_drafts(logits, tokens, noise, uniforms, accept_out, draft_logits, n_drafts, temperature,
+                                            positions, logprobs, workspace, status, stream)
+    _call(*call)
+
+
+def prepare_verify_drafts(logits, tokens, noise=None, uniforms=None, accept_out=None, draft_logits=None, n_drafts=None,
+                          temperature=None, positions=None, logprobs=None, workspace=None, status=None, stream=None):
+    """verify_drafts' marshalling without its launch: (_call's arguments, the workspace, to be kept until the call)."""
+    dev = logits.get_device()
+    _need(dev >= 0, "verify_drafts needs CUDA tensors")
+    _need(noise is not None and accept_out is not None, "verify_drafts needs noise and accept_out")
+    head, tail = _pack_drafts_args(logits, tokens, noise, uniforms, accept_out, draft_logits, n_drafts, temperature, positions,
+                                   logprobs, dev)
+    st = _vector(status, _I32, 1, dev, "status")
+    if workspace is None:
+        size = _workspace_size(load().mk_verify_drafts_workspace, _pack_drafts(*head, 0, st, 0, *tail), dev, "verify_drafts")
+        workspace = _workspace(size, logits.device, dev, stream)
+    packed = _pack_drafts(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), st, workspace.numel(), *tail)
+    return (load().mk_verify_drafts, packed, dev, stream, "verify_drafts"), workspace
+
+
+def check_verify_drafts(call) -> None:
+    """Raises what the library would refuse of a prepared call, without enqueueing it."""
+    _, packed, dev, _, what = call
+    rc = load().mk_verify_drafts_check(packed, dev)
     if rc != MK_OK:
         raise MKError(rc, f"{what} (details on stderr)")

@@ -393,8 +393,9 @@ mk_status mk_decode_step_static(const mk_model_desc* desc, const mk_weights* wei
 /* ---- Serving operators ---------------------------------------------------------------------------
  * The step's own kinds of work (RoPE and cache append, grouped-query attention, the choice of the next
  * token) as calls of their own, over a PAGED cache, for serving programs that keep many ragged requests:
- * mk_page_tables (pages and slots from request lengths), mk_qk_norm_rope (per-head norms, rotation,
- * append), mk_paged_attention, mk_logit_controls. The source pages have no counterpart for these calls.
+ * mk_page_tables (pages and slots from request lengths), mk_rms_norm (between blocks), mk_qk_norm_rope (per-head
+ * norms, rotation, append), mk_paged_attention, mk_prefix_attention, mk_logit_controls, mk_verify_drafts. The source
+ * pages have no counterpart for these calls.
  *
  * They need no handle. Each takes its arguments as one struct, the device and a stream, enqueues its
  * kernels on that stream and returns without waiting; nothing is allocated, nothing is kept between
@@ -419,7 +420,8 @@ typedef enum mk_op_flag {
   MK_OP_BAD_LENGTH = 2, /* a length that is negative, inconsistent or beyond the table             */
   MK_OP_NO_PAGES = 4,   /* mk_page_tables: the ring holds fewer free pages than the step needs      */
   MK_OP_NO_ROOM = 8,    /* mk_page_tables: more new tokens than the slot map has places             */
-  MK_OP_TIMEOUT = 16    /* mk_paged_attention: a wait inside a CTA passed 2 s (a fault of the library) */
+  MK_OP_TIMEOUT = 16,   /* attention: a wait inside a CTA passed 2 s (a fault of the library)        */
+  MK_OP_BAD_TOKEN = 32  /* mk_verify_drafts: a drafted token outside the vocabulary                 */
 } mk_op_flag;
 
 #define MK_PAGE_TABLES_MAX_BATCH 4096
@@ -548,6 +550,50 @@ mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, vo
  * program's calls fits all of them. Reads the shape fields only (batch to cache_dtype), no pointer and no length. */
 mk_status mk_paged_attention_workspace(const mk_paged_attention_args* args, int device, uint64_t* bytes);
 
+/* Attention of the newest `rows` tokens of requests that share a prefix: mk_paged_attention where the first
+ * prefix_len positions of every request are the same pages (a system prompt, a document, samples forked from one prompt),
+ * which are read once for all requests instead of once for each.
+ * Row r of request b sees the prefix's positions 0 .. prefix_len - 1 and the request's own positions 0 .. lens[b] - (rows - 1
+ * - r) - 1 (none where that is negative: such a row is padding and sees the prefix alone); own position p lives on page
+ * table[b][p / page_size], so own pages begin a page of their own wherever the prefix ends. out and lse are of one softmax over both;
+ * a row that sees nothing gives out = 0 and lse = -infinity.
+ * prefix_len counts as within 0 .. max_prefix_pages * page_size (MK_OP_BAD_LENGTH). All else (types, scales, lengths, pages
+ * out of range, what unseen values may hold, infinities) is as in mk_paged_attention, and own positions are computed by it, in fp32 up to
+ * the sum of both parts. Over the prefix probabilities are rounded once to 16 bits before they meet the values (2^-8 of
+ * each in bf16, 2^-11 in fp16 and over e4m3 caches, which is at most what out's own rounding takes); fp16 ones below 2^-38 of a row's
+ * largest may vanish. Sums and statistics are fp32.
+ * The result does not depend on timing. `workspace`: mk_prefix_attention_workspace bytes of device scratch, 16-byte aligned, any
+ * contents; calls that may overlap need one each. Three launches, or four.
+ * Errors: as mk_paged_attention; batch * rows * n_q_heads / n_kv_heads beyond 2^24. */
+typedef struct mk_prefix_attention_args {
+  const void* q;               /* device [batch][rows][n_q_heads][head_dim], dtype                  */
+  const void* k_pages;         /* device, cache_dtype                                             */
+  const void* v_pages;
+  const int32_t* prefix_table; /* device [max_prefix_pages]                                       */
+  const int32_t* prefix_len;   /* device [1]                                                      */
+  const int32_t* table;        /* device [batch][table_stride], max_pages used per row              */
+  const int32_t* lens;         /* device [batch]: own positions in the cache, the new rows' included */
+  const float* k_scale;        /* device [n_kv_heads], e4m3 caches only                             */
+  const float* v_scale;
+  void* out;                   /* device [batch][rows][n_q_heads][head_dim], dtype                  */
+  float* lse;                  /* device [batch][rows][n_q_heads] contiguous, or NULL                 */
+  void* workspace;
+  int32_t* status;
+  int64_t workspace_bytes;
+  int64_t table_stride;
+  int64_t q_stride[3], out_stride[3];              /* batch, row, head                             */
+  int64_t k_page_stride[3], v_page_stride[3];      /* page, head, place                            */
+  int32_t batch, rows, n_q_heads, n_kv_heads, head_dim, n_pages, page_size, max_pages, max_prefix_pages;
+  int32_t dtype;               /* MK_BF16 or MK_F16                                               */
+  int32_t cache_dtype;         /* dtype or MK_E4M3                                                */
+  float scale;
+} mk_prefix_attention_args;
+mk_status mk_prefix_attention(const mk_prefix_attention_args* args, int device, void* stream);
+
+/* Bytes of workspace mk_prefix_attention needs for these arguments on `device`; never less for more requests or wider tables.
+ * Reads the shape fields only (batch to cache_dtype), no pointer and no length. */
+mk_status mk_prefix_attention_workspace(const mk_prefix_attention_args* args, int device, uint64_t* bytes);
+
 #define MK_LOGIT_MAX_HISTORY ((1 << 20) - 1)
 #define MK_LOGIT_MAX_BIASES 2047
 
@@ -594,6 +640,81 @@ mk_status mk_logit_controls_workspace(const mk_logit_controls_args* args, int de
 /* What mk_logit_controls would return for these arguments, short of enqueueing anything: every host-side argument error,
  * the workspace's among them. For callers that must know before they enqueue the step whose logits are controlled. */
 mk_status mk_logit_controls_check(const mk_logit_controls_args* args, int device);
+
+/* Root-mean-square norm of rows, with the residual's addition before it and, where asked, results in 8 bits.
+ *   h = x + residual                             (residual NULL: h = x); residual_out = h rounded to dtype
+ *   y = h / sqrt(mean(h^2) + eps) * gain         (gain NULL: 1)
+ *   out = y rounded to dtype; or out_dtype MK_E4M3: for each `group` columns s = max |y| / 448, scales = s and
+ *   out = the code of y / s (nearest even, saturating; s = 0: code 0)
+ * h, the mean square and y are fp32 (y is made of the unrounded h); each result is rounded once. Sums whose squares pass fp32
+ * (rows with elements of 2^60 and more, infinities or NaN): 16- and 32-bit results follow the formula with a mean of infinity or
+ * NaN, scales and codes of such a row are NaN.
+ * residual_out may be x or residual, and a 16- or 32-bit out may be x or residual (not both the same buffer), where the strides
+ * are the same; other overlaps are not allowed. One launch.
+ * Errors: width not a multiple of 8 in 8..32768; group not width or 8, 16, 32, 64, 128 or 256 dividing it; pointers not 16-byte
+ * aligned (scales: 4), strides not multiples of 8 elements or rows that overlap. */
+typedef struct mk_rms_norm_args {
+  const void* x;               /* device [rows][x_stride], dtype                                   */
+  const void* residual;        /* device [rows][residual_stride], dtype, or NULL                   */
+  const void* gain;            /* device [width], dtype, or NULL                                   */
+  void* residual_out;          /* device [rows][residual_out_stride], dtype, or NULL                 */
+  void* out;                   /* device [rows][out_stride], out_dtype                             */
+  float* scales;               /* device [rows][scales_stride], width / group used; MK_E4M3 only      */
+  int64_t x_stride, residual_stride, residual_out_stride, out_stride, scales_stride;
+  int32_t rows, width;
+  int32_t group;               /* columns of a scale; MK_E4M3 only                                 */
+  int32_t dtype;               /* MK_BF16, MK_F16 or MK_F32                                       */
+  int32_t out_dtype;           /* dtype or MK_E4M3                                                */
+  float eps;
+} mk_rms_norm_args;
+mk_status mk_rms_norm(const mk_rms_norm_args* args, int device, void* stream);
+
+/* How much of each request's drafts to keep, and the token after them, when tokens are sampled: each request's accepted
+ * prefix is distributed as if every token had been drawn from the target alone. Request b has `rows` rows of target logits (row
+ * 0 the anchor's, as a verify step of mk_decode_step writes them) and drafts tokens[b][1 .. n], n = n_drafts[b]. With T =
+ * temperature[b],
+ *   p_r = softmax(logits[b * rows + r] / T),  q_r = softmax(draft_logits[b * (rows - 1) + r] / T)  (draft_logits NULL: q_r is 1 at
+ *   the draft and 0 elsewhere: drafts that were not sampled)
+ * draft x = tokens[b][r + 1] is accepted while uniforms[b][r] * q_r(x) < p_r(x). With a accepted drafts, the bonus token is the
+ * one with the largest w_i / noise[b][i], w_i > 0 (the lowest index on ties), where w = max(p_a - q_a, 0) if draft a was refused (p_a if
+ * that is 0 everywhere) and w = p_a if a = n: for noise from the exponential distribution, a draw from w. T = 0 (or
+ * below, or NaN): p_r and q_r are 1 at the first largest logit, so drafts are accepted while they are the greedy token.
+ * accept_out is mk_verify_step's: accept_out[b] = a + 1 accepted rows, accept_out[batch + b] = the bonus token (-1 when every logit
+ * of its row is -infinity), accept_out[2 * batch + b] = positions[b] + a + 1.
+ * logprobs[b][r] = log p_r of the token that follows row r: the drafts r < a, the bonus token at a (-infinity for token -1), 0
+ * behind it.
+ * Temperatures above 0 count as within 2^-100 .. 2^100. Logits that are NaN count as -infinity; where a row has some of +infinity, these share it. Noise below 0 or NaN: the token is
+ * not drawn; 0: it comes before all others. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
+ * as within 0 .. rows - 1 (MK_OP_BAD_LENGTH).
+ * Weights and sums are fp32: where uniforms * q and p, or the two largest quotients, are within 2^-18 of each other,
+ * either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.
+ * `workspace`: mk_verify_drafts_workspace bytes of device scratch, 16-byte aligned, any contents; calls that may
+ * overlap need one each. Two launches. */
+typedef struct mk_verify_drafts_args {
+  const void* logits;          /* device [batch * rows][logits_stride], dtype                       */
+  const void* draft_logits;    /* device [batch * (rows - 1)][draft_stride], dtype, or NULL           */
+  const int32_t* tokens;       /* device [batch][rows]; entry 0 (the anchor) is not read             */
+  const int32_t* n_drafts;     /* device [batch] or NULL (= rows - 1)                               */
+  const int32_t* positions;    /* device [batch] or NULL (= 0)                                     */
+  const float* temperature;    /* device [batch] or NULL (= 1)                                     */
+  const float* uniforms;       /* device [batch][rows - 1], 0 <= u < 1; may be NULL when rows = 1      */
+  const float* noise;          /* device [batch][noise_stride]                                     */
+  int32_t* accept_out;         /* device [3][batch]                                               */
+  float* logprobs;             /* device [batch][rows] or NULL                                     */
+  void* workspace;
+  int32_t* status;
+  int64_t workspace_bytes;
+  int64_t logits_stride, draft_stride, noise_stride;
+  int32_t batch, rows, vocab;  /* rows 1 .. 64, batch * rows <= 2^20, vocab <= 2^24                   */
+  int32_t dtype;               /* MK_F32, MK_BF16 or MK_F16                                       */
+} mk_verify_drafts_args;
+mk_status mk_verify_drafts(const mk_verify_drafts_args* args, int device, void* stream);
+
+/* Bytes of workspace mk_verify_drafts needs (batch, rows and vocab decide; nothing is read through a pointer). */
+mk_status mk_verify_drafts_workspace(const mk_verify_drafts_args* args, int device, uint64_t* bytes);
+
+/* What mk_verify_drafts would return for these arguments, short of enqueueing anything. */
+mk_status mk_verify_drafts_check(const mk_verify_drafts_args* args, int device);
 
 #ifdef __cplusplus
 }
