@@ -14,10 +14,12 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mk_host.cu", "mk_kernel_dense.cu", "
 SOURCES += [os.path.join(OPS, f) for f in ("page_tables.cu", "rms_norm.cu", "qk_norm_rope.cu", "logit_controls.cu", "verify_drafts.cu", "prefix_attention.cu", "paged_attention.cu",
                                            "paged_attention_bf16.cu", "paged_attention_f16.cu",
                                            "paged_attention_e4m3_bf16.cu", "paged_attention_e4m3_f16.cu",
-                                           "paged_attention_tc_bf16.cu", "paged_attention_tc_f16.cu")]
+                                           "paged_attention_tc_bf16.cu", "paged_attention_tc_f16.cu",
+                                           "prefix_attention_bf16.cu", "prefix_attention_f16.cu",
+                                           "prefix_attention_e4m3_bf16.cu", "prefix_attention_e4m3_f16.cu")]
 HEADERS = [os.path.join(CSRC, "mk_internal.h"), os.path.join(CSRC, "mk_kernel.cuh"), os.path.join(INCLUDE, "mk.h")]
 HEADERS += [os.path.join(OPS, "mk_ops.cuh"), os.path.join(OPS, "paged_attention.cuh"),
-            os.path.join(OPS, "paged_attention_tc.cuh")]
+            os.path.join(OPS, "paged_attention_tc.cuh"), os.path.join(OPS, "prefix_attention.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",

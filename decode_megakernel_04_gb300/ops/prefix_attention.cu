@@ -1,188 +1,95 @@
 // mk_prefix_attention: attention of a batch over a prefix that its requests share and over each request's own positions.
 //
-// softmax over both parts is joined from parts: own positions by mk_paged_attention (results and their log-sums in fp32),
-// the prefix once for all query rows of a kv head, cut along its keys, and a last kernel that weights the parts of a row.
-#include <cuda_fp8.h>
-
-#include "paged_attention.cuh"
+// One softmax over both, joined from parts: own positions by mk_paged_attention (results and their log-sums in fp32), the
+// prefix once for all query rows of a kv head (prefix_attention.cuh), cut along its keys, and a last kernel that weights the
+// parts of a row.
+#include "prefix_attention.cuh"
 
 namespace mkop {
 namespace prefix {
 namespace {
 
-using attn::piece_begin;
-using attn::row_at;
-
-constexpr int kMinTiles = 2;   // of a piece at least
 constexpr int kJoinWarps = 8;
 
-struct Params {
-  mk_prefix_attention_args a;
-  Div page, group_div;
-  int group;          // query heads per kv head
-  int n_rows;         // query rows of a kv head: batch * rows * group
-  int blocks;         // of block_rows query rows
-  int block_rows;
-  int tile;           // keys
-  int ctas;           // pieces that the line is cut into at most
-  int max_len;
-  int dp;             // 64, 128 or 256
-  float scale_log2;
-  uint32_t k_step[3], v_step[3];  // the caches' strides (page, head, place) in units of 16 bytes
-  float* part;        // [ctas + kv heads * blocks][block_rows][dp] sums of a part
-  float2* part_ml;    // [..][block_rows] its base (log2 units) and sum
-  float* raw;         // [batch][rows][n_q_heads][dp] results over the own positions
-  float* raw_lse;     // [batch][rows][n_q_heads] their log-sums, log2 units
-};
-
-// The prefix as a line of tiles, one (kv head, row block) after the other, cut into `used` pieces. Piece c's part of item i
-// goes to slot c + i: along the line either grows by one from part to part.
-struct Line {
-  int len, tiles, used;
-  long long total;
-  __device__ explicit Line(const Params& p) {
-    len = min(max(p.a.prefix_len[0], 0), p.max_len);
-    tiles = (len + p.tile - 1) / p.tile;
-    total = static_cast<long long>(p.a.n_kv_heads) * p.blocks * tiles;
-    const long long worth = (total + kMinTiles - 1) / kMinTiles;
-    used = static_cast<int>(worth < p.ctas ? worth : p.ctas);
-  }
-  // the last piece that begins at or before tile x
-  __device__ int piece_of(long long x) const { return static_cast<int>(((x + 1) * used - 1) / total); }
-};
-
-constexpr int kRows = 16, kTile = 32, kThreads = 128;
-
-template <typename T>
-__device__ inline float element(const unsigned char* row, int i) { return static_cast<float>(reinterpret_cast<const T*>(row)[i]); }
-
-// One CTA per piece. A thread has one of 16 rows and every eighth key and column.
-template <typename T, typename Cache, int DP>
-__global__ void __launch_bounds__(kThreads) prefix_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float smem[];
-  float* q = smem;                         // [16][DP + 1]
-  float* kv = q + kRows * (DP + 1);        // [32][DP + 1]
-  float* prob = kv + kTile * (DP + 1);     // [16][32]
+// W warps for each row of out: the parts of the prefix and the result over the own positions, weighted by exp2(base - largest
+// base). Launched so that it may start while the prefix's kernel runs; it waits for that kernel's end, which waits for what
+// came before it.
+template <typename T, int W>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ PrefixParams p) {
+  __shared__ float4 part_sums[kJoinWarps][32];
+  __shared__ float part_sum[kJoinWarps];
   const mk_prefix_attention_args& a = p.a;
-  const int tid = threadIdx.x, row = tid >> 3, sub = tid & 7;
-  const Line line(p);
-  if (blockIdx.x == 0 && tid == 0 && line.len != a.prefix_len[0]) flag(a.status, MK_OP_BAD_LENGTH);
-  const int c = blockIdx.x;
-  if (c >= line.used) return;
-  const long long end = piece_begin(c + 1, line.total, line.used);
-  for (long long x = piece_begin(c, line.total, line.used); x < end;) {
-    const int item = static_cast<int>(x / line.tiles), t0 = static_cast<int>(x - static_cast<long long>(item) * line.tiles);
-    const int t1 = static_cast<int>(min(static_cast<long long>(line.tiles), t0 + end - x));
-    const int head = item / p.blocks, block = item - head * p.blocks;
-    __syncthreads();
-    for (int i = tid; i < kRows * DP; i += kThreads) {
-      const int r = i / DP, d = i % DP, m = block * kRows + r;
-      float v = 0;
-      if (m < p.n_rows && d < a.head_dim) {
-        const int br = p.group_div(m), h = head * p.group + m - br * p.group, b = br / a.rows, qr = br - b * a.rows;
-        v = static_cast<float>(static_cast<const T*>(a.q)[b * a.q_stride[0] + qr * a.q_stride[1] + h * a.q_stride[2] + d]);
-      }
-      q[r * (DP + 1) + d] = v;
-    }
-    float o[DP / 8], base = -INFINITY, sum = 0;
-    for (int i = 0; i < DP / 8; ++i) o[i] = 0;
-    const float scale = p.scale_log2 * (sizeof(Cache) == 1 ? a.k_scale[head] : 1.0f);
-    auto load = [&](const void* cache, const uint32_t (&step)[3], int key0) {
-      __syncthreads();
-      for (int i = tid; i < kTile * DP; i += kThreads) {
-        const int k = i / DP, d = i % DP, key = key0 + k;
-        float v = 0;
-        if (key < line.len && d < a.head_dim) {
-          const int pg = p.page(key), page = a.prefix_table[pg];
-          if (page >= 0 && page < a.n_pages) v = element<Cache>(row_at(cache, step, page, head, key - pg * a.page_size), d);
-          else flag(a.status, MK_OP_BAD_PAGE);
-        }
-        kv[k * (DP + 1) + d] = v;
-      }
-      __syncthreads();
-    };
-    for (int t = t0; t < t1; ++t) {
-      const int key0 = t * kTile;
-      load(a.k_pages, p.k_step, key0);
-      float s[4], top = base;
-      for (int j = 0; j < 4; ++j) {
-        const int k = sub + 8 * j;
-        float x = 0;
-        for (int d = 0; d < DP; ++d) x += q[row * (DP + 1) + d] * kv[k * (DP + 1) + d];
-        s[j] = key0 + k < line.len ? x * scale : -INFINITY;
-        top = fmaxf(top, s[j]);
-      }
-      for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      const float safe = top == -INFINITY ? 0.0f : top, shrink = exp2f(base - safe);
-      base = top;
-      sum *= shrink;
-      for (int i = 0; i < DP / 8; ++i) o[i] *= shrink;
-      for (int j = 0; j < 4; ++j) {
-        const float e = exp2f(s[j] - safe);
-        sum += e;
-        prob[row * kTile + sub + 8 * j] = e;
-      }
-      load(a.v_pages, p.v_step, key0);
-      for (int k = 0; k < kTile; ++k) {
-        const float e = prob[row * kTile + k];
-        for (int i = 0; i < DP / 8; ++i) o[i] += e * kv[k * (DP + 1) + sub + 8 * i];
-      }
-    }
-    for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-    const long long at = static_cast<long long>(c + item) * kRows + row;
-    for (int i = 0; i < DP / 8; ++i) p.part[at * DP + sub + 8 * i] = o[i];
-    if (sub == 0) p.part_ml[at] = make_float2(base, sum);
-    x += t1 - t0;
-  }
-}
-
-// A warp for each row of out: the parts of the prefix and the result over the own positions, weighted by exp2(base - largest base).
-template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
-  const mk_prefix_attention_args& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.batch) * a.rows * a.n_q_heads) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
+  const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / W) + warp / W;
+  const bool there = row < static_cast<long long>(a.batch) * a.rows * a.n_q_heads;  // (W = 8: the whole CTA)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!there) return;
   const int br = static_cast<int>(row / a.n_q_heads), h = static_cast<int>(row - static_cast<long long>(br) * a.n_q_heads);
-  const int head = h / p.group, m = br * p.group + h - head * p.group, block = m / p.block_rows;
+  const int head = h / p.group, m = br * p.group + h - head * p.group;
   const int b = br / a.rows, r = br - b * a.rows;
-  const Line line(p);
-  const long long item = static_cast<long long>(head) * p.blocks + block;
-  int c0 = 0, n = 0;
+  // the places of this row's sums: part k is place0 + k / subs, stream k % subs (or the row tile's own)
+  const int which = p.lane[1].blocks && m >= p.lane[1].first_row;
+  const Lane& ln = p.lane[which];
+  const int block = (m - ln.first_row) / ln.rows, in_block = m - ln.first_row - block * ln.rows;
+  const int subs = which ? p.streams : 1, stream = in_block / kTileRows, tile_row = in_block % kTileRows;
+  const Line line(p, ln);
+  const long long item = static_cast<long long>(head) * ln.blocks + block;
+  long long place0 = 0;
+  int n = 0;
   if (line.total) {
-    c0 = line.piece_of(item * line.tiles);
-    n = line.piece_of((item + 1) * line.tiles - 1) - c0 + 1;
+    const int c0 = line.piece_of(item * line.tiles);
+    n = (line.piece_of((item + 1) * line.tiles - 1) - c0 + 1) * subs;
+    place0 = ln.place0 + c0 + item;
   }
-  auto at = [&](int k) { return (c0 + k + item) * p.block_rows + m - block * p.block_rows; };
+  auto at = [&](int k) {
+    return ((place0 + (subs == 2 ? k >> 1 : k)) * p.streams + (subs == 2 ? k & 1 : stream)) * kTileRows + tile_row;
+  };
   const float own = p.raw_lse[row];
   float top = own;
   for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[at(k)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
   const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0;
-  for (int k = lane; k < n; k += 32) {
-    const float2 s = p.part_ml[at(k)];
-    sum += attn::exp2_fast(s.x - base) * s.y;
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  const float f_own = attn::exp2_fast(own - base);
-  sum += f_own;
-  const float scale = sum == 0.0f ? 0.0f : 1.0f / sum, vs = a.cache_dtype == MK_E4M3 ? a.v_scale[head] : 1.0f;
+  const float f_own = exp2_fast(own - base), vs = a.cache_dtype == MK_E4M3 ? a.v_scale[head] : 1.0f;
   T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2];
-  for (int d = lane * 4; d < a.head_dim; d += 128) {
+  float sum = 0;
+#pragma unroll 1
+  for (int d0 = 0; d0 < a.head_dim; d0 += 128) {
+    const int d = min(d0 + lane * 4, p.dp - 4);  // (64 wide: half of the lanes repeat the last columns)
     float4 y = make_float4(0, 0, 0, 0);
-    for (int k = 0; k < n; ++k) {
-      const float f = attn::exp2_fast(p.part_ml[at(k)].x - base);
+    sum = 0;
+#pragma unroll 4
+    for (int k = w; k < n; k += W) {
+      const float2 ml = p.part_ml[at(k)];
+      const float f = exp2_fast(ml.x - base);
+      sum += f * ml.y;
+      if (ml.y == 0.0f) continue;  // an empty part has no sums
       const float4 x = *reinterpret_cast<const float4*>(p.part + at(k) * p.dp + d);
       y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
     }
-    const float4 x = *reinterpret_cast<const float4*>(p.raw + row * p.dp + d);
-    y.x = y.x * vs + f_own * x.x, y.y = y.y * vs + f_own * x.y, y.z = y.z * vs + f_own * x.z, y.w = y.w * vs + f_own * x.w;
-    *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(y.x * scale, y.y * scale), pack2<T>(y.z * scale, y.w * scale));
+    if (W > 1) {
+      __syncthreads();
+      part_sums[warp][lane] = y;
+      if (lane == 0) part_sum[warp] = sum;
+      __syncthreads();
+      if (w == 0)
+        for (int k = 1; k < W; ++k) {
+          const float4 x = part_sums[warp + k][lane];
+          y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+          sum += part_sum[warp + k];
+        }
+    }
+    if (w == 0) {
+      sum += f_own;
+      const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+      float4 x = make_float4(0, 0, 0, 0);
+      if (f_own != 0.0f && d < a.head_dim) x = *reinterpret_cast<const float4*>(p.raw + row * p.dp + d);
+      y.x = (y.x * vs + f_own * x.x) * scale, y.y = (y.y * vs + f_own * x.y) * scale;
+      y.z = (y.z * vs + f_own * x.z) * scale, y.w = (y.w * vs + f_own * x.w) * scale;
+      if (d0 + lane * 4 < a.head_dim) *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
+    }
   }
-  if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+  if (w == 0 && lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
 }
 
 const char* const kMe = "mk_prefix_attention";
@@ -204,7 +111,8 @@ mk_paged_attention_args own_call(const mk_prefix_attention_args& a) {
 
 // What follows from the shape fields alone.
 struct Plan {
-  int group, n_rows, blocks, block_rows, tile, ctas, dp;
+  int group, n_rows, dp, streams;
+  Lane lane[2];
   uint64_t ml_at, raw_at, lse_at, own_at, bytes;
 };
 
@@ -225,32 +133,45 @@ mk_status plan(const mk_prefix_attention_args& a, int device, Plan* out) {
   pl.group = a.n_q_heads / a.n_kv_heads;
   pl.n_rows = a.batch * a.rows * pl.group;
   pl.dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
-  pl.block_rows = kRows;
-  pl.tile = kTile;
-  pl.blocks = (pl.n_rows + kRows - 1) / kRows;
+  pl.streams = pl.dp == 256 ? 1 : 2;
   int sms;
   if (const cudaError_t e = sm_count(device, &sms)) return launched(kMe, e);
-  pl.ctas = 4 * sms;
-  const uint64_t slots = pl.ctas + static_cast<uint64_t>(a.n_kv_heads) * pl.blocks, results = static_cast<uint64_t>(pl.n_rows) * a.n_kv_heads;
+  // Pairs of row tiles and single ones, their CTAs in proportion to their products.
+  const int tiles = (pl.n_rows + kTileRows - 1) / kTileRows, pairs = pl.streams == 2 ? tiles / 2 : 0, singles = tiles - 2 * pairs;
+  int ctas = pairs == 0 ? 0 : singles == 0 ? sms : (sms * 2 * pairs + pairs) / (2 * pairs + singles);
+  if (pairs && singles && ctas > sms - 1) ctas = sms - 1;
+  pl.lane[0] = {ctas, pairs, 0, 2 * kTileRows, 0};
+  pl.lane[1] = {singles ? sms - ctas : 0, singles, 2 * pairs * kTileRows, kTileRows, ctas + a.n_kv_heads * pairs};
+  const uint64_t places = sms + static_cast<uint64_t>(a.n_kv_heads) * (pairs + singles), results = static_cast<uint64_t>(pl.n_rows) * a.n_kv_heads;
   auto whole = [](uint64_t n) { return (n + 255) / 256 * 256; };
-  pl.ml_at = whole(slots * pl.block_rows * pl.dp * sizeof(float));
-  pl.raw_at = pl.ml_at + whole(slots * pl.block_rows * sizeof(float2));
+  const uint64_t rows = places * pl.streams * kTileRows;
+  pl.ml_at = whole(rows * pl.dp * sizeof(float));
+  pl.raw_at = pl.ml_at + whole(rows * sizeof(float2));
   pl.lse_at = pl.raw_at + whole(results * pl.dp * sizeof(float));
   pl.own_at = pl.lse_at + whole(results * sizeof(float));
   pl.bytes = pl.own_at + own;
   return MK_OK;
 }
 
-template <typename T, typename Cache, int DP>
-cudaError_t launch(const Params& p, int device, cudaStream_t s) {
-  constexpr int kSmem = (kRows * (DP + 1) + kTile * (DP + 1) + kRows * kTile) * 4;
-  if (const cudaError_t e = allow_smem<prefix_kernel<T, Cache, DP>>(device, kSmem)) return e;
-  return start(prefix_kernel<T, Cache, DP>, p.ctas, kThreads, kSmem, s, p);
+template <typename T, int W>
+cudaError_t join(const PrefixParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  const long long rows = static_cast<long long>(p.n_rows) * p.a.n_kv_heads;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows * W + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, W>, p);
 }
-template <typename T, typename Cache>
-cudaError_t launch(const Params& p, int device, cudaStream_t s) {
-  return p.dp == 64 ? launch<T, Cache, 64>(p, device, s) : p.dp == 128 ? launch<T, Cache, 128>(p, device, s)
-                                                                       : launch<T, Cache, 256>(p, device, s);
+template <typename T>
+cudaError_t join(const PrefixParams& p, cudaStream_t s) {
+  // a row has about this many parts at most
+  const int parts = (p.lane[0].ctas + p.lane[1].ctas) * p.streams / (p.a.n_kv_heads * (p.lane[0].blocks + p.lane[1].blocks)) + 1;
+  return parts > 8 ? join<T, 8>(p, s) : join<T, 1>(p, s);
 }
 
 }  // namespace
@@ -271,7 +192,7 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   using namespace mkop;
   using namespace mkop::prefix;
   if (!args) return MK_ERR_INVALID_ARG;
-  Params p{};
+  PrefixParams p{};
   p.a = *args;
   const mk_prefix_attention_args& a = p.a;
   if (mk_status s = check_shape(a, device)) return s;
@@ -295,28 +216,26 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   p.group_div = div_by(pl.group);
   p.group = pl.group;
   p.n_rows = pl.n_rows;
-  p.blocks = pl.blocks;
-  p.block_rows = pl.block_rows;
-  p.tile = pl.tile;
-  p.ctas = pl.ctas;
+  p.row_div = div_by(a.rows);
+  p.streams = pl.streams;
+  p.lane[0] = pl.lane[0];
+  p.lane[1] = pl.lane[1];
   p.max_len = a.max_prefix_pages * a.page_size;
   p.dp = pl.dp;
-  p.scale_log2 = a.scale * 1.44269504088896340736f;
-  attn::cache_steps(a.cache_dtype, a.n_pages, a.n_kv_heads, a.page_size, a.k_page_stride, a.v_page_stride, p.k_step, p.v_step);
+  p.scale_log2 = fabsf(a.scale) * 1.44269504088896340736f;
+  p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
+  cache_steps(a.cache_dtype, a.n_pages, a.n_kv_heads, a.page_size, a.k_page_stride, a.v_page_stride, p.k_step, p.v_step);
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_at);
   p.raw = reinterpret_cast<float*>(ws + pl.raw_at);
   p.raw_lse = reinterpret_cast<float*>(ws + pl.lse_at);
   own.workspace = ws + pl.own_at;
   own.workspace_bytes = a.workspace_bytes - static_cast<int64_t>(pl.own_at);
-  if (mk_status s = attn::attend(kMe, own, p.raw, p.raw_lse, device, stream)) return s;
+  if (mk_status s = attend(kMe, own, p.raw, p.raw_lse, device, stream)) return s;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = a.dtype == MK_BF16, e4m3 = a.cache_dtype == MK_E4M3;
-  cudaError_t e = bf ? e4m3 ? launch<__nv_bfloat16, __nv_fp8_e4m3>(p, device, s) : launch<__nv_bfloat16, __nv_bfloat16>(p, device, s)
-                     : e4m3 ? launch<__half, __nv_fp8_e4m3>(p, device, s) : launch<__half, __half>(p, device, s);
-  const long long results = static_cast<long long>(p.n_rows) * a.n_kv_heads;
-  const unsigned grid = static_cast<unsigned>((results + kJoinWarps - 1) / kJoinWarps);
-  if (e == cudaSuccess)
-    e = bf ? start(join_kernel<__nv_bfloat16>, grid, kJoinWarps * 32, 0, s, p) : start(join_kernel<__half>, grid, kJoinWarps * 32, 0, s, p);
+  cudaError_t e = e4m3 ? bf ? launch_prefix_e4m3_bf16(p, device, s) : launch_prefix_e4m3_f16(p, device, s)
+                       : bf ? launch_prefix_bf16(p, device, s) : launch_prefix_f16(p, device, s);
+  if (e == cudaSuccess) e = bf ? join<__nv_bfloat16>(p, s) : join<__half>(p, s);
   return launched(kMe, e);
 }

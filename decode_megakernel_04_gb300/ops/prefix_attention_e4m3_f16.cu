@@ -1,0 +1,8 @@
+// The shared prefix's kernels over e4m3 caches with fp16 queries.
+#include "prefix_attention.cuh"
+
+namespace mkop {
+namespace prefix {
+cudaError_t launch_prefix_e4m3_f16(const PrefixParams& p, int device, cudaStream_t s) { return launch_prefix<__half, __half, true>(p, device, s); }
+}  // namespace prefix
+}  // namespace mkop
