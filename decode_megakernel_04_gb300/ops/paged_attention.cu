@@ -21,7 +21,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const mk_paged_attention_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = blockIdx.x + 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Piece pc = p.piece[c];
   if (c >= pc.used) return;
@@ -58,15 +57,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
           const float g = __shfl_sync(~0u, f, k);
           y.x += g * x.x, y.y += g * x.y, y.z += g * x.z, y.w += g * x.w;
         }
-        if (p.raw)
-          *reinterpret_cast<float4*>(p.raw + ((static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h) * dp + d) =
-              make_float4(y.x * scale, y.y * scale, y.z * scale, y.w * scale);
-        else if (d < a.head_dim)
+        if (d < a.head_dim)
           *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(y.x * scale, y.y * scale), pack2<T>(y.z * scale, y.w * scale));
       }
-      if (lane == 0 && p.raw)
-        p.raw_lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] = sum == 0.0f ? -INFINITY : top + log2f(sum);
-      else if (lane == 0 && a.lse)
+      if (lane == 0 && a.lse)
         a.lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] =
             sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
     }
@@ -112,14 +106,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     for (int d = 2 * tid; d < a.head_dim; d += 2 * kJoinWarps * 32) {
       float x = 0, y = 0;
       for (int w = 0; w < kJoinWarps; ++w) x += sums[w][d], y += sums[w][d + 1];
-      if (p.raw)
-        *reinterpret_cast<float2*>(p.raw + ((static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h) * dp + d) = make_float2(x * f, y * f);
-      else
-        out[d / 2] = pack2<T>(x * f, y * f);
+      out[d / 2] = pack2<T>(x * f, y * f);
     }
-    if (tid == 0 && p.raw)
-      p.raw_lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] = sum == 0.0f ? -INFINITY : top + log2f(sum);
-    else if (tid == 0 && a.lse)
+    if (tid == 0 && a.lse)
       a.lse[(static_cast<long long>(pc.b) * a.rows + r) * a.n_q_heads + h] =
           sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
     __syncthreads();
@@ -246,16 +235,6 @@ mk_status check_shape(const char* me, const mk_paged_attention_args& a, int devi
   return check_device(me, device);
 }
 
-mk_status workspace_of(const char* me, const mk_paged_attention_args& a, int device, uint64_t* bytes) {
-  if (mk_status s = check_shape(me, a, device)) return s;
-  DeviceGuard guard(device);
-  if (guard.err != cudaSuccess) return launched(me, guard.err);
-  Plan pl;
-  if (const cudaError_t e = plan(a, device, &pl)) return launched(me, e);
-  *bytes = pl.offer;
-  return MK_OK;
-}
-
 mk_status check(const char* me, const mk_paged_attention_args& a, int device) {
   const bool e4m3 = a.cache_dtype == MK_E4M3;
   if (a.batch < 0 || a.batch > 1 << 24 || a.n_pages < 1 || a.page_size < 1 || a.max_pages < 1)
@@ -288,12 +267,33 @@ mk_status check(const char* me, const mk_paged_attention_args& a, int device) {
   return MK_OK;
 }
 
-mk_status attend(const char* me, const mk_paged_attention_args& args, float* raw, float* raw_lse, int device, void* stream) {
-  if (mk_status s = check(me, args, device)) return s;
-  if (args.batch == 0) return MK_OK;
+}  // namespace attn
+}  // namespace mkop
+
+extern "C" mk_status mk_paged_attention_workspace(const mk_paged_attention_args* p, int device, uint64_t* bytes) {
+  using namespace mkop;
+  using namespace mkop::attn;
+  static const char* me = "mk_paged_attention";
+  if (!p || !bytes) return MK_ERR_INVALID_ARG;
+  if (mk_status s = check_shape(me, *p, device)) return s;
+  DeviceGuard guard(device);
+  if (guard.err != cudaSuccess) return launched(me, guard.err);
+  Plan pl;
+  if (const cudaError_t e = plan(*p, device, &pl)) return launched(me, e);
+  *bytes = pl.offer;
+  return MK_OK;
+}
+
+extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream) {
+  using namespace mkop;
+  using namespace mkop::attn;
+  static const char* me = "mk_paged_attention";
+  if (!args) return MK_ERR_INVALID_ARG;
   Params p{};
-  p.a = args;
+  p.a = *args;
   const mk_paged_attention_args& a = p.a;
+  if (mk_status s = check(me, a, device)) return s;
+  if (a.batch == 0) return MK_OK;
   cache_steps(a.cache_dtype, a.n_pages, a.n_kv_heads, a.page_size, a.k_page_stride, a.v_page_stride, p.k_step, p.v_step);
   DeviceGuard guard(device);
   if (guard.err != cudaSuccess) return launched(me, guard.err);
@@ -314,21 +314,8 @@ mk_status attend(const char* me, const mk_paged_attention_args& args, float* raw
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_at);
   p.piece = reinterpret_cast<Piece*>(ws + pl.piece_at);
-  p.raw = raw;
-  p.raw_lse = raw_lse;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pl.build->launch(p, s);
   if (e == cudaSuccess && !pl.parts && pl.ctas > 1) e = a.dtype == MK_BF16 ? join<__nv_bfloat16>(p, pl, s) : join<__half>(p, pl, s);
   return launched(me, e);
-}
-
-}  // namespace attn
-}  // namespace mkop
-
-extern "C" mk_status mk_paged_attention_workspace(const mk_paged_attention_args* p, int device, uint64_t* bytes) {
-  return p && bytes ? mkop::attn::workspace_of("mk_paged_attention", *p, device, bytes) : MK_ERR_INVALID_ARG;
-}
-
-extern "C" mk_status mk_paged_attention(const mk_paged_attention_args* args, int device, void* stream) {
-  return args ? mkop::attn::attend("mk_paged_attention", *args, nullptr, nullptr, device, stream) : MK_ERR_INVALID_ARG;
 }

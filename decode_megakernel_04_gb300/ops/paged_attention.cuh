@@ -59,8 +59,6 @@ struct Params {
   float* part;      // [2 ctas][16 MT][DP] sums of a part
   float2* part_ml;  // [2 ctas][16 MT] its maximum (log2 units) and sum
   struct Piece* piece;  // [ctas]
-  float* raw;       // NULL, or [batch][rows][n_q_heads][DP]: where results go in fp32 instead of a.out
-  float* raw_lse;   // [batch][rows][n_q_heads], log2 units
 };
 
 // Where a CTA's piece of the line of tiles begins (written by every CTA for the join).
@@ -450,12 +448,6 @@ __global__ void __launch_bounds__(Shape<T, DP, MT, E4M3, LONG>::kThreads, Shape<
     if (d >= a.head_dim) return;
     const int mrow = block * S::kRows + row, r = p.group_div(mrow), h = head * p.group + mrow - r * p.group;
     const float f = sum == 0.0f ? 0.0f : (E4M3 ? a.v_scale[head] : 1.0f) / sum;
-    if (p.raw) {
-      const long long at = (static_cast<long long>(b) * a.rows + r) * a.n_q_heads + h;
-      *reinterpret_cast<float4*>(p.raw + at * DP + d) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
-      if (d == 0) p.raw_lse[at] = sum == 0.0f ? -INFINITY : top + log2f(sum);
-      return;
-    }
     const uint2 u = make_uint2(pack2<Out>(y.x * f, y.y * f), pack2<Out>(y.z * f, y.w * f));
     uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2] + d;
     *reinterpret_cast<uint2*>(out) = u;
@@ -835,12 +827,9 @@ inline const Build* pick(int dp, int mt, bool longer) {
   return &all[dp == 64 ? 0 : dp == 128 ? 1 : 2][mt - 1];
 }
 
-// mk_paged_attention, its host-side refusals (of the shape, and all short of the workspace's) and its workspace, in the name of
-// `me`. raw (with raw_lse): see Params.
+// mk_paged_attention's host-side refusals, in the name of `me`: of the shape, and all short of the workspace's.
 mk_status check_shape(const char* me, const mk_paged_attention_args& a, int device);
 mk_status check(const char* me, const mk_paged_attention_args& a, int device);
-mk_status attend(const char* me, const mk_paged_attention_args& a, float* raw, float* raw_lse, int device, void* stream);
-mk_status workspace_of(const char* me, const mk_paged_attention_args& a, int device, uint64_t* bytes);
 
 // The caches' strides (page, head, place) in units of 16 bytes; those of a dimension of one element are never used and 0 here.
 inline void cache_steps(int cache_dtype, int n_pages, int n_kv_heads, int page_size, const int64_t* k, const int64_t* v,

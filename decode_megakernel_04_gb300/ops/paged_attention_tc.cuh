@@ -678,18 +678,14 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
           for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
           if (lane == 0 && r < rows) {
             const int mrow = w.block * R + r, q = p.group_div(mrow), h = w.head * p.group + mrow - q * p.group;
-            const long long at = (static_cast<long long>(w.b) * a.rows + q) * a.n_q_heads + h;
-            if (whole && p.raw) {
-              out_of[r] = reinterpret_cast<unsigned char*>(p.raw + at * D);
-              sum_of[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
-              p.raw_lse[at] = sum == 0.0f ? -INFINITY : base_of[r] + log2f(sum);
-            } else if (whole) {
+            if (whole) {
               out_of[r] = reinterpret_cast<unsigned char*>(static_cast<T*>(a.out) + w.b * a.out_stride[0] + q * a.out_stride[1] + h * a.out_stride[2]);
               sum_of[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
-              if (a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (base_of[r] + log2f(sum)) * 0.693147180559945309f;
+              if (a.lse)
+                a.lse[(static_cast<long long>(w.b) * a.rows + q) * a.n_q_heads + h] =
+                    sum == 0.0f ? -INFINITY : (base_of[r] + log2f(sum)) * 0.693147180559945309f;
             } else {
               out_of[r] = reinterpret_cast<unsigned char*>(p.part + (slot * R + r) * D);
-              sum_of[r] = 1.0f;
               p.part_ml[slot * R + r] = make_float2(sum == 0.0f ? -INFINITY : base_of[r], sum);
             }
           }
@@ -717,8 +713,8 @@ __global__ void __launch_bounds__(TcShape<D, R>::kThreads, 1) tc_kernel(const __
 #pragma unroll
           for (int r = 0; r < RH; ++r) {
             if (r0 + r >= rows) break;
-            if (whole && !p.raw) reinterpret_cast<T*>(out_of[r0 + r])[h * 128 + t] = static_cast<T>(v[r] * sum_of[r0 + r]);
-            else reinterpret_cast<float*>(out_of[r0 + r])[h * 128 + t] = v[r] * sum_of[r0 + r];
+            if (whole) reinterpret_cast<T*>(out_of[r0 + r])[h * 128 + t] = static_cast<T>(v[r] * sum_of[r0 + r]);
+            else reinterpret_cast<float*>(out_of[r0 + r])[h * 128 + t] = v[r];
           }
         }
         tc_before();                 // the next part's first product comes after its first p_full

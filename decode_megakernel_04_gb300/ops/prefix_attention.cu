@@ -1,8 +1,5 @@
-// mk_prefix_attention: attention of a batch over a prefix that its requests share and over each request's own positions.
-//
-// One softmax over both, joined from parts: own positions by mk_paged_attention (results and their log-sums in fp32), the
-// prefix once for all query rows of a kv head (prefix_attention.cuh), cut along its keys, and a last kernel that weights the
-// parts of a row.
+// mk_prefix_attention: attention of a batch over a prefix that its requests share and over each request's own positions: the
+// arguments, and the second kernel, which joins a row's parts (prefix_attention.cuh has the first).
 #include "prefix_attention.cuh"
 
 namespace mkop {
@@ -11,46 +8,59 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-// W warps for each row of out: the parts of the prefix and the result over the own positions, weighted by exp2(base - largest
-// base). Launched so that it may start while the prefix's kernel runs; it waits for that kernel's end, which waits for what
-// came before it.
+// W warps for each row of out: its parts over the prefix and over its own keys, weighted by exp2(base - largest base). Launched
+// so that it may start while the first kernel runs, whose end it waits for.
 template <typename T, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ PrefixParams p) {
   __shared__ float4 part_sums[kJoinWarps][32];
-  __shared__ float part_sum[kJoinWarps];
   const mk_prefix_attention_args& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
-  const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / W) + warp / W;
-  const bool there = row < static_cast<long long>(a.batch) * a.rows * a.n_q_heads;  // (W = 8: the whole CTA)
+  const int row = blockIdx.x * (kJoinWarps / W) + warp / W;
+  const int br = p.q_head_div(row), h = row - br * a.n_q_heads, head = p.group_div(h), m = br * p.group + h - head * p.group;
+  const int b = p.row_div(br), r = br - b * a.rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!there) return;
-  const int br = static_cast<int>(row / a.n_q_heads), h = static_cast<int>(row - static_cast<long long>(br) * a.n_q_heads);
-  const int head = h / p.group, m = br * p.group + h - head * p.group;
-  const int b = br / a.rows, r = br - b * a.rows;
-  // the places of this row's sums: part k is place0 + k / subs, stream k % subs (or the row tile's own)
-  const int which = p.lane[1].blocks && m >= p.lane[1].first_row;
-  const Lane& ln = p.lane[which];
-  const int block = (m - ln.first_row) / ln.rows, in_block = m - ln.first_row - block * ln.rows;
-  const int subs = which ? p.streams : 1, stream = in_block / kTileRows, tile_row = in_block % kTileRows;
-  const Line line(p, ln);
-  const long long item = static_cast<long long>(head) * ln.blocks + block;
-  long long place0 = 0;
-  int n = 0;
-  if (line.total) {
-    const int c0 = line.piece_of(item * line.tiles);
-    n = (line.piece_of((item + 1) * line.tiles - 1) - c0 + 1) * subs;
-    place0 = ln.place0 + c0 + item;
+  if (br >= a.batch * a.rows) return;  // (W = 8: the whole CTA)
+  const Head hd = *p.head;
+  // Parts 0 .. n0 - 1 are over the prefix, n0 .. n - 1 over own keys. Part k of either is place0 + k / subs, stream k % subs (of a
+  // pair: its own stream).
+  const int pairs = p.blocks[kPairs], line = pairs && m < p.first_single() ? kPairs : kSingles;
+  const int in_line = line == kPairs ? m : m - p.first_single(), per_block = line == kPairs ? 2 * kTileRows : kTileRows;
+  const int block = in_line / per_block, in_block = in_line - block * per_block;
+  const int subs = line == kSingles ? p.streams : 1, own_subs = p.streams;
+  const long long item = static_cast<long long>(head) * p.blocks[line] + block;
+  long long place0 = item, own0 = 0;
+  int n0 = 0, n1 = 0;
+  if (hd.total[line]) {
+    const int c0 = Head::piece_of(item * hd.tiles, hd.total[line], hd.used[line]);
+    n0 = (Head::piece_of((item + 1) * hd.tiles - 1, hd.total[line], hd.used[line]) - c0 + 1) * subs;
+    place0 += c0 + (line == kSingles ? hd.used[kPairs] + static_cast<long long>(a.n_kv_heads) * pairs : 0);
   }
-  auto at = [&](int k) {
-    return ((place0 + (subs == 2 ? k >> 1 : k)) * p.streams + (subs == 2 ? k & 1 : stream)) * kTileRows + tile_row;
+  const int group = r / kGroupRows, bg = b * p.groups + group, own_m = (r - group * kGroupRows) * p.group + h - head * p.group;
+  const int own_row = own_m % kTileRows;
+  const long long cum = p.cum[bg], own_n = p.cum[bg + 1] - cum;
+  if (own_n) {
+    const int per = a.n_kv_heads * p.blocks[kOwn], hm = head * p.blocks[kOwn] + own_m / kTileRows;
+    const long long x = cum * per + hm * own_n;
+    const int c0 = Head::piece_of(x, hd.total[kOwn], hd.used[kOwn]);
+    n1 = (Head::piece_of(x + own_n - 1, hd.total[kOwn], hd.used[kOwn]) - c0 + 1) * own_subs;
+    own0 = c0 + static_cast<long long>(bg) * per + hm;
+  }
+  const int n = n0 + n1;
+  // the index of a part's row, and whether it is over own keys
+  auto at = [&](int k) -> long long {
+    if (k >= n0) return (own0 * own_subs + (k - n0)) * p.own_rows + own_row;
+    return (subs == p.streams ? place0 * p.streams + k : (place0 + k) * p.streams + in_block / kTileRows) * kTileRows + in_block % kTileRows;
   };
-  const float own = p.raw_lse[row];
-  float top = own;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[at(k)].x);
+  auto ml_of = [&](int k) { return (k < n0 ? p.part_ml : p.own_ml)[at(k)]; };
+  // A lane has a part: its base, its sum, where its row is. (Up to 32 are kept; more are read again.)
+  float2 mine = lane < n ? ml_of(lane) : make_float2(-INFINITY, 0.0f);
+  const float* from = lane < n ? (lane < n0 ? p.part : p.own) + at(lane) * p.dp : p.part;
+  float top = mine.x;
+  for (int k = lane + 32; k < n; k += 32) top = fmaxf(top, ml_of(k).x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
   const float base = top == -INFINITY ? 0.0f : top;
-  const float f_own = exp2_fast(own - base), vs = a.cache_dtype == MK_E4M3 ? a.v_scale[head] : 1.0f;
+  const float vs = a.cache_dtype == MK_E4M3 ? a.v_scale[head] : 1.0f;
   T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + r * a.out_stride[1] + h * a.out_stride[2];
   float sum = 0;
 #pragma unroll 1
@@ -58,34 +68,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const int d = min(d0 + lane * 4, p.dp - 4);  // (64 wide: half of the lanes repeat the last columns)
     float4 y = make_float4(0, 0, 0, 0);
     sum = 0;
-#pragma unroll 4
-    for (int k = w; k < n; k += W) {
-      const float2 ml = p.part_ml[at(k)];
-      const float f = exp2_fast(ml.x - base);
-      sum += f * ml.y;
-      if (ml.y == 0.0f) continue;  // an empty part has no sums
-      const float4 x = *reinterpret_cast<const float4*>(p.part + at(k) * p.dp + d);
-      y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      if (n > 32) {
+        const int k = k0 + lane;
+        mine = k < n ? ml_of(k) : make_float2(-INFINITY, 0.0f);
+        from = k < n ? (k < n0 ? p.part : p.own) + at(k) * p.dp : p.part;
+      }
+      const float weight = exp2_fast(mine.x - base);
+      sum += weight * mine.y;
+      // (an empty part has no sums: its weight is 0 and its row is not read)
+      const unsigned there = __ballot_sync(~0u, !(mine.y == 0.0f));
+#pragma unroll 8
+      for (int k = w; k < min(32, n - k0); k += W) {
+        const float f = __shfl_sync(~0u, weight, k);
+        const float* x_at = reinterpret_cast<const float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(from), k));
+        if (!(there >> k & 1)) continue;
+        const float4 x = *reinterpret_cast<const float4*>(x_at + d);
+        y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+      }
     }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
     if (W > 1) {
       __syncthreads();
       part_sums[warp][lane] = y;
-      if (lane == 0) part_sum[warp] = sum;
       __syncthreads();
       if (w == 0)
         for (int k = 1; k < W; ++k) {
           const float4 x = part_sums[warp + k][lane];
           y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
-          sum += part_sum[warp + k];
         }
     }
     if (w == 0) {
-      sum += f_own;
-      const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-      float4 x = make_float4(0, 0, 0, 0);
-      if (f_own != 0.0f && d < a.head_dim) x = *reinterpret_cast<const float4*>(p.raw + row * p.dp + d);
-      y.x = (y.x * vs + f_own * x.x) * scale, y.y = (y.y * vs + f_own * x.y) * scale;
-      y.z = (y.z * vs + f_own * x.z) * scale, y.w = (y.w * vs + f_own * x.w) * scale;
+      const float scale = sum == 0.0f ? 0.0f : vs / sum;
+      y.x *= scale, y.y *= scale, y.z *= scale, y.w *= scale;
       if (d0 + lane * 4 < a.head_dim) *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(y.x, y.y), pack2<T>(y.z, y.w));
     }
   }
@@ -94,7 +111,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 const char* const kMe = "mk_prefix_attention";
 
-// What mk_paged_attention is asked for the own positions.
+// The same call of mk_paged_attention over own positions alone: most refusals are its.
 mk_paged_attention_args own_call(const mk_prefix_attention_args& a) {
   mk_paged_attention_args o{};
   o.q = a.q, o.k_pages = a.k_pages, o.v_pages = a.v_pages, o.table = a.table, o.lens = a.lens, o.k_scale = a.k_scale;
@@ -111,9 +128,8 @@ mk_paged_attention_args own_call(const mk_prefix_attention_args& a) {
 
 // What follows from the shape fields alone.
 struct Plan {
-  int group, n_rows, dp, streams;
-  Lane lane[2];
-  uint64_t ml_at, raw_at, lse_at, own_at, bytes;
+  int group, n_rows, dp, streams, blocks[3], groups, own_rows, ctas;
+  uint64_t ml_at, own_at, own_ml_at, head_at, cum_at, bytes;
 };
 
 mk_status check_shape(const mk_prefix_attention_args& a, int device) {
@@ -121,6 +137,7 @@ mk_status check_shape(const mk_prefix_attention_args& a, int device) {
     return refuse(MK_ERR_INVALID_ARG, kMe, "batch %d, max_prefix_pages %d", a.batch, a.max_prefix_pages);
   if (mk_status s = attn::check_shape(kMe, own_call(a), device)) return s;
   const int64_t n_rows = static_cast<int64_t>(a.batch) * a.rows * (a.n_q_heads / a.n_kv_heads);
+  if (n_rows * a.n_kv_heads > INT32_MAX - 64) return refuse(MK_ERR_UNSUPPORTED, kMe, "2^31 rows and more");
   if (n_rows > 1 << 24) return refuse(MK_ERR_UNSUPPORTED, kMe, "%lld query rows of a kv head", static_cast<long long>(n_rows));
   return MK_OK;
 }
@@ -128,28 +145,29 @@ mk_status check_shape(const mk_prefix_attention_args& a, int device) {
 // check_shape() has passed
 mk_status plan(const mk_prefix_attention_args& a, int device, Plan* out) {
   Plan& pl = *out;
-  uint64_t own = 0;
-  if (mk_status s = attn::workspace_of(kMe, own_call(a), device, &own)) return s;
+  DeviceGuard guard(device);
+  if (guard.err != cudaSuccess) return launched(kMe, guard.err);
+  if (const cudaError_t e = sm_count(device, &pl.ctas)) return launched(kMe, e);
   pl.group = a.n_q_heads / a.n_kv_heads;
   pl.n_rows = a.batch * a.rows * pl.group;
   pl.dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
   pl.streams = pl.dp == 256 ? 1 : 2;
-  int sms;
-  if (const cudaError_t e = sm_count(device, &sms)) return launched(kMe, e);
-  // Pairs of row tiles and single ones, their CTAs in proportion to their products.
-  const int tiles = (pl.n_rows + kTileRows - 1) / kTileRows, pairs = pl.streams == 2 ? tiles / 2 : 0, singles = tiles - 2 * pairs;
-  int ctas = pairs == 0 ? 0 : singles == 0 ? sms : (sms * 2 * pairs + pairs) / (2 * pairs + singles);
-  if (pairs && singles && ctas > sms - 1) ctas = sms - 1;
-  pl.lane[0] = {ctas, pairs, 0, 2 * kTileRows, 0};
-  pl.lane[1] = {singles ? sms - ctas : 0, singles, 2 * pairs * kTileRows, kTileRows, ctas + a.n_kv_heads * pairs};
-  const uint64_t places = sms + static_cast<uint64_t>(a.n_kv_heads) * (pairs + singles), results = static_cast<uint64_t>(pl.n_rows) * a.n_kv_heads;
+  const int tiles = (pl.n_rows + kTileRows - 1) / kTileRows, own = (a.rows < kGroupRows ? a.rows : kGroupRows) * pl.group;
+  pl.blocks[kPairs] = pl.streams == 2 ? tiles / 2 : 0;
+  pl.blocks[kSingles] = tiles - 2 * pl.blocks[kPairs];
+  pl.blocks[kOwn] = (own + kTileRows - 1) / kTileRows;
+  pl.groups = (a.rows + kGroupRows - 1) / kGroupRows;
+  pl.own_rows = own < kTileRows ? own : kTileRows;
+  const uint64_t kv = a.n_kv_heads, groups = static_cast<uint64_t>(a.batch) * pl.groups;
+  const uint64_t rows = (pl.ctas + kv * (pl.blocks[kPairs] + pl.blocks[kSingles])) * pl.streams * kTileRows;
+  const uint64_t own_rows = (pl.ctas + groups * kv * pl.blocks[kOwn]) * pl.streams * pl.own_rows;
   auto whole = [](uint64_t n) { return (n + 255) / 256 * 256; };
-  const uint64_t rows = places * pl.streams * kTileRows;
   pl.ml_at = whole(rows * pl.dp * sizeof(float));
-  pl.raw_at = pl.ml_at + whole(rows * sizeof(float2));
-  pl.lse_at = pl.raw_at + whole(results * pl.dp * sizeof(float));
-  pl.own_at = pl.lse_at + whole(results * sizeof(float));
-  pl.bytes = pl.own_at + own;
+  pl.own_at = pl.ml_at + whole(rows * sizeof(float2));
+  pl.own_ml_at = pl.own_at + whole(own_rows * pl.dp * sizeof(float));
+  pl.head_at = pl.own_ml_at + whole(own_rows * sizeof(float2));
+  pl.cum_at = pl.head_at + whole(sizeof(Head));
+  pl.bytes = pl.cum_at + whole((groups + 1) * sizeof(long long));
   return MK_OK;
 }
 
@@ -169,9 +187,9 @@ cudaError_t join(const PrefixParams& p, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t join(const PrefixParams& p, cudaStream_t s) {
-  // a row has about this many parts at most
-  const int parts = (p.lane[0].ctas + p.lane[1].ctas) * p.streams / (p.a.n_kv_heads * (p.lane[0].blocks + p.lane[1].blocks)) + 1;
-  return parts > 8 ? join<T, 8>(p, s) : join<T, 1>(p, s);
+  // Few rows of many parts: 8 warps each.
+  const long long rows = static_cast<long long>(p.n_rows) * p.a.n_kv_heads;
+  return rows * 8 <= 16 * p.ctas * kJoinWarps ? join<T, 8>(p, s) : join<T, 1>(p, s);
 }
 
 }  // namespace
@@ -196,8 +214,7 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   p.a = *args;
   const mk_prefix_attention_args& a = p.a;
   if (mk_status s = check_shape(a, device)) return s;
-  mk_paged_attention_args own = own_call(a);
-  if (mk_status s = attn::check(kMe, own, device)) return s;
+  if (mk_status s = attn::check(kMe, own_call(a), device)) return s;
   if (static_cast<int64_t>(a.max_prefix_pages) * a.page_size > INT32_MAX - 1024)
     return refuse(MK_ERR_UNSUPPORTED, kMe, "positions beyond 2^31 - 1024");
   if (a.batch == 0) return MK_OK;
@@ -217,21 +234,24 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   p.group = pl.group;
   p.n_rows = pl.n_rows;
   p.row_div = div_by(a.rows);
-  p.streams = pl.streams;
-  p.lane[0] = pl.lane[0];
-  p.lane[1] = pl.lane[1];
-  p.max_len = a.max_prefix_pages * a.page_size;
+  p.q_head_div = div_by(a.n_q_heads);
+  p.max_prefix = a.max_prefix_pages * a.page_size;
+  p.max_own = a.max_pages * a.page_size;
   p.dp = pl.dp;
+  p.streams = pl.streams;
+  for (int i = 0; i < 3; ++i) p.blocks[i] = pl.blocks[i];
+  p.groups = pl.groups;
+  p.own_rows = pl.own_rows;
+  p.ctas = pl.ctas;
   p.scale_log2 = fabsf(a.scale) * 1.44269504088896340736f;
   p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
   cache_steps(a.cache_dtype, a.n_pages, a.n_kv_heads, a.page_size, a.k_page_stride, a.v_page_stride, p.k_step, p.v_step);
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml_at);
-  p.raw = reinterpret_cast<float*>(ws + pl.raw_at);
-  p.raw_lse = reinterpret_cast<float*>(ws + pl.lse_at);
-  own.workspace = ws + pl.own_at;
-  own.workspace_bytes = a.workspace_bytes - static_cast<int64_t>(pl.own_at);
-  if (mk_status s = attend(kMe, own, p.raw, p.raw_lse, device, stream)) return s;
+  p.own = reinterpret_cast<float*>(ws + pl.own_at);
+  p.own_ml = reinterpret_cast<float2*>(ws + pl.own_ml_at);
+  p.head = reinterpret_cast<Head*>(ws + pl.head_at);
+  p.cum = reinterpret_cast<long long*>(ws + pl.cum_at);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = a.dtype == MK_BF16, e4m3 = a.cache_dtype == MK_E4M3;
   cudaError_t e = e4m3 ? bf ? launch_prefix_e4m3_bf16(p, device, s) : launch_prefix_e4m3_f16(p, device, s)
