@@ -193,6 +193,37 @@ cudaError_t join(const PrefixParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t map_cache(CUtensorMap* map, const void* pages, const mk_prefix_attention_args& a, const int64_t* strides, int rows, bool e4m3) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const int size = e4m3 ? 1 : 2;
+  const int order[3] = {2, 1, 0};  // place, head, page
+  const int counts[3] = {a.n_pages, a.n_kv_heads, a.page_size};
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim)}, steps[3];
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = counts[order[i]];
+    // (a dimension of one element has no stride, but one is asked for)
+    steps[i] = counts[order[i]] > 1 ? strides[order[i]] * size : 16;
+  }
+  const cuuint32_t box[4] = {e4m3 ? 128u : 64u, static_cast<cuuint32_t>(rows), 1, 1}, ones[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(pages), dims,
+                            steps, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace prefix
 }  // namespace mkop
 
@@ -239,8 +270,12 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   p.max_own = a.max_pages * a.page_size;
   p.dp = pl.dp;
   p.streams = pl.streams;
-  for (int i = 0; i < 3; ++i) p.blocks[i] = pl.blocks[i];
+  for (int i = 0; i < 3; ++i) {
+    p.blocks[i] = pl.blocks[i];
+    p.block_div[i] = div_by(pl.blocks[i] ? pl.blocks[i] : 1);
+  }
   p.groups = pl.groups;
+  p.groups_div = div_by(pl.groups);
   p.own_rows = pl.own_rows;
   p.ctas = pl.ctas;
   p.scale_log2 = fabsf(a.scale) * 1.44269504088896340736f;

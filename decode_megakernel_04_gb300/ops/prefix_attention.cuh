@@ -10,21 +10,27 @@
 //   new rows) over its own keys. CTAs are dealt to the lines in proportion to their products, by a rule on the lengths alone.
 //   Where a CTA has one row tile, even and odd key tiles go to two sets of sums, so that there are two streams of work
 //   in any case (one 256 wide).
-// - Units: the product of one row tile and one key tile, in turn on two score buffers. One warp issues S(0), S(1), then
-//   for each unit u: O += P(u) V and S(u + 2): while one stream's softmax runs, the tensor cores work on the other.
+// - Units: the product of one row tile and one key tile. A warp for each stream issues S of its first unit, then for each
+//   unit O += P V and S of the next: while one stream's softmax runs, the tensor cores work on the other. (256 wide: one
+//   stream with two score buffers, S two units ahead.)
 // - Softmax: a thread has a row (128 threads a stream), so nothing is exchanged; its 128 scores are in registers at once.
 //   Probabilities go back to tensor memory over the first half of the scores' columns as the product's operand (16 bits).
 //   They are taken against a base that moves only when a score passes it by kPrefixGrow: else sums stay as they are.
-// - Loads: warps 9-11 copy keys, 12-14 values (cp.async, row by row through the page table) into a ring of slots; codes of e4m3
-//   caches pass through registers and become fp16 there. Queries are stored by the softmax threads; those of the next item
-//   while the last product of this one runs.
-// - Keys that not every row of a request's tile sees (at most 7): their values stay out of the product (they may hold
-//   anything, NaN too) and are added one by one at the item's end, by the rows that see them.
+// - Loads: warps for keys and for values copy boxes of a page's rows (TMA, through the page table) into a ring of slots
+//   each; a copy takes its warp 140 cycles, so the two 64-column pieces of a tile have a warp each. Over own keys few query rows
+//   leave room for a third tile, which memory's latency under load asks for. (Prefetches into L2 by warps of their own
+//   made it slower, 169 us against 127 for the 64 requests below.) Codes of e4m3 caches go through a stage of 64 rows, from
+//   where two warps each make fp16 of them. Queries are stored by the softmax threads; those of the next item while the last
+//   product of this one runs.
+// - Keys that not every row of a request's tile sees (at most 7) have probability 0 in the others. Should their values hold an
+//   infinity or NaN (0 times that is NaN), they are left out of the product and added one by one by the rows that see them.
 // Probabilities are one 16-bit number (a pair hi + lo would be half as much work again for the tensor cores). bf16: 2^-8 of each
 // at most; fp16: 2^-11, against a base 14 under the maximum, so that what falls under its range is 2^-39 of the largest. Sums of
 // probabilities are those of the unrounded ones.
 // Every wait has a limit (2 s), after which the CTA gives up, drains and frees what it holds and MK_OP_TIMEOUT is set.
 #pragma once
+#include <cuda.h>
+
 #include "paged_attention_tc.cuh"
 
 namespace mkop {
@@ -32,11 +38,19 @@ namespace prefix {
 
 using namespace attn;
 
+// a * b / c, in 32 bits where that holds the product (a division in 64 bits takes some hundred cycles)
+__device__ inline long long scaled(long long a, long long b, long long c) {
+  const unsigned long long ab = static_cast<unsigned long long>(a) * b;
+  return (ab | c) >> 32 ? static_cast<long long>(ab / c) : static_cast<uint32_t>(ab) / static_cast<uint32_t>(c);
+}
+
 constexpr int kPrefixTile = 128;      // keys
 constexpr int kTileRows = 128;        // query rows of a row tile
 constexpr int kGroupRows = 8;         // new rows of a request that share an item over its own keys
 constexpr int kMinPiece = 1;          // key tiles of a piece at least
 enum { kPairs, kSingles, kOwn };      // the lines
+// What a tile of a line, and an item over own keys, take of a CTA (in 250 cycles, 128 wide)
+constexpr int kPairCost = 12, kSingleCost = 7, kOwnCost = 7, kItemCost = 10;
 
 // What the first CTA writes for the join. Piece c's part of item i of a line goes to place c + i (after `place0`): along the line
 // either grows by one from part to part.
@@ -45,15 +59,14 @@ struct Head {
   int used[3];         // its pieces
   int tiles;           // key tiles of the prefix
   __device__ static int piece_of(long long x, long long total, int used) {  // the last piece that begins at or before tile x
-    if (total <= 0xffffffffu / static_cast<unsigned>(used))
-      return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(used) - 1) / static_cast<uint32_t>(total));
-    return static_cast<int>(((x + 1) * used - 1) / total);
+    const unsigned long long n = static_cast<unsigned long long>(x + 1) * used - 1;
+    return static_cast<int>((n | total) >> 32 ? n / total : static_cast<uint32_t>(n) / static_cast<uint32_t>(total));
   }
 };
 
 struct PrefixParams {
   mk_prefix_attention_args a;
-  Div page, group_div, row_div, q_head_div;
+  Div page, group_div, row_div, q_head_div, block_div[3], groups_div;
   int group;          // query heads per kv head
   int n_rows;         // query rows of a kv head: batch * rows * group
   int max_prefix, max_own;
@@ -72,11 +85,13 @@ struct PrefixParams {
   float2* own_ml;     // [places][streams][own_rows] over own keys
   Head* head;
   long long* cum;     // [batch * groups + 1] key tiles of the row groups so far (of one row tile)
+  int box;            // rows of a copied box: the largest power of two that divides the page size, up to the slot or stage
+  CUtensorMap keys, values;  // [n_pages][n_kv_heads][page_size][head_dim]
   __device__ int first_single() const { return blocks[kPairs] * 2 * kTileRows; }
   __device__ int rows_of(int group_index) const { return min(kGroupRows, a.rows - group_index * kGroupRows); }
   // Own keys of a row group: those its last row sees.
   __device__ int own_len(int bg) const {
-    const int b = bg / groups, g = bg - b * groups;
+    const int b = groups_div(bg), g = bg - b * groups;
     return max(0, min(max(a.lens[b], 0), max_own) - (a.rows - g * kGroupRows - rows_of(g)));
   }
   __device__ static int tiles_of(int len) { return (len + kPrefixTile - 1) >> 7; }
@@ -115,34 +130,32 @@ struct PrefixWalk {
     done += left();
     next_item();
   }
-  __device__ int kv_head() const { return hm / p.blocks[line]; }
+  __device__ int kv_head() const { return p.block_div[line](hm); }
   __device__ int block() const { return hm - kv_head() * p.blocks[line]; }
-  __device__ int request() const { return bg / p.groups; }
+  __device__ int request() const { return p.groups_div(bg); }
   __device__ int group_rows() const { return p.rows_of(bg - request() * p.groups); }
   __device__ int all_see() const { return line == kOwn ? len - (group_rows() - 1) : len; }  // keys before it are seen by every row
 };
 
-// Registers of a thread: 256 threads each of 512 launched with 128 (e4m3 loaders hold codes in registers)
-template <bool E4M3>
-constexpr int kSoftmaxRegs = E4M3 ? 176 : 192;
-template <bool E4M3>
-constexpr int kOtherRegs = E4M3 ? 72 : 56;
-
-template <int D>
+template <int D, bool E4M3>
 struct PrefixShape {
-  static constexpr int kThreads = 512, kLoaders = 96, kStreamThreads = 128;
+  static constexpr int kThreads = 512, kStreamThreads = 128;
+  // Registers of a thread after the launch's 128: the softmax's 256 threads and the others
+  static constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= 65536 / kThreads / 8 * 8 * kThreads, "of those launched with");
   static constexpr int kStreams = D == 256 ? 1 : 2;
   static constexpr int kHalves = D == 256 ? 2 : 1;          // slots of a tile's keys
   static constexpr int kWide = D == 256 ? 128 : D;          // columns of a slot
+  static constexpr int kPieces = kWide / 64;                // of 64 columns: [128 rows][128 bytes] each
   static constexpr int kSlot = kPrefixTile * kWide * 2;
-  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kKeySlots = D == 64 ? 4 : 2, kValueSlots = D == 64 ? 4 : 2;
+  static constexpr int kStageRows = 64, kStages = D == 256 ? 1 : 2, kStage = kStageRows * 128;  // codes
+  static constexpr int kConverters = 64;                    // threads, of keys and of values
   static constexpr int kQ = kTileRows * D * 2;              // a stream's queries
-  static constexpr int kOffQ = kSlots * kSlot;
-  static constexpr int kOffAddr = kOffQ + kStreams * kQ;    // address [2 roles][2 tiles][128]
-  // of keys that not all rows see: scores, float [2 streams][8][128]; values as they are in the cache, [streams][2 turns][8][D]
-  static constexpr int kOffLate = kOffAddr + 2 * 2 * 128 * 8;
-  static constexpr int kOffLateV = kOffLate + 2 * kGroupRows * 128 * 4;
-  static constexpr int kOffBar = kOffLateV + kStreams * 2 * kGroupRows * D * 2;
+  // Queries, keys' slots, values' slots. 128 wide, 16 bits, items of up to 64 or 32 rows: 5 or 6 slots and queries twice.
+  static constexpr bool kFewRows = D == 128 && !E4M3;
+  static constexpr int kOffStage = kFewRows ? 7 * kSlot : (kKeySlots + kValueSlots) * kSlot + kStreams * kQ;  // [keys, values][kStages]
+  static constexpr int kOffBar = kOffStage + (E4M3 ? 2 * kStages * kStage : 0);
   static constexpr int kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -152,10 +165,25 @@ constexpr float kPrefixLift = std::is_same<T, __half>::value ? 14.0f : 0.0f;  //
 template <typename T>
 constexpr float kPrefixGrow = std::is_same<T, __half>::value ? 1.0f : 8.0f;   // and moves when a score passes that by this
 
+// A place in a ring of slots and its barriers. There are as many barriers as slots, or twice as many where that is an odd number: two
+// streams use tiles in turn, and a stream that waits for every other turn of a barrier could not tell the one it waits
+// for from the one before the last.
+struct Ring {
+  uint32_t slots, bars, slot, bar, phase;
+  __device__ explicit Ring(uint32_t n) : slots(n), bars(n & 1 ? 2 * n : n), slot(0), bar(0), phase(0) {}
+  __device__ void next() {
+    if (++slot == slots) slot = 0;
+    if (++bar == bars) bar = 0, phase ^= 1;
+  }
+};
+
 struct PrefixBars {
-  uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], pv_done[2], late_full[2], drained;
+  uint64_t key_full[6], key_empty[6], value_full[6], value_empty[6], stage_full[4], stage_empty[4];
+  uint64_t q_full[4], s_full[2], p_full[2], pv_done[2], issued[2], tail[2], drained;
   uint32_t tmem;
   int dead;
+  alignas(4) uint8_t slow[16][4];  // of key tile j % 16, if not all rows see all of it: whether values are left out of a part of the product
+  uint8_t since[16];  // of key tile j % 16: how many of its item's tiles come before it in this piece (2: two and more)
 };
 static_assert(sizeof(PrefixBars) <= 512, "");
 
@@ -172,6 +200,14 @@ __device__ inline bool elected() {
 }
 // A value that all lanes have, as the warp's one value.
 __device__ inline uint32_t of_warp(uint32_t x) { return __reduce_max_sync(~0u, x); }
+__device__ inline void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+// One box into shared memory; what lies outside of the tensor is written as zeros.
+__device__ inline void copy_box(uint32_t to, const CUtensorMap* map, int column, int place, int head, int page, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+               "l"(map), "r"(column), "r"(place), "r"(head), "r"(page), "r"(smem_u32(bar)) : "memory");
+}
 // 64 consecutive fp32 columns of this warp's 32 lanes into v[at ..]. Load and wait are one statement: before the wait the
 // registers do not hold the values.
 __device__ inline void tc_ld64(float (&v)[128], int at, uint32_t addr) {
@@ -225,6 +261,12 @@ __device__ inline float max3(float a, float b, float c) {
   return d;
 }
 __device__ inline void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Whether one of a pair of 16-bit values is an infinity or NaN
+template <typename T>
+__device__ inline bool not_finite(uint32_t pair) {
+  constexpr uint32_t kMask = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  return (pair & kMask) == kMask || (pair >> 16 & kMask) == kMask;
+}
 // Instruction descriptor: fp32 sums, 16-bit operands, M = 128; `turned`: B is N-major
 template <typename T>
 __device__ constexpr uint32_t prefix_idesc(int n, bool turned) {
@@ -232,10 +274,19 @@ __device__ constexpr uint32_t prefix_idesc(int n, bool turned) {
   return 1u << 4 | type << 7 | type << 10 | (turned ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | (128u >> 4) << 24;
 }
 
+// Element d of a cached row.
+template <typename T, bool E4M3>
+__device__ inline float cached(const unsigned char* row, int d) {
+  if (!E4M3) return static_cast<float>(reinterpret_cast<const T*>(row)[d]);
+  uint32_t f[2];
+  e4m3_to_f16(f, row[d]);
+  return unpack2<__half>(f[0]).x;
+}
+
 // T: the products' type; QT: the queries'; E4M3: the cache holds codes (T is __half then)
 template <typename T, typename QT, int D, bool E4M3>
-__global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
-  using S = PrefixShape<D>;
+__global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using S = PrefixShape<D, E4M3>;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const uint32_t s0 = smem_u32(smem);
@@ -277,12 +328,13 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
     hd.total[kPairs] = static_cast<long long>(a.n_kv_heads) * p.blocks[kPairs] * hd.tiles;
     hd.total[kSingles] = static_cast<long long>(a.n_kv_heads) * p.blocks[kSingles] * hd.tiles;
     hd.total[kOwn] = own * per;
-    // A line's CTAs: in proportion to its products, one at least. (An item over own keys counts as a tile more: it is short.)
+    // A line's CTAs: in proportion to what its tiles and items take, one at least.
     const int ctas = gridDim.x;
-    const long long cost[3] = {2 * hd.total[kPairs], hd.total[kSingles],
-                               hd.total[kOwn] ? hd.total[kOwn] + static_cast<long long>(n_groups) * per : 0};
+    const long long cost[3] = {kPairCost * hd.total[kPairs], kSingleCost * hd.total[kSingles],
+                               hd.total[kOwn] ? kOwnCost * hd.total[kOwn] + kItemCost * static_cast<long long>(n_groups) * per : 0};
     const long long sum = cost[0] + cost[1] + cost[2];
-    int n0 = cost[0] ? max(1, static_cast<int>(cost[0] * ctas / sum)) : 0, n1 = cost[1] ? max(1, static_cast<int>(cost[1] * ctas / sum)) : 0;
+    int n0 = cost[0] ? max(1, static_cast<int>(scaled(cost[0], ctas, sum))) : 0;
+    int n1 = cost[1] ? max(1, static_cast<int>(scaled(cost[1], ctas, sum))) : 0;
     const int most = ctas - (cost[2] ? 1 : 0);
     if (n0 + n1 > most) (n0 > n1 ? n0 : n1) -= n0 + n1 - most;
     if (!cost[2]) (cost[1] ? n1 : n0) += most - n0 - n1;
@@ -294,7 +346,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
     }
     line = c < n0 ? kPairs : c < n0 + n1 ? kSingles : kOwn;
     c -= line == kPairs ? 0 : line == kSingles ? n0 : n0 + n1;
-    begin = hd.used[line] ? piece_begin(c, hd.total[line], hd.used[line]) : 0;
+    begin = hd.used[line] ? scaled(c, hd.total[line], hd.used[line]) : 0;  // (as piece_of() has it)
     if (blockIdx.x == 0) {
       if (tid == 0) {
         *p.head = hd;
@@ -305,7 +357,7 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
       for (int g = g0; g < g1; ++g) {
         p.cum[g] = at;
         at += PrefixParams::tiles_of(p.own_len(g));
-        const int b = g / p.groups;
+        const int b = p.groups_div(g);
         if (a.lens[b] < 0 || a.lens[b] > p.max_own) flag(a.status, MK_OP_BAD_LENGTH);
       }
     }
@@ -322,14 +374,19 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
     }
   }
   if (tid == 0) {
-    for (int i = 0; i < S::kSlots; ++i) bar_init(&bars.full[i], S::kLoaders), bar_init(&bars.empty[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&bars.q_full[i], S::kStreamThreads), bar_init(&bars.s_full[i], 1);
-      bar_init(&bars.p_full[i], S::kStreamThreads), bar_init(&bars.pv_done[i], 1);
-      bar_init(&bars.late_full[i], S::kStreamThreads);
+    for (int i = 0; i < 6; ++i) {
+      bar_init(&bars.key_full[i], E4M3 ? S::kConverters : S::kPieces), bar_init(&bars.key_empty[i], line == kPairs ? 2 : 1);
+      bar_init(&bars.value_full[i], E4M3 ? S::kConverters : S::kPieces), bar_init(&bars.value_empty[i], line == kPairs ? 2 : 1);
     }
-    bar_init(&bars.drained, 1);
+    for (int i = 0; i < 4; ++i) bar_init(&bars.stage_full[i], 1), bar_init(&bars.stage_empty[i], S::kConverters);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&bars.q_full[i], S::kStreamThreads), bar_init(&bars.q_full[2 + i], S::kStreamThreads), bar_init(&bars.s_full[i], 1);
+      bar_init(&bars.p_full[i], S::kStreamThreads), bar_init(&bars.pv_done[i], 1), bar_init(&bars.issued[i], 1);
+      bar_init(&bars.tail[i], 1);
+    }
+    bar_init(&bars.drained, S::kStreams);
     bars.dead = 0;
+    for (auto& x : bars.slow) *reinterpret_cast<uint32_t*>(x) = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (c >= hd.used[line]) return;
@@ -342,227 +399,314 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
   tc_after();
   const uint32_t tmem = bars.tmem;
   const bool pair = line == kPairs;
-  const long long count = piece_begin(c + 1, hd.total[line], hd.used[line]) - begin;  // key tiles of this piece
+  // how shared memory is dealt
+  const int few = S::kFewRows && line == kOwn ? p.own_rows <= 32 ? 32 : p.own_rows <= 64 ? 64 : 0 : 0;
+  const int q_rows = few ? few : kTileRows, key_slots = few ? 3 : S::kKeySlots, value_slots = few == 32 ? 3 : S::kValueSlots;
+  // A stream's queries: [q_turns][columns / 64][q_rows][128 bytes]. They come first: a product reads 128 rows of a piece, and what it reads
+  // behind fewer (rows that nothing is done with) has to be the CTA's memory, here slots.
+  const uint32_t q_turns = few ? 2 : 1, q_bytes = q_rows * D * 2, at_q = s0, at_k = s0 + S::kStreams * q_turns * q_bytes;
+  const uint32_t at_v = at_k + key_slots * S::kSlot;
+  const long long count = scaled(c + 1, hd.total[line], hd.used[line]) - begin;  // key tiles of this piece
   auto walk = [&]() -> PrefixWalk {
     PrefixWalk w{p, line, per, 0, 0, 0, prefix_len, hd.tiles, 0, 0, count};
     if (line == kOwn) {
       w.bg = at_bg;
       w.len = p.own_len(w.bg);
       w.n = PrefixParams::tiles_of(w.len);
-      w.hm = static_cast<int>(at_rem / w.n);
+      w.hm = static_cast<int>(scaled(at_rem, 1, w.n));
       w.tile = static_cast<int>(at_rem - static_cast<long long>(w.hm) * w.n);
       w.item = static_cast<long long>(w.bg) * per + w.hm;
     } else {
-      w.item = begin / hd.tiles;
+      w.item = scaled(begin, 1, hd.tiles);
       w.tile = static_cast<int>(begin - w.item * hd.tiles);
       w.hm = static_cast<int>(w.item);
     }
     return w;
   };
 
-  // (256 x (192 + 56) or 256 x (176 + 72) registers: 63488 of the 65536 of 512 x 128)
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<E4M3>));
-    if (warp >= 9 && warp < 15) {
-      // ---- loaders ------------------------------------------------------------------------------------------------
-      const bool value = warp >= 12;
-      const int t = tid - (value ? 384 : 288), barrier = value ? 3 : 2;
-      const unsigned char** addr = reinterpret_cast<const unsigned char**>(smem + S::kOffAddr) + (value ? 256 : 0);
-      PrefixWalk w = walk();  // at the next tile that gets addresses
-      auto look_up = [&](int key) -> int {
-        key += w.tile * kPrefixTile;
-        if (w.ends() || key >= w.len) return -1;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+    constexpr int kSecondIssuer = E4M3 ? 15 : 11;
+    const bool loader = E4M3 ? warp == 9 || warp == 10 : warp == 9 || warp == 12 || (S::kPieces == 2 && (warp == 10 || warp == 13));
+    if (loader) {
+      // ---- loaders: keys, values --------------------------------------------------------------------------------------
+      const bool value = E4M3 ? warp == 10 : warp >= 12;
+      const int piece = E4M3 ? 0 : warp - (value ? 12 : 9);  // 64 columns of a slot's
+      uint64_t* full = E4M3 ? bars.stage_full + 2 * value : value ? bars.value_full : bars.key_full;
+      uint64_t* empty = E4M3 ? bars.stage_empty + 2 * value : value ? bars.value_empty : bars.key_empty;
+      // A turn is a slot, or 64 rows of one on their way through a stage.
+      constexpr int kRows = E4M3 ? S::kStageRows : kPrefixTile, kParts = kPrefixTile / kRows;
+      Ring ring(E4M3 ? S::kStages : value ? value_slots : key_slots), freed = ring;
+      const uint32_t base = E4M3 ? s0 + S::kOffStage + value * S::kStages * S::kStage : value ? at_v : at_k;
+      constexpr uint32_t kBytes = E4M3 ? S::kStage : S::kSlot;
+      const CUtensorMap* map = value ? &p.values : &p.keys;
+      const int box = of_warp(p.box);
+      PrefixWalk w = walk();
+      long long since = 0;
+      uint32_t turn = 0, tails = 0;
+      bool ok = true;
+      // The pages of 32 boxes of walk w's tile, one a lane, looked up a tile ahead. (A copy of many lanes is issued as one each, 140
+      // cycles; by one lane with operands handed over it took 440.)
+      auto pages_from = [&](int first) -> int {
+        const int at = (first + lane) * box, key = w.tile * kPrefixTile + at;
+        if (at >= kPrefixTile || key >= w.len) return -1;
         return line == kOwn ? a.table[w.request() * a.table_stride + p.page(key)] : a.prefix_table[p.page(key)];
       };
-      auto make_address = [&](const unsigned char** at, int page, int i) {
-        const unsigned char* from = kZeros;
-        const int key = w.tile * kPrefixTile + i;
-        if (!w.ends() && key < w.len) {
-          if (page < 0 || page >= a.n_pages) {
-            flag(a.status, MK_OP_BAD_PAGE);
-          } else if (!value || key < w.all_see()) {
-            const int place = key - p.page(key) * a.page_size, head = w.kv_head();
-            from = value ? row_at(a.v_pages, p.v_step, page, head, place) : row_at(a.k_pages, p.k_step, page, head, place);
+      int page = pages_from(0), held = 0;
+      for (long long j = 0; ok && j < count; ++j) {
+        const int key0 = of_warp(w.tile * kPrefixTile), head = of_warp(w.kv_head()), len = of_warp(w.len), all_see = w.all_see();
+        const bool tail = !E4M3 && value && key0 + kPrefixTile > all_see;
+        const long long item = w.item;
+#pragma unroll 1
+        for (int h = 0; ok && h < S::kHalves; ++h) {
+#pragma unroll 1
+          for (int part = 0; ok && part < kParts; ++part, ++turn) {
+            if (turn >= ring.slots) {
+              ok = __all_sync(~0u, bar_wait(&empty[freed.bar], freed.phase, dead));
+              freed.next();
+            }
+            if (!ok) break;
+            const int row0 = part * kRows, end = min(len - key0, row0 + kRows);  // rows with keys
+            uint64_t* bar = tail ? &bars.tail[piece] : &full[ring.bar];
+            if (lane == 0) {
+              if (!E4M3 && !value && piece == 0) bars.since[j & 15] = static_cast<uint8_t>(since);
+              bar_expect(bar, max((end - row0 + box - 1) / box, 0) * box * 128);
+            }
+            __syncwarp();
+            const uint32_t to = base + ring.slot * kBytes + piece * (kPrefixTile * 128);
+#pragma unroll 1
+            for (int i = row0 / box & ~31; i * box < end; i += 32) {
+              if (held != i) held = i, page = pages_from(i);
+              const int row = (i + lane) * box, key = key0 + row;
+              if (row < row0 || row >= end) continue;
+              int id = page;
+              if (id < 0 || id >= a.n_pages) {
+                flag(a.status, MK_OP_BAD_PAGE);
+                id = a.n_pages;  // outside of the tensor: zeros
+              }
+              copy_box(to + (row - row0) * 128, map, h * S::kWide + piece * 64, key - p.page(key) * a.page_size, head, id, bar);
+            }
+            __syncwarp();
+            if (tail) {
+              // Rows that are not there have to be zeros (0 times what they hold may be NaN), and so those that not every row sees,
+              // if they hold such values.
+              ok = __all_sync(~0u, bar_wait(bar, tails++ & 1, dead));
+              uint4* at = reinterpret_cast<uint4*>(smem + (to - s0));  // 8 a row
+              bool bad = false;
+#pragma unroll 1
+              for (int i = max(all_see - key0, 0) * 8 + lane; i < end * 8; i += 32) {
+                const uint4 x = at[i];
+                bad |= not_finite<T>(x.x) || not_finite<T>(x.y) || not_finite<T>(x.z) || not_finite<T>(x.w);
+              }
+              bad = __any_sync(~0u, bad);
+              if (lane == 0) bars.slow[j & 15][h * 2 + piece] = bad;
+#pragma unroll 1
+              for (int i = (bad ? max(all_see - key0, 0) : end) * 8 + lane; i < kPrefixTile * 8; i += 32) at[i] = make_uint4(0, 0, 0, 0);
+              proxy_fence();
+              __syncwarp();
+              if (lane == 0) bar_arrive(&full[ring.bar]);
+            }
+            ring.next();
           }
         }
-        at[i] = from;
-      };
-      const bool two = t < 128 - S::kLoaders;
+        w.next();
+        since = w.item != item ? 0 : min(since + 1, 2ll);
+        if (!w.ends()) page = pages_from(0), held = 0;
+      }
+      // What has been asked for lands before the CTA's memory goes: the last turns, from the oldest one on.
+      int alive = 0;
+      for (uint32_t i = 0; i < min(turn, ring.slots); ++i, freed.next()) bar_wait(&full[freed.bar], freed.phase, &alive);
+    } else if (E4M3 && warp >= 11 && warp < 15) {
+      // ---- converters: codes of a stage become a slot's fp16 values -------------------------------------------------------
+      const bool value = warp >= 13;
+      const int t = tid - (value ? 416 : 352);
+      Ring ring(value ? value_slots : key_slots), freed = ring;
+      uint64_t *full = value ? bars.value_full : bars.key_full, *empty = value ? bars.value_empty : bars.key_empty;
+      PrefixWalk w = walk();
+      long long since = 0;
+      uint32_t turn = 0;
+      Ring stage(S::kStages);
       bool ok = true;
-      make_address(addr, look_up(t), t);
-      if (two) make_address(addr, look_up(t + S::kLoaders), t + S::kLoaders);
-      w.next();
-      int page = look_up(t), page2 = two ? look_up(t + S::kLoaders) : -1;
-      constexpr int kSrc = E4M3 ? S::kWide / 16 : S::kWide / 8;  // 16-byte pieces of a slot's row in the cache
-      constexpr int kStep = S::kLoaders / kSrc, kTurns = (kPrefixTile + kStep - 1) / kStep;
+      constexpr int kSrc = S::kWide / 16, kStep = S::kConverters / kSrc;
       const int chunk = t % kSrc, row0 = t / kSrc;
-      for (long long j = 0; j < count; ++j) {
-        const unsigned char** at = addr + (j & 1) * 128;
-        if (any_of(barrier, S::kLoaders, !ok)) break;
+      for (long long j = 0; ok && j < count; ++j) {
+        const int key0 = w.tile * kPrefixTile;
+        const int all_see = w.all_see() - key0, end = w.len - key0;
 #pragma unroll 1
-        for (int h = 0; h < S::kHalves; ++h) {
-          const uint32_t g = (static_cast<uint32_t>(j) * 2 + (value ? 1 : 0)) * S::kHalves + h;
-          const int slot = g % S::kSlots, turn = (g / S::kSlots) & 1;
-          const bool waits = j >= S::kSlots / (2 * S::kHalves);         // the slot has been used before
-          const int column = h * S::kWide * (E4M3 ? 1 : 2) + chunk * 16;  // bytes
-          const bool in = column < a.head_dim * (E4M3 ? 1 : 2);         // columns behind the head are not read, or not used
-          const unsigned char* const* from = at + row0;
-          if (!E4M3) {
-            if (waits) ok = bar_wait(&bars.empty[slot], turn ^ 1, dead) && ok;
-            const uint32_t to = s0 + slot * S::kSlot + (chunk >> 3) * (kPrefixTile * 128);
-            if (in)
+        for (int h = 0; ok && h < S::kHalves; ++h, ++turn) {
+          if (turn >= ring.slots) {
+            ok = __all_sync(~0u, bar_wait(&empty[freed.bar], freed.phase, dead));
+            freed.next();
+          }
+          unsigned char* to = smem + ((value ? at_v : at_k) - s0) + ring.slot * S::kSlot + (chunk >> 2) * (kPrefixTile * 128);
+#pragma unroll 1
+          for (int part = 0; ok && part < kPrefixTile / S::kStageRows; ++part, stage.next()) {
+            ok = __all_sync(~0u, bar_wait(&bars.stage_full[2 * value + stage.bar], stage.phase, dead));
+            if (!ok) break;
+            const unsigned char* codes = smem + S::kOffStage + (value * S::kStages + stage.slot) * S::kStage;
+            const unsigned char* from = codes + row0 * 128 + chunk * 16;
+            int live = value ? end : kPrefixTile;  // rows from there on are zeros (see the loaders; each warp looks at all of them)
+            if (value && all_see < end && all_see < kPrefixTile) {
+              const int first = max(all_see, part * S::kStageRows), last = min(min(end, kPrefixTile), (part + 1) * S::kStageRows);
+              bool bad = false;
+              for (int i = first * 32 + lane; i < last * 32; i += 32) {  // four codes
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(codes + (i - part * S::kStageRows * 32) * 4);
 #pragma unroll
-              for (int i = 0; i < kTurns; ++i) {
-                const int row = row0 + kStep * i;
-                if (row >= kPrefixTile) break;
-                cp16(to + row * 128 + (((chunk ^ row) & 7) << 4), from[kStep * i] + column);
+                for (int k = 0; k < 32; k += 8) bad |= (x >> k & 0x7f) == 0x7f && (i & 31) * 4 + k / 8 < a.head_dim - h * S::kWide;
               }
-            cp_arrive(&bars.full[slot]);
-          } else {
-            constexpr int kAhead = kTurns < 6 ? kTurns : 6;  // loads in flight
-            uint4 u[kAhead];
-            auto fetch = [&](int i) {
-              if (row0 + kStep * i < kPrefixTile)
-                u[i % kAhead] = in ? *reinterpret_cast<const uint4*>(from[kStep * i] + column) : make_uint4(0, 0, 0, 0);
-            };
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) fetch(i);
-            if (waits) ok = bar_wait(&bars.empty[slot], turn ^ 1, dead) && ok;
-            // codes 16 chunk .. become pieces 2 chunk and 2 chunk + 1
-            unsigned char* to = smem + slot * S::kSlot + (chunk >> 2) * (kPrefixTile * 128);
-#pragma unroll
-            for (int i = 0; i < kTurns; ++i) {
-              const int row = row0 + kStep * i;
-              if (row >= kPrefixTile) break;
-              const uint4 x = u[i % kAhead];
-              if (i + kAhead < kTurns) fetch(i + kAhead);
+              bad = __any_sync(~0u, bad);
+              if (bad) live = all_see;
+              if (t == 0) bars.slow[j & 15][h * 2 + part] = bad;
+            }
+#pragma unroll 4
+            for (int i = 0; i < S::kStageRows / kStep; ++i) {
+              const int row = part * S::kStageRows + row0 + i * kStep;
+              uint4 x = *reinterpret_cast<const uint4*>(from + i * kStep * 128);
+              if (row >= live) x = make_uint4(0, 0, 0, 0);
               const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
+              for (int k = 0; k < 2; ++k) {  // codes 16 chunk .. become pieces 2 chunk and 2 chunk + 1
                 uint32_t lo[2], hi[2];
                 e4m3_to_f16(lo, v[2 * k]);
                 e4m3_to_f16(hi, v[2 * k + 1]);
                 *reinterpret_cast<uint4*>(to + row * 128 + ((((2 * chunk + k) ^ row) & 7) << 4)) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
               }
             }
-            proxy_fence();
-            bar_arrive(&bars.full[slot]);
+            bar_arrive(&bars.stage_empty[2 * value + stage.bar]);
           }
-          if (h == 0) {  // the next tile's addresses, while copies are in flight
-            make_address(addr + (~j & 1) * 128, page, t);
-            if (two) make_address(addr + (~j & 1) * 128, page2, t + S::kLoaders);
-            if (!w.ends()) w.next();
-            page = look_up(t);
-            if (two) page2 = look_up(t + S::kLoaders);
-          }
+          if (!ok) break;
+          if (!value && h == 0 && t == 0) bars.since[j & 15] = static_cast<uint8_t>(since);
+          proxy_fence();
+          bar_arrive(&full[ring.bar]);
+          ring.next();
         }
+        const long long item = w.item;
+        w.next();
+        since = w.item != item ? 0 : min(since + 1, 2ll);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 8) {
-      // ---- the warp that issues the products ----------------------------------------------------------------------------
+    } else if (warp == 8 || (S::kStreams == 2 && warp == kSecondIssuer)) {
+      // ---- the warps that issue the products, one for each stream ---------------------------------------------------------
       // All lanes walk and wait together, on values that are the warp's; one issues. (Under a branch of one lane, on values of
-      // that lane, a product took 130 cycles to issue.)
+      // that lane, a product took 130 cycles to issue; one warp for both streams left the tensor cores idle for 700 cycles of
+      // 1850 while it waited and looked for the next unit.)
       constexpr uint32_t kScores = prefix_idesc<T>(kPrefixTile, false), kSums = prefix_idesc<T>(S::kWide, true);
+      constexpr bool kOneStream = S::kStreams == 1;
+      constexpr uint32_t kAhead = kOneStream ? 2 : 1;  // score buffers of a stream
+      const uint32_t st = warp == 8 ? 0 : 1;
       const int steps = a.head_dim / 16;
-      const uint32_t tm = of_warp(tmem), base_q = of_warp(s0 + S::kOffQ), base_kv = of_warp(s0);
-      const long long units = pair ? 2 * count : count;
-      PrefixWalk ws = walk(), wp = walk();  // at the key tile of the next scores, of the next sums
-      long long q_item0 = -1, q_item1 = -1, o_item0 = -1, o_item1 = -1;  // of either stream
-      uint32_t q_turn0 = 0, q_turn1 = 0;
+      const uint32_t tm = of_warp(tmem), base_q = of_warp(at_q + st * q_turns * q_bytes), base_k = of_warp(at_k), base_v = of_warp(at_v);
+      const uint32_t q_piece = of_warp(q_rows * 128);
+      const long long units = pair || kOneStream ? count : (count + 1 - st) / 2;
+      // this stream's next tile of keys and of values; single tiles go to two streams in turn
+      Ring keys(of_warp(key_slots)), values(of_warp(value_slots));
+      const bool every = pair || kOneStream;
+      uint32_t key_tile = st;  // (where since[] has the next tile of keys)
+      if (every) key_tile = 0;
+      else if (st) keys.next(), values.next();
+      uint32_t q_turn = 0;  // items so far
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (__all_sync(~0u, bar_try(bar, parity))) return true;
-        return __all_sync(~0u, bar_wait(bar, parity, dead));
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!__all_sync(~0u, bar_try(bar, parity))) ok = __all_sync(~0u, ok && bar_wait(bar, parity, dead));
       };
-      auto stream_of = [&](long long u) { return S::kStreams == 2 ? static_cast<int>(u) & 1 : 0; };
-      // Waits for what the scores of unit u need.
-      auto ready = [&](long long u) {
-        const int st = stream_of(u);
-        if (ws.item != (st ? q_item1 : q_item0)) {
-          (st ? q_item1 : q_item0) = ws.item;
-          ok = ok && wait(&bars.q_full[st], (st ? q_turn1 : q_turn0) & 1);
-          ++(st ? q_turn1 : q_turn0);
+      // (numbers of units wrap: parities are all that is used of them)
+      auto buffer_of = [&](uint32_t i) { return kOneStream ? i & 1 : st; };
+      auto turn_of = [&](uint32_t i) { return kOneStream ? i >> 1 & 1 : i & 1; };  // its parity
+      // Waits for the next tile of keys. Returns whether its unit is the stream's first of an item: the tile is the item's first, or,
+      // of single tiles in two streams, the second.
+      auto keys_there = [&]() -> bool {
+        wait(&bars.key_full[keys.bar], keys.phase);
+        if (S::kHalves == 2) {
+          Ring second = keys;
+          second.next();
+          wait(&bars.key_full[second.bar], second.phase);
         }
-        if (pair && (u & 1)) return;  // the keys are those of unit u - 1
-        const uint32_t j = static_cast<uint32_t>(pair ? u >> 1 : u);
-#pragma unroll
-        for (int h = 0; h < S::kHalves; ++h) {
-          const uint32_t g = j * 2 * S::kHalves + h;
-          ok = ok && wait(&bars.full[g % S::kSlots], (g / S::kSlots) & 1);
-        }
+        return of_warp(bars.since[key_tile & 15]) < (every ? 1 : 2);
       };
-      // By one lane, after ready().
-      auto scores = [&](long long u) {
-        const uint32_t j = static_cast<uint32_t>(pair ? u >> 1 : u), b = static_cast<uint32_t>(u) & 1;
+      auto queries = [&]() {
+        const uint32_t buffer = q_turns == 2 ? q_turn & 1 : 0;
+        wait(&bars.q_full[st * 2 + buffer], (q_turns == 2 ? q_turn >> 1 : q_turn) & 1);
+        ++q_turn;
+        if (!E4M3) proxy_fence();  // (their copies' writes are ordinary ones)
+      };
+      auto next_keys = [&]() {
+        for (int h = 0; h < S::kHalves; ++h) keys.next();
+        ++key_tile;
+        if (!every) keys.next(), ++key_tile;
+      };
+      // By one lane: a unit's scores from the next tile of keys.
+      auto scores = [&](uint32_t i) {
+        Ring r = keys;
 #pragma unroll
-        for (int h = 0; h < S::kHalves; ++h) {
-          const uint32_t slot = (j * 2 * S::kHalves + h) % S::kSlots;
-          const uint64_t kd = tc_desc(base_kv + slot * S::kSlot, 16);
-          const uint64_t qd = tc_desc(base_q + stream_of(u) * S::kQ + 2 * h * (kTileRows * 128), 16);
+        for (int h = 0; h < S::kHalves; ++h, r.next()) {
+          const uint64_t kd = tc_desc(base_k + r.slot * S::kSlot, 16);
+          const uint64_t qd = tc_desc(base_q + (q_turns == 2 && !(q_turn & 1) ? q_bytes : 0) + 2 * h * q_piece, 16);
 #pragma unroll
           for (int k = 0; k < S::kWide / 16; ++k)
             if (h * 8 + k < steps)
-              tc_mma(tm + b * 128, qd + ((k >> 2) * (kTileRows * 128) + (k & 3) * 32) / 16,
+              tc_mma(tm + buffer_of(i) * 128, qd + ((k >> 2) * q_piece + (k & 3) * 32) / 16,
                      kd + ((k >> 2) * (kPrefixTile * 128) + (k & 3) * 32) / 16, kScores, h > 0 || k > 0);
-          if (!pair || b) tc_commit(&bars.empty[slot]);
+          tc_commit(&bars.key_empty[r.bar]);
         }
-        tc_commit(&bars.s_full[b]);
+        tc_commit(&bars.s_full[buffer_of(i)]);
       };
-      auto after_scores = [&](long long u) {
-        if ((!pair || (u & 1)) && !ws.ends()) ws.next();
-      };
-      for (int u = 0; u < 2 && u < units && ok; ++u) {
-        ready(u);
-        proxy_fence();
+      uint32_t firsts = 0;  // bit i % 2: unit i is the first of an item
+      for (uint32_t i = 0; i < kAhead && i < units && ok; ++i) {
+        if (keys_there()) {
+          firsts |= 1u << i;
+          queries();
+        }
         tc_after();
-        if (ok && elected()) scores(u);
+        if (ok && elected()) scores(i);
         __syncwarp();
-        after_scores(u);
+        next_keys();
       }
-      for (long long u = 0; u < units && ok; ++u) {
-        const int st = stream_of(u);
-        const uint32_t j = static_cast<uint32_t>(pair ? u >> 1 : u), b = static_cast<uint32_t>(u) & 1;
-        const bool fresh = wp.item != (st ? o_item1 : o_item0), more = u + 2 < units;
-        (st ? o_item1 : o_item0) = wp.item;
+      long long left = units;
+      for (uint32_t i = 0; left > 0 && ok; ++i, --left) {
+        const bool fresh = firsts >> (i & 1) & 1, more = left > kAhead;
         // The next scores' keys are waited for before these sums are issued, so that both run without a pause; not so
         // the first of another item, whose queries come after this unit's probabilities.
-        const bool same = more && ws.item == (st ? q_item1 : q_item0);
-        if (same) ready(u + 2);
-        ok = ok && wait(&bars.p_full[b], static_cast<uint32_t>(u >> 1) & 1);
-        if (!pair || !b) {
-#pragma unroll
-          for (int h = 0; h < S::kHalves; ++h) {
-            const uint32_t g = j * 2 * S::kHalves + S::kHalves + h;
-            ok = ok && wait(&bars.full[g % S::kSlots], (g / S::kSlots) & 1);
-          }
-          proxy_fence();  // of these values, and of the keys that ready() waited for
+        bool same = more;
+        if (more) {
+          same = !keys_there();
+          const uint32_t bit = 1u << ((i + kAhead) & 1);
+          firsts = same ? firsts & ~bit : firsts | bit;
         }
+        {
+          Ring r = values;
+#pragma unroll
+          for (int h = 0; h < S::kHalves; ++h, r.next()) wait(&bars.value_full[r.bar], r.phase);
+        }
+        wait(&bars.p_full[buffer_of(i)], turn_of(i));
+        // The streams take turns, so that one's softmax runs while the other's products do (both at once is as stable a state, and a
+        // third slower: the products of both, then the softmax of both).
+        if (!kOneStream && (st || i)) wait(&bars.issued[st ^ 1], (st ? i : i - 1) & 1);
         if (!ok) break;
         tc_after();
         if (elected()) {
+          Ring r = values;
 #pragma unroll
-          for (int h = 0; h < S::kHalves; ++h) {
-            const uint32_t slot = (j * 2 * S::kHalves + S::kHalves + h) % S::kSlots;
-            const uint64_t vd = tc_desc(base_kv + slot * S::kSlot, kPrefixTile * 128);
+          for (int h = 0; h < S::kHalves; ++h, r.next()) {
+            const uint64_t vd = tc_desc(base_v + r.slot * S::kSlot, kPrefixTile * 128);
 #pragma unroll
             for (int k = 0; k < kPrefixTile / 16; ++k)
-              tc_mma_ts(tm + 256 + st * D + h * 128, tm + b * 128 + k * 8, vd + k * 2048 / 16, kSums, !fresh || k > 0);
-            if (!pair || b) tc_commit(&bars.empty[slot]);
+              tc_mma_ts(tm + 256 + st * D + h * 128, tm + buffer_of(i) * 128 + k * 8, vd + k * 2048 / 16, kSums, !fresh || k > 0);
+            tc_commit(&bars.value_empty[r.bar]);
           }
-          tc_commit(&bars.pv_done[b]);
-          // (the scores of u + 2 go where the probabilities of u were: the products run in the order of their issue)
-          if (same) scores(u + 2);
+          tc_commit(&bars.pv_done[buffer_of(i)]);
+          // (these scores go where the probabilities were: the products run in the order of their issue)
+          if (same) scores(i + kAhead);
+          if (!kOneStream) bar_arrive(&bars.issued[st]);
         }
         __syncwarp();
         if (more && !same) {
-          ready(u + 2);
-          proxy_fence();
+          queries();
           tc_after();
-          if (ok && elected()) scores(u + 2);
+          if (ok && elected()) scores(i + kAhead);
           __syncwarp();
         }
-        if (more) after_scores(u + 2);
-        if ((!pair || b) && !wp.ends()) wp.next();
+        if (more) next_keys();
+        for (int h = 0; h < S::kHalves; ++h) values.next();
+        if (!every) values.next();
       }
       // every product has ended before the tensor memory is freed, also when the CTA gave up
       if (elected()) tc_commit(&bars.drained);
@@ -571,83 +715,97 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<E4M3>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
     if (warp < 4 * S::kStreams) {
       // ---- softmax: a thread has a row of the stream's row tile -------------------------------------------------------
       const int st = warp >> 2, row = tid & 127;
       const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
       const uint32_t sums_at = tmem + lanes + 256 + static_cast<uint32_t>(st) * D;
-      float* late = reinterpret_cast<float*>(smem + S::kOffLate) + st * kGroupRows * 128 + row;  // [8][128]
       float cs = fmaxf(p.scale_log2, 1.17549435e-38f);  // (a score of -infinity stays one where the scale is 0)
       float next_cs = cs;                               // of the queries loaded last
-      // A warp's 32 rows of an item's queries into shared memory: a lane makes the address of its own row, D / 8 lanes copy one.
-      auto load_queries = [&](const PrefixWalk& w) {
+      // Where this thread's row of an item's queries is, in elements; -1: the item has fewer rows.
+      auto query_at = [&](const PrefixWalk& w) -> long long {
         const int head = w.kv_head();
-        const float ks = E4M3 ? a.k_scale[head] : 1.0f;
-        const uint32_t flip = p.flip ^ (ks < 0.0f ? 0x80008000u : 0u);
-        long long mine = -1;
         if (line == kOwn) {
           const int m = w.block() * kTileRows + row, q = p.group_div(m), b = w.request();
-          if (q < w.group_rows())
-            mine = b * a.q_stride[0] + ((w.bg - b * p.groups) * kGroupRows + q) * a.q_stride[1] + (head * p.group + m - q * p.group) * a.q_stride[2];
-        } else {
-          const int m = pair ? (2 * w.block() + st) * kTileRows + row : p.first_single() + w.block() * kTileRows + row;
-          if (m < p.n_rows) {
-            const int br = p.group_div(m), h = head * p.group + m - br * p.group, b = p.row_div(br), qr = br - b * a.rows;
-            mine = b * a.q_stride[0] + qr * a.q_stride[1] + h * a.q_stride[2];
-          }
+          if (q >= w.group_rows()) return -1;
+          return b * a.q_stride[0] + ((w.bg - b * p.groups) * kGroupRows + q) * a.q_stride[1] + (head * p.group + m - q * p.group) * a.q_stride[2];
         }
-        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+        const int m = pair ? (2 * w.block() + st) * kTileRows + row : p.first_single() + w.block() * kTileRows + row;
+        if (m >= p.n_rows) return -1;
+        const int br = p.group_div(m), h = head * p.group + m - br * p.group, b = p.row_div(br), qr = br - b * a.rows;
+        return b * a.q_stride[0] + qr * a.q_stride[1] + h * a.q_stride[2];
+      };
+      // A warp's 32 rows of an item's queries on their way into shared memory: a lane makes the address of its own row, D / 8 lanes
+      // copy one.
+      uint32_t q_turn = 0;
+      auto load_queries = [&](const PrefixWalk& w) {
+        const long long mine = query_at(w);
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
         const int chunk = lane % kLanes, sub = lane / kLanes;
         const bool in = chunk * 8 < a.head_dim;
-        unsigned char* to = smem + S::kOffQ + st * S::kQ + (chunk >> 3) * (kTileRows * 128);
+        const uint32_t buffer = q_turns == 2 ? q_turn & 1 : 0;
+        const uint32_t to = at_q + (st * q_turns + buffer) * q_bytes + (chunk >> 3) * 128 * q_rows;
+        uint64_t* bar = &bars.q_full[st * 2 + buffer];
+        ++q_turn;
+        const QT* q = static_cast<const QT*>(a.q);
+        if (!E4M3) {
+          // (rows that are not there are not written: nothing is done with what the products make of them)
+          const int n = __popc(__ballot_sync(~0u, mine != -1));
+#pragma unroll 2
+            for (int i = 0; i * kRows < n; ++i) {
+              const long long off = __shfl_sync(~0u, mine, i * kRows + sub);
+              const int r = (row & ~31) + i * kRows + sub;
+              cp16(to + r * 128 + (((chunk ^ r) & 7) << 4), off == -1 || !in ? q : q + off + chunk * 8, off != -1 && in);
+            }
+          cp_arrive(bar);
+          return;
+        }
+        const float ks = a.k_scale[w.kv_head()];
+        const uint32_t flip = p.flip ^ (ks < 0.0f ? 0x80008000u : 0u);
+        const int n = __popc(__ballot_sync(~0u, mine != -1));
 #pragma unroll 1
-        for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
+        for (int i0 = 0; i0 * kRows < n; i0 += kBatch) {
           uint4 u[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
             const long long off = __shfl_sync(~0u, mine, (i0 + i) * kRows + sub);
             u[i] = make_uint4(0, 0, 0, 0);
-            if (in && off != -1) u[i] = *reinterpret_cast<const uint4*>(static_cast<const QT*>(a.q) + off + chunk * 8);
+            if (in && off != -1) u[i] = *reinterpret_cast<const uint4*>(q + off + chunk * 8);
           }
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
+            // fp16 against a power of two near the row's largest (bf16 mantissas fit); the scores take it back
             const int r = (row & ~31) + (i0 + i) * kRows + sub;
-            uint4 x = u[i];
-            x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-            if (E4M3) {
-              // fp16 against a power of two near the row's largest (bf16 mantissas fit); the scores take it back
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              float big = 0;
+            const uint32_t w4[4] = {u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip};
+            float big = 0;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = unpack2<QT>(w[k]);
-                big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-#pragma unroll
-              for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
-              const int e = big > 0 && big < INFINITY ? min(max(ilogbf(big), -120), 120) : 0;
-              const float down = __uint_as_float((127 - e) << 23);
-              uint32_t v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = unpack2<QT>(w[k]);
-                v[k] = pack2<__half>(f.x * down, f.y * down);
-              }
-              x = make_uint4(v[0], v[1], v[2], v[3]);
-              const float up = __shfl_sync(~0u, __uint_as_float((127 + e) << 23), (lane % kRows) * kLanes);
-              if (lane / kRows == i0 + i) next_cs = fmaxf(p.scale_log2 * fabsf(ks), 1.17549435e-38f) * up;
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack2<QT>(w4[k]);
+              big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-            *reinterpret_cast<uint4*>(to + r * 128 + (((chunk ^ r) & 7) << 4)) = x;
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+            // 2^e <= big < 2^(e + 1), within 2^+-120; 1 for a row of zeros or with an infinity
+            const int e = big > 0 && big < INFINITY ? min(max((__float_as_int(big) >> 23) - 127, -120), 120) : 0;
+            const float down = __uint_as_float((127 - e) << 23);
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = unpack2<QT>(w4[k]);
+              v[k] = pack2<__half>(f.x * down, f.y * down);
+            }
+            const float up = __shfl_sync(~0u, __uint_as_float((127 + e) << 23), (lane % kRows) * kLanes);
+            if (lane / kRows == i0 + i) next_cs = fmaxf(p.scale_log2 * fabsf(ks), 1.17549435e-38f) * up;
+            *reinterpret_cast<uint4*>(smem + (to - s0) + r * 128 + (((chunk ^ r) & 7) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
         proxy_fence();
-        bar_arrive(&bars.q_full[st]);
+        bar_arrive(bar);
       };
       // the first key tile of this stream in the piece's tiles j0 .. j1 - 1 of an item
       auto first_of = [&](long long j0) { return pair || S::kStreams == 1 ? j0 : j0 + ((j0 ^ st) & 1); };
       bool ok = true;
-      uint32_t late_turn = 0;
       const int rows = line == kOwn ? p.own_rows : kTileRows;  // of a place
       auto row_of = [&](const PrefixWalk& w) -> long long {    // this row's place among the parts
         long long place = c + w.item;
@@ -663,42 +821,48 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
       seek();
       if (!w.ends()) load_queries(w);
       while (ok && !w.ends()) {
+        const PrefixWalk item = w;
         const long long j0 = w.done, j1 = j0 + w.left(), at_row = row_of(w);
         float2* ml = (line == kOwn ? p.own_ml : p.part_ml) + at_row;
-        long long j = first_of(j0);
         cs = next_cs;
         const int first_tile = w.tile;
         // keys that this row sees: those before `limit`
         int limit = w.len;
         if (line == kOwn) limit -= max(0, w.group_rows() - 1 - p.group_div(w.block() * kTileRows + row));
-        const int all_see = w.all_see(), len = w.len;
-        uint32_t late_keys = 0;  // of this part: bit i is key all_see + i
+        const int all_see = w.all_see();
         float base = kNoBase, l = 0;  // (the first unit sets the base)
         bool first = true;
+        const bool idle = (row & ~31) >= rows;  // none of this warp's rows is one: its scores are not looked at
         long long u = 0;
-        for (; ok && j < j1; j += pair ? 1 : S::kStreams) {
+        w.skip();
+        seek();
+        // The next item's queries: now, where there is room for two, or when the last scores have left their place.
+#pragma unroll 1
+        for (int step = 0; step < 2; ++step) {
+        if (ok && !w.ends() && (step == 0) == (q_turns == 2)) load_queries(w);
+        if (step == 0)
+        for (long long j = first_of(j0); ok && j < j1; j += pair ? 1 : S::kStreams) {
           u = pair ? 2 * j + st : j;
           ok = __all_sync(~0u, bar_wait(&bars.s_full[u & 1], static_cast<uint32_t>(u >> 1) & 1, dead));
           if (!ok) break;
-          tc_after();
           const int key0 = (first_tile + static_cast<int>(j - j0)) * kPrefixTile;
+          if (idle) {
+            bar_arrive(&bars.p_full[u & 1]);
+            continue;
+          }
+          tc_after();
           const uint32_t at = tmem + lanes + static_cast<uint32_t>(u & 1) * 128;
           float s[128];
           tc_ld64(s, 0, at);
           tc_ld64(s, 64, at + 64);
+          if (!E4M3 && p.flip)  // a negative scale
+#pragma unroll
+            for (int x = 0; x < 128; ++x) s[x] = -s[x];
           if (key0 + kPrefixTile > all_see) {
             const int valid = limit - key0;
 #pragma unroll
             for (int x = 0; x < 128; ++x)
               if (x >= valid) s[x] = -INFINITY;
-            const int lo = all_see - key0;
-#pragma unroll 1
-            for (int x = max(lo, 0); x < min(len - key0, 128); ++x) {
-              float y;
-              tc_ld1(y, at + x);
-              late[(x - lo) * 128] = x < valid ? y * cs : -INFINITY;
-              late_keys |= 1u << (x - lo);
-            }
           }
           float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -749,65 +913,52 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
           tc_before();
           bar_arrive(&bars.p_full[u & 1]);
         }
+        }
         if (!ok) break;
-        // Values of the part's keys that not all rows see, into shared memory (two turns: a warp may be an item behind).
-        constexpr int kBytes = E4M3 ? 1 : 2;
-        const unsigned char* late_v = smem + S::kOffLateV + (st * 2 + (late_turn & 1)) * (kGroupRows * D * 2);
-        if (late_keys) {
-          const int pieces = a.head_dim * kBytes / 16;
-          for (int i = row; i < kGroupRows * pieces; i += S::kStreamThreads) {
-            const int x = i / pieces, at = (i - x * pieces) * 16;
-            if (!(late_keys >> x & 1)) continue;
-            const int key = all_see + x, page = a.table[w.request() * a.table_stride + p.page(key)];
-            const unsigned char* from = kZeros;
-            if (page >= 0 && page < a.n_pages) from = row_at(a.v_pages, p.v_step, page, w.kv_head(), key - p.page(key) * a.page_size);
-            cp16(s0 + static_cast<uint32_t>(late_v - smem) + x * D * 2 + at, from + at);
-          }
-          cp_arrive(&bars.late_full[st]);
-        }
-        // the next item's queries, whose place the last scores have left
-        w.skip();
-        seek();
-        if (!w.ends()) load_queries(w);
-        if (late_keys) {
-          ok = __all_sync(~0u, bar_wait(&bars.late_full[st], late_turn & 1, dead));
-          ++late_turn;
-        }
-        ok = __all_sync(~0u, bar_wait(&bars.pv_done[u & 1], static_cast<uint32_t>(u >> 1) & 1, dead)) && ok;
+        ok = __all_sync(~0u, bar_wait(&bars.pv_done[u & 1], static_cast<uint32_t>(u >> 1) & 1, dead));
         tc_after();
         float* out = (line == kOwn ? p.own : p.part) + at_row * D;
         const bool write = row < rows;
+        // keys that not all rows see and whose values were left out: their probabilities once more
+        bool slow = false;
+        float late[kGroupRows];
+        auto left_out_of = [&](int key) -> const uint8_t* { return bars.slow[(j0 + (key >> 7) - first_tile) & 15]; };
+        auto any_left_out = [&](int key) -> bool {  // of the key's tile, where that is one of this stream's
+          const long long j = j0 + (key >> 7) - first_tile;
+          return j >= j0 && j < j1 && (S::kStreams == 1 || (j & 1) == st) && *reinterpret_cast<const uint32_t*>(left_out_of(key));
+        };
+        if (all_see < item.len && (any_left_out(max(all_see, 0)) || any_left_out(item.len - 1))) {
+          for (int x = 0; x < kGroupRows; ++x) {
+            const int key = all_see + x;
+            late[x] = -1.0f;
+            if (key < 0 || key >= item.len || !any_left_out(key)) continue;
+            slow = true;
+            const long long at = query_at(item);
+            if (at == -1 || key >= limit) continue;
+            const int page = a.table[item.request() * a.table_stride + p.page(key)];
+            if (page < 0 || page >= a.n_pages) continue;
+            const unsigned char* k = row_at(a.k_pages, p.k_step, page, item.kv_head(), key - p.page(key) * a.page_size);
+            float t = 0;
+            for (int d = 0; d < a.head_dim; ++d) t += static_cast<float>(static_cast<const QT*>(a.q)[at + d]) * cached<T, E4M3>(k, d);
+            if (E4M3) t *= a.k_scale[item.kv_head()];
+            late[x] = exp2_fast(t * a.scale * 1.44269504088896340736f - base);
+          }
+        }
 #pragma unroll 1
-        for (int d = 0; d < a.head_dim; d += 32) {
+        for (int d = 0; d < a.head_dim && !idle; d += 32) {
           float v[32];
           tc_ld(v, sums_at + d);
-#pragma unroll 1
-          for (uint32_t left = late_keys; left; left &= left - 1) {
-            const int x = __ffs(left) - 1;
-            if (all_see + x >= limit) continue;
-            const float f = exp2_fast(late[x * 128] - base);
-            const unsigned char* from = late_v + x * D * 2 + d * kBytes;
+          if (slow)
+            for (int x = 0; x < kGroupRows; ++x) {
+              if (late[x] == -1.0f) continue;
+              const int key = all_see + x;
+              if (!left_out_of(key)[E4M3 ? (d >> 7) * 2 + (key >> 6 & 1) : d >> 6]) continue;
+              const int page = a.table[item.request() * a.table_stride + p.page(key)];
+              const unsigned char* from = row_at(a.v_pages, p.v_step, page, item.kv_head(), key - p.page(key) * a.page_size);
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              if (d + k >= a.head_dim) break;
-              uint32_t q[4];  // eight 16-bit values
-              if (E4M3) {
-                const uint2 codes = *reinterpret_cast<const uint2*>(from + k);
-                uint32_t lo[2], hi[2];
-                e4m3_to_f16(lo, codes.x);
-                e4m3_to_f16(hi, codes.y);
-                q[0] = lo[0], q[1] = lo[1], q[2] = hi[0], q[3] = hi[1];
-              } else {
-                const uint4 y = *reinterpret_cast<const uint4*>(from + k * 2);
-                q[0] = y.x, q[1] = y.y, q[2] = y.z, q[3] = y.w;
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 y = unpack2<T>(q[i]);
-                v[k + 2 * i] += f * y.x, v[k + 2 * i + 1] += f * y.y;
-              }
+              for (int i = 0; i < 32; ++i)
+                if (d + i < a.head_dim) v[i] += late[x] * cached<T, E4M3>(from, d + i);
             }
-          }
           if (write)
 #pragma unroll
             for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(out + d + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
@@ -824,17 +975,29 @@ __global__ void __launch_bounds__(PrefixShape<D>::kThreads, 1) prefix_kernel(con
   if (tid == 0 && *dead) flag(a.status, MK_OP_TIMEOUT);
 }
 
+// The cache as the copies see it: boxes of `rows` places and 128 bytes of a head (copies begin on 128 bytes of shared memory).
+cudaError_t map_cache(CUtensorMap* map, const void* pages, const mk_prefix_attention_args& a, const int64_t* strides, int rows, bool e4m3);
+
 template <typename T, typename QT, int D, bool E4M3>
 cudaError_t launch_prefix(const PrefixParams& p, int device, cudaStream_t s) {
   constexpr auto kernel = prefix_kernel<T, QT, D, E4M3>;
-  if (const cudaError_t e = allow_smem<kernel>(device, PrefixShape<D>::kSmem)) return e;
+  using S = PrefixShape<D, E4M3>;
+  if (const cudaError_t e = allow_smem<kernel>(device, S::kSmem)) return e;
   // setmaxnreg hands out what the block was launched with; a build with less would wait for ever
   static const int regs = [] {
     cudaFuncAttributes f{};
     return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
   }();
-  if (regs * PrefixShape<D>::kThreads < 256 * (kSoftmaxRegs<E4M3> + kOtherRegs<E4M3>)) return cudaErrorInvalidConfiguration;
-  return start(kernel, p.ctas, PrefixShape<D>::kThreads, PrefixShape<D>::kSmem, s, p);
+  if (regs * S::kThreads < 256 * S::kSoftmaxRegs + (S::kThreads - 256) * S::kOtherRegs) return cudaErrorInvalidConfiguration;
+  PrefixParams q = p;
+  const mk_prefix_attention_args& a = p.a;
+  q.box = a.page_size & -a.page_size;
+  const int most = E4M3 ? S::kStageRows : kPrefixTile;
+  if (q.box > most) q.box = most;
+  const int64_t *ks = a.k_page_stride, *vs = a.v_page_stride;
+  cudaError_t e = map_cache(&q.keys, a.k_pages, a, ks, q.box, E4M3);
+  if (e == cudaSuccess) e = map_cache(&q.values, a.v_pages, a, vs, q.box, E4M3);
+  return e == cudaSuccess ? start(kernel, p.ctas, S::kThreads, S::kSmem, s, q) : e;
 }
 template <typename T, typename QT, bool E4M3>
 cudaError_t launch_prefix(const PrefixParams& p, int device, cudaStream_t s) {

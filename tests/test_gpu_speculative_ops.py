@@ -638,8 +638,11 @@ def test_prefix_hidden_values_do_not_leak(cache):
         bad["k"][at, :, p % 16] = float("nan")
         bad["v"][at, :, p % 16] = float("nan")
     got2, lse2 = run_prefix(bad)
-    assert torch.equal(got2[:, :7], got[:, :7]) and torch.equal(lse2[:, :7], lse[:, :7])
-    assert got2[:, 7].isnan().all()
+    assert got2[:, 7].isnan().all() and lse2[:, 7].isnan().all()
+    # The other rows are what they were, within the same bounds (values beside those that are left out of a product are added to
+    # its sums in fp32, in another order and unrounded, so not bit for bit).
+    got2[:, 7], lse2[:, 7] = got[:, 7], lse[:, 7]
+    check_prefix(s, got2, lse2, 128 ** -0.5, "beside hidden values")
 
 
 def test_prefix_values_that_are_not_finite_reach_their_rows():
