@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const int b = p.row_div(br), r = br - b * a.rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (br >= a.batch * a.rows) return;  // (W = 8: the whole CTA)
-  const Head hd = *p.head;
+  const Head& hd = *p.head;
   // Parts 0 .. n0 - 1 are over the prefix, n0 .. n - 1 over own keys. Part k of either is place0 + k / subs, stream k % subs (of a
   // pair: its own stream).
   const int pairs = p.blocks[kPairs], line = pairs && m < p.first_single() ? kPairs : kSingles;
@@ -79,13 +79,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       sum += weight * mine.y;
       // (an empty part has no sums: its weight is 0 and its row is not read)
       const unsigned there = __ballot_sync(~0u, !(mine.y == 0.0f));
-#pragma unroll 8
-      for (int k = w; k < min(32, n - k0); k += W) {
-        const float f = __shfl_sync(~0u, weight, k);
-        const float* x_at = reinterpret_cast<const float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(from), k));
-        if (!(there >> k & 1)) continue;
-        const float4 x = *reinterpret_cast<const float4*>(x_at + d);
-        y.x += f * x.x, y.y += f * x.y, y.z += f * x.z, y.w += f * x.w;
+      constexpr int kFlight = 6;
+#pragma unroll 1
+      for (int k1 = w; k1 < min(32, n - k0); k1 += W * kFlight) {
+        float4 x[kFlight];
+        float f[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int k = min(k1 + i * W, 31);
+          f[i] = __shfl_sync(~0u, weight, k);
+          const float* x_at = reinterpret_cast<const float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(from), k));
+          x[i] = make_float4(0, 0, 0, 0);
+          if (k1 + i * W < 32 && there >> k & 1) x[i] = *reinterpret_cast<const float4*>(x_at + d);
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) y.x += f[i] * x[i].x, y.y += f[i] * x[i].y, y.z += f[i] * x[i].z, y.w += f[i] * x[i].w;
       }
     }
 #pragma unroll

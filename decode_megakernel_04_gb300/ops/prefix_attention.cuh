@@ -50,7 +50,7 @@ constexpr int kGroupRows = 8;         // new rows of a request that share an ite
 constexpr int kMinPiece = 1;          // key tiles of a piece at least
 enum { kPairs, kSingles, kOwn };      // the lines
 // What a tile of a line, and an item over own keys, take of a CTA (in 250 cycles, 128 wide)
-constexpr int kPairCost = 12, kSingleCost = 7, kOwnCost = 7, kItemCost = 10;
+constexpr int kPairCost = 12, kSingleCost = 9, kOwnCost = 8, kItemCost = 40;
 
 // What the first CTA writes for the join. Piece c's part of item i of a line goes to place c + i (after `place0`): along the line
 // either grows by one from part to part.
@@ -834,22 +834,13 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
         bool first = true;
         const bool idle = (row & ~31) >= rows;  // none of this warp's rows is one: its scores are not looked at
         long long u = 0;
-        w.skip();
-        seek();
-        // The next item's queries: now, where there is room for two, or when the last scores have left their place.
-#pragma unroll 1
-        for (int step = 0; step < 2; ++step) {
-        if (ok && !w.ends() && (step == 0) == (q_turns == 2)) load_queries(w);
-        if (step == 0)
-        for (long long j = first_of(j0); ok && j < j1; j += pair ? 1 : S::kStreams) {
+        const int every = pair ? 1 : S::kStreams;
+        for (long long j = first_of(j0); ok && j < j1; j += every) {
           u = pair ? 2 * j + st : j;
           ok = __all_sync(~0u, bar_wait(&bars.s_full[u & 1], static_cast<uint32_t>(u >> 1) & 1, dead));
           if (!ok) break;
           const int key0 = (first_tile + static_cast<int>(j - j0)) * kPrefixTile;
-          if (idle) {
-            bar_arrive(&bars.p_full[u & 1]);
-            continue;
-          }
+          if (!idle) {
           tc_after();
           const uint32_t at = tmem + lanes + static_cast<uint32_t>(u & 1) * 128;
           float s[128];
@@ -911,8 +902,15 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
           l += sums[0].x + sums[0].y;
           tc_wait_st();
           tc_before();
+          }
           bar_arrive(&bars.p_full[u & 1]);
-        }
+          // The next item's queries: as soon as there is room for them. With two buffers that is at the item's start, but its
+          // first probabilities go before.
+          if (q_turns == 2 ? j == first_of(j0) : j + every >= j1) {
+            w.skip();
+            seek();
+            if (!w.ends()) load_queries(w);
+          }
         }
         if (!ok) break;
         ok = __all_sync(~0u, bar_wait(&bars.pv_done[u & 1], static_cast<uint32_t>(u >> 1) & 1, dead));
@@ -961,7 +959,9 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
             }
           if (write)
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(out + d + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            for (int x = 0; x < 32; x += 8)
+              asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + d + x), "f"(v[x]), "f"(v[x + 1]),
+                           "f"(v[x + 2]), "f"(v[x + 3]), "f"(v[x + 4]), "f"(v[x + 5]), "f"(v[x + 6]), "f"(v[x + 7]) : "memory");
         }
         if (write) *ml = make_float2(l == 0.0f ? -INFINITY : base, l);
         tc_before();
