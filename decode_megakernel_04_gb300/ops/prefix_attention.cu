@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   if (own_n) {
     const int per = a.n_kv_heads * p.blocks[kOwn], hm = head * p.blocks[kOwn] + own_m / kTileRows;
     const long long x = cum * per + hm * own_n;
-    const int c0 = Head::piece_of(x, hd.total[kOwn], hd.used[kOwn]);
+    const int c0 = Head::piece_of(x + kItemTiles, hd.total[kOwn], hd.used[kOwn]);
     n1 = (Head::piece_of(x + own_n - 1, hd.total[kOwn], hd.used[kOwn]) - c0 + 1) * own_subs;
     own0 = c0 + static_cast<long long>(bg) * per + hm;
   }

@@ -47,15 +47,16 @@ __device__ inline long long scaled(long long a, long long b, long long c) {
 constexpr int kPrefixTile = 128;      // keys
 constexpr int kTileRows = 128;        // query rows of a row tile
 constexpr int kGroupRows = 8;         // new rows of a request that share an item over its own keys
-constexpr int kMinPiece = 1;          // key tiles of a piece at least
+constexpr int kItemTiles = 2;         // what an item over own keys takes besides its tiles, in tiles
 enum { kPairs, kSingles, kOwn };      // the lines
-// What a tile of a line, and an item over own keys, take of a CTA (in 250 cycles, 128 wide)
-constexpr int kPairCost = 12, kSingleCost = 9, kOwnCost = 8, kItemCost = 40;
+// What a tile of a line takes of a CTA (in 250 cycles, 128 wide)
+template <bool E4M3>
+constexpr int kLineCost[3] = {12, E4M3 ? 11 : 9, E4M3 ? 11 : 9};
 
 // What the first CTA writes for the join. Piece c's part of item i of a line goes to place c + i (after `place0`): along the line
 // either grows by one from part to part.
 struct Head {
-  long long total[3];  // key tiles of a line
+  long long total[3];  // key tiles of a line; over own keys with kItemTiles before each item's
   int used[3];         // its pieces
   int tiles;           // key tiles of the prefix
   __device__ static int piece_of(long long x, long long total, int used) {  // the last piece that begins at or before tile x
@@ -84,7 +85,7 @@ struct PrefixParams {
   float* own;         // [places][streams][own_rows][dp] and
   float2* own_ml;     // [places][streams][own_rows] over own keys
   Head* head;
-  long long* cum;     // [batch * groups + 1] key tiles of the row groups so far (of one row tile)
+  long long* cum;     // [batch * groups + 1] as total[kOwn], of the row groups so far (of one row tile)
   int box;            // rows of a copied box: the largest power of two that divides the page size, up to the slot or stage
   CUtensorMap keys, values;  // [n_pages][n_kv_heads][page_size][head_dim]
   __device__ int first_single() const { return blocks[kPairs] * 2 * kTileRows; }
@@ -95,6 +96,7 @@ struct PrefixParams {
     return max(0, min(max(a.lens[b], 0), max_own) - (a.rows - g * kGroupRows - rows_of(g)));
   }
   __device__ static int tiles_of(int len) { return (len + kPrefixTile - 1) >> 7; }
+  __device__ static int with_item(int n) { return n ? n + kItemTiles : 0; }
 };
 
 // A role's place in its CTA's piece of a line.
@@ -294,9 +296,11 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
   const int tid = threadIdx.x, lane = tid & 31, warp = of_warp(tid >> 5);
   PrefixBars& bars = *reinterpret_cast<PrefixBars*>(smem + S::kOffBar);
   volatile int* dead = &bars.dead;
-  __shared__ long long warp_tiles[S::kThreads / 32];
-  __shared__ long long at_rem;
-  __shared__ int at_bg;
+  __shared__ long long warp_tiles[2][S::kThreads / 32];
+  __shared__ struct {
+    long long tiles[2];  // over own keys: this piece's tiles among all, its first and behind its last
+    int bg, hm, tile;    // and where the first is
+  } ends;
 
   // ---- the lines, and this CTA's piece of one -------------------------------------------------------------------------
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -308,30 +312,37 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
   {
     const int each = (n_groups + S::kThreads - 1) / S::kThreads;
     const int g0 = min(n_groups, tid * each), g1 = min(n_groups, g0 + each);
-    long long mine = 0;
-    for (int g = g0; g < g1; ++g) mine += PrefixParams::tiles_of(p.own_len(g));
-    long long before = mine;
+    // [0] tiles, [1] with what the items take
+    long long mine[2] = {}, before[2], own[2] = {};
+    for (int g = g0; g < g1; ++g) {
+      const int n = PrefixParams::tiles_of(p.own_len(g));
+      mine[0] += n, mine[1] += PrefixParams::with_item(n);
+    }
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(~0u, before, d);
-      if (lane >= d) before += o;
+    for (int i = 0; i < 2; ++i) {
+      before[i] = mine[i];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(~0u, before[i], d);
+        if (lane >= d) before[i] += o;
+      }
+      if (lane == 31) warp_tiles[i][warp] = before[i];
+      before[i] -= mine[i];
     }
-    if (lane == 31) warp_tiles[warp] = before;
     __syncthreads();
-    before -= mine;
-    long long own = 0;
-    for (int w = 0; w < S::kThreads / 32; ++w) {
-      if (w < warp) before += warp_tiles[w];
-      own += warp_tiles[w];
-    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      for (int w = 0; w < S::kThreads / 32; ++w) {
+        if (w < warp) before[i] += warp_tiles[i][w];
+        own[i] += warp_tiles[i][w];
+      }
     hd.tiles = PrefixParams::tiles_of(prefix_len);
     hd.total[kPairs] = static_cast<long long>(a.n_kv_heads) * p.blocks[kPairs] * hd.tiles;
     hd.total[kSingles] = static_cast<long long>(a.n_kv_heads) * p.blocks[kSingles] * hd.tiles;
-    hd.total[kOwn] = own * per;
-    // A line's CTAs: in proportion to what its tiles and items take, one at least.
+    hd.total[kOwn] = own[1] * per;
+    // A line's CTAs: in proportion to what its tiles take, one at least.
     const int ctas = gridDim.x;
-    const long long cost[3] = {kPairCost * hd.total[kPairs], kSingleCost * hd.total[kSingles],
-                               hd.total[kOwn] ? kOwnCost * hd.total[kOwn] + kItemCost * static_cast<long long>(n_groups) * per : 0};
+    const long long cost[3] = {kLineCost<E4M3>[0] * hd.total[0], kLineCost<E4M3>[1] * hd.total[1], kLineCost<E4M3>[2] * hd.total[2]};
     const long long sum = cost[0] + cost[1] + cost[2];
     int n0 = cost[0] ? max(1, static_cast<int>(scaled(cost[0], ctas, sum))) : 0;
     int n1 = cost[1] ? max(1, static_cast<int>(scaled(cost[1], ctas, sum))) : 0;
@@ -340,8 +351,8 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
     if (!cost[2]) (cost[1] ? n1 : n0) += most - n0 - n1;
     const int got[3] = {n0, n1, ctas - n0 - n1};
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const long long worth = (hd.total[i] + kMinPiece - 1) / kMinPiece;
+    for (int i = 0; i < 3; ++i) {  // (a piece has a tile)
+      const long long worth = i == kOwn ? hd.total[i] / (kItemTiles + 1) : hd.total[i];
       hd.used[i] = static_cast<int>(worth < got[i] ? worth : got[i]);
     }
     line = c < n0 ? kPairs : c < n0 + n1 ? kSingles : kOwn;
@@ -350,26 +361,37 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
     if (blockIdx.x == 0) {
       if (tid == 0) {
         *p.head = hd;
-        p.cum[n_groups] = own;
+        p.cum[n_groups] = own[1];
         if (prefix_len != a.prefix_len[0]) flag(a.status, MK_OP_BAD_LENGTH);
       }
-      long long at = before;
+      long long at = before[1];
       for (int g = g0; g < g1; ++g) {
         p.cum[g] = at;
-        at += PrefixParams::tiles_of(p.own_len(g));
+        at += PrefixParams::with_item(PrefixParams::tiles_of(p.own_len(g)));
         const int b = p.groups_div(g);
         if (a.lens[b] < 0 || a.lens[b] > p.max_own) flag(a.status, MK_OP_BAD_LENGTH);
       }
     }
-    if (line == kOwn && c < hd.used[kOwn] && before * per <= begin && begin < (before + mine) * per) {
-      for (int g = g0; g < g1; ++g) {
-        const int n = PrefixParams::tiles_of(p.own_len(g));
-        if (begin < (before + n) * per) {
-          at_bg = g;
-          at_rem = begin - before * per;
-          break;
+    if (line == kOwn && c < hd.used[kOwn]) {
+      // the first tile at or behind where the piece begins, and that where the next does
+      const long long to = scaled(c + 1, hd.total[kOwn], hd.used[kOwn]);
+      if (tid == 0 && to == hd.total[kOwn]) ends.tiles[1] = own[0] * per;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const long long x = e ? to : begin;
+        if (x < before[1] * per || x >= (before[1] + mine[1]) * per) continue;
+        long long tiles = before[0], at = before[1];
+        for (int g = g0; g < g1; ++g) {
+          const int n = PrefixParams::tiles_of(p.own_len(g)), all = PrefixParams::with_item(n);
+          if (x < (at + all) * per) {
+            const int hm = static_cast<int>(scaled(x - at * per, 1, all));
+            const int tile = max(0, static_cast<int>(x - at * per - static_cast<long long>(hm) * all) - kItemTiles);
+            ends.tiles[e] = tiles * per + static_cast<long long>(hm) * n + tile;
+            if (!e) ends.bg = g, ends.hm = hm, ends.tile = tile;
+            break;
+          }
+          tiles += n, at += all;
         }
-        before += n;
       }
     }
   }
@@ -406,15 +428,16 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
   // behind fewer (rows that nothing is done with) has to be the CTA's memory, here slots.
   const uint32_t q_turns = few ? 2 : 1, q_bytes = q_rows * D * 2, at_q = s0, at_k = s0 + S::kStreams * q_turns * q_bytes;
   const uint32_t at_v = at_k + key_slots * S::kSlot;
-  const long long count = scaled(c + 1, hd.total[line], hd.used[line]) - begin;  // key tiles of this piece
+  // key tiles of this piece
+  const long long count = line == kOwn ? ends.tiles[1] - ends.tiles[0] : scaled(c + 1, hd.total[line], hd.used[line]) - begin;
   auto walk = [&]() -> PrefixWalk {
     PrefixWalk w{p, line, per, 0, 0, 0, prefix_len, hd.tiles, 0, 0, count};
     if (line == kOwn) {
-      w.bg = at_bg;
+      w.bg = ends.bg;
       w.len = p.own_len(w.bg);
       w.n = PrefixParams::tiles_of(w.len);
-      w.hm = static_cast<int>(scaled(at_rem, 1, w.n));
-      w.tile = static_cast<int>(at_rem - static_cast<long long>(w.hm) * w.n);
+      w.hm = ends.hm;
+      w.tile = ends.tile;
       w.item = static_cast<long long>(w.bg) * per + w.hm;
     } else {
       w.item = scaled(begin, 1, hd.tiles);
