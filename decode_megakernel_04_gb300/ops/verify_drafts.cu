@@ -1,12 +1,17 @@
 // mk_verify_drafts: drafted tokens against the target's probabilities from given random numbers, and the token after them.
 //
 // Two kernels. `stats_kernel`: the largest logit of every row, its first place and the sum of exp((z - largest) / T), one
-// pass, a row cut into up to 32 parts so that few rows fill the GPU. `draw_kernel`: a cluster for each request joins the
-// parts, walks the drafts and runs the race: the token with the largest weight / noise. With given exponential noise the
-// race is a draw from the weights, and unlike an inverse distribution function it is no sum over the vocabulary: a token's
-// quotient depends on that token alone, in fp32, whatever the order of the work.
-// Bound by memory: every logit once, and the drawn row, its draft row and the noise.
-#include <cooperative_groups.h>
+// pass, a row cut into up to 32 parts so that few rows fill the GPU. `draw_kernel`: up to 64 CTAs for each request. Each joins
+// the statistics and walks the drafts (what that reads is small, and asked for before the first kernel has ended), and runs
+// the race over its share of the drawn row: the token with the largest weight / noise. The request's last CTA joins the shares.
+// With given exponential noise the race is a draw from the weights, and unlike an inverse distribution function it is no sum
+// over the vocabulary: a token's quotient depends on that token alone, in fp32, whatever the order of the work.
+// Bound by memory: every logit once, and the drawn row, its draft row and the noise. 64 requests of 4 rows of 202048 fp32 logits
+// and 3 of the drafts: 105 us, 60 of them for the statistics (6.0 TB/s); one request of 8 x 151936: 19 us, all latencies (the
+// statistics 7, the draw 11: a row's parts, the drafts' probabilities, the race and its join wait for each other); 128 rows of
+// 163841 bf16: 56.
+#include <algorithm>
+#include <type_traits>
 
 #include "mk_ops.cuh"
 
@@ -14,11 +19,12 @@ namespace mkop {
 namespace drafts {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kThreads = 256;
-constexpr int kMaxParts = 32;    // of a row: one a lane
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxParts = 32;    // of a row's statistics: one a lane
+constexpr int kMaxShares = 64;   // of a request's race
 constexpr int kMaxRows = 64;     // of a request
+constexpr int kVectors = 4;      // of 16 bytes that a thread asks for before it uses the first
+constexpr int kFlight = 4;       // of a race's elements (rows and noise begin anywhere, so these loads are of one element)
 
 struct Part {
   float top, sum;  // the largest logit, the sum of exp2((z - top) * c)
@@ -28,7 +34,11 @@ struct Part {
 struct Work {
   mk_verify_drafts_args a;
   int parts;       // of a row
+  int shares;      // of a race
   Part* part;      // [batch * rows + batch * (rows - 1)][parts]
+  float* score;    // [batch][shares] the best quotient of a share and
+  int* score_at;   // [batch][shares] its token
+  int* ended;      // [batch] shares that are there
 };
 
 __device__ inline float exp2_fast(float x) {
@@ -46,12 +56,18 @@ __device__ inline float per_log2(float t) {
   return t > 0.0f ? 1.44269504088896340736f / fminf(fmaxf(t, 0x1p-100f), 0x1p100f) : 0.0f;
 }
 
+// log of a token's probability: its logit z of a row with a largest `top` and a `sum`. (The product is rounded once; a
+// logarithm in 64 bits takes some thousand cycles, and the 32-bit sum has no more to give.)
+__device__ inline float log_p(float z, float top, float sum, float c) {
+  return static_cast<float>((static_cast<double>(logit(z)) - top) * c * 0.6931471805599453 - logf(sum));
+}
+
 // An online softmax's state of one thread. `base`: the largest so far, 0 while there is none.
 struct State {
   float top = -INFINITY, base = 0, sum = 0;
   int at = -1;
   template <int N>
-  __device__ void add(const float (&z)[N], int first, int step, float c) {
+  __device__ void add(const float (&z)[N], int first, float c) {
     float big = z[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) big = fmaxf(big, z[i]);
@@ -60,7 +76,7 @@ struct State {
       top = base = big;
 #pragma unroll
       for (int i = N - 1; i >= 0; --i)
-        if (z[i] == big) at = first + i * step;
+        if (z[i] == big) at = first + i;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) sum += exp2_fast((z[i] - base) * c);
@@ -74,10 +90,31 @@ struct State {
   }
 };
 
+// The logits of 16 bytes
+template <typename T>
+struct Logits {
+  float v[16 / sizeof(T)];
+};
+template <typename T>
+__device__ inline Logits<T> logits_of(const uint4& u) {
+  Logits<T> l;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      l.v[i] = logit(__uint_as_float(w[i]));
+    } else {
+      const float2 f = unpack2<T>(w[i]);
+      l.v[2 * i] = logit(f.x), l.v[2 * i + 1] = logit(f.y);
+    }
+  }
+  return l;
+}
+
 // Part y of row x (target rows, then draft rows).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) stats_kernel(const __grid_constant__ Work w) {
-  __shared__ Part red[kThreads / 32];
+  __shared__ Part red[kWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const mk_verify_drafts_args& a = w.a;
   const int row = blockIdx.x / w.parts, part = blockIdx.x - row * w.parts, tid = threadIdx.x;
@@ -89,11 +126,28 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const __grid_constant__
   const float c = per_log2(a.temperature ? a.temperature[b] : 1.0f);
   const int i0 = static_cast<int>(static_cast<long long>(a.vocab) * part / w.parts);
   const int i1 = static_cast<int>(static_cast<long long>(a.vocab) * (part + 1) / w.parts);
+  if (!draft && part == 0 && tid == 0 && row == b * a.rows) w.ended[b] = 0;
   State s;
-  for (int i = i0 + tid; i < i1; i += kThreads) {
+  // elements up to the first on 16 bytes, vectors, elements behind the last whole one
+  constexpr int kPer = 16 / sizeof(T);
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z + i0) % 16 / sizeof(T));
+  const int v0 = min(i1, i0 + (off ? kPer - off : 0)), nv = (i1 - v0) / kPer;
+  auto one = [&](int i) {
     const float v[1] = {logit(as_float(z[i]))};
-    s.add(v, i, 1, c);
+    s.add(v, i, c);
+  };
+  if (i0 + tid < v0) one(i0 + tid);
+  const uint4* from = reinterpret_cast<const uint4*>(z + v0);
+  int k = tid;
+  for (; k + (kVectors - 1) * kThreads < nv; k += kVectors * kThreads) {
+    uint4 u[kVectors];
+#pragma unroll
+    for (int x = 0; x < kVectors; ++x) u[x] = from[k + x * kThreads];
+#pragma unroll
+    for (int x = 0; x < kVectors; ++x) s.add(logits_of<T>(u[x]).v, v0 + (k + x * kThreads) * kPer, c);
   }
+  for (; k < nv; k += kThreads) s.add(logits_of<T>(from[k]).v, v0 + k * kPer, c);
+  if (v0 + nv * kPer + tid < i1) one(v0 + nv * kPer + tid);
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
     const float otop = __shfl_xor_sync(~0u, s.top, d), osum = __shfl_xor_sync(~0u, s.sum, d);
@@ -103,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const __grid_constant__
   if ((tid & 31) == 0) red[tid >> 5] = {s.top, s.sum, s.at, 0};
   __syncthreads();
   if (tid == 0) {
-    for (int k = 1; k < kThreads / 32; ++k) s.join(red[k].top, red[k].sum, red[k].at, c);
+    for (int k = 1; k < kWarps; ++k) s.join(red[k].top, red[k].sum, red[k].at, c);
     w.part[static_cast<long long>(row) * w.parts + part] = {s.top, s.sum, s.at, 0};
   }
 }
@@ -121,22 +175,41 @@ struct Chosen {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) draw_kernel(const __grid_constant__ Work w, int ctas) {
+__global__ void __launch_bounds__(kThreads, 6) draw_kernel(const __grid_constant__ Work w) {
   __shared__ Part stats[2 * kMaxRows];
   __shared__ Chosen chosen;
-  __shared__ float best_score[kThreads / 32];
-  __shared__ int best_at[kThreads / 32];
-  __shared__ float mine_score;
-  __shared__ int mine_at;
+  __shared__ float draft_log_p[kMaxRows];
+  __shared__ int verdict[kMaxRows];  // 1: taken, 0: refused, -1: no token of the vocabulary
+  __shared__ float best_score[kWarps];
+  __shared__ int best_at[kWarps];
+  __shared__ bool last;
   const mk_verify_drafts_args& a = w.a;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float t = a.temperature ? a.temperature[b] : 1.0f;
-  const float c = per_log2(t);
+  const int b = blockIdx.x / w.shares, share = blockIdx.x - b * w.shares, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rows = a.rows, all = a.draft_logits ? 2 * rows - 1 : rows;
+  const float c = per_log2(a.temperature ? a.temperature[b] : 1.0f);
+  const T* z = static_cast<const T*>(a.logits) + static_cast<long long>(b) * rows * a.logits_stride;
+  const T* y = static_cast<const T*>(a.draft_logits) + static_cast<long long>(b) * (rows - 1) * a.draft_stride;
+  // ---- what the drafts need of the inputs, before the statistics are there (the first kernel began after whatever wrote the inputs)
+  const int asked = a.n_drafts ? a.n_drafts[b] : rows - 1, n = min(max(asked, 0), rows - 1);
+  int x = -1;
+  float zx = 0, yx = 0, uniform = 0;
+  if (tid < n) {
+    x = a.tokens[static_cast<long long>(b) * rows + tid + 1];
+    uniform = a.uniforms[static_cast<long long>(b) * (rows - 1) + tid];
+    if (x >= 0 && x < a.vocab) {
+      zx = as_float(z[tid * a.logits_stride + x]);
+      if (a.draft_logits) yx = as_float(y[tid * a.draft_stride + x]);
+    }
+  }
+  const float* noise = a.noise + b * a.noise_stride;
+  const int i0 = static_cast<int>(static_cast<long long>(a.vocab) * share / w.shares);
+  const int i1 = static_cast<int>(static_cast<long long>(a.vocab) * (share + 1) / w.shares);
+  // (and the noise on its way: a request alone 21.0 -> 19.3 us)
+  if (c != 0.0f)
+    for (int i = i0 + tid * 32; i < i1; i += kThreads * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + i));
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- the rows' statistics ----------------------------------------------------------------------------------------
-  const int rows = a.rows, all = a.draft_logits ? 2 * rows - 1 : rows;
-  for (int r = warp; r < all; r += kThreads / 32) {
+  for (int r = warp; r < all; r += kWarps) {
     const long long row = r < rows ? static_cast<long long>(b) * rows + r
                                    : static_cast<long long>(a.batch) * rows + static_cast<long long>(b) * (rows - 1) + r - rows;
     State s;
@@ -153,36 +226,30 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const __grid_constant__ 
     if (lane == 0) stats[r] = {s.top, s.sum, s.at, 0};
   }
   __syncthreads();
-  const T* z = static_cast<const T*>(a.logits) + static_cast<long long>(b) * rows * a.logits_stride;
-  const T* y = static_cast<const T*>(a.draft_logits) + static_cast<long long>(b) * (rows - 1) * a.draft_stride;
-  // ---- the drafts, by the first thread of each CTA -------------------------------------------------------------------
-  if (tid == 0) {
-    const bool says = rank == 0;  // one CTA writes
-    int n = a.n_drafts ? a.n_drafts[b] : rows - 1;
-    if (n < 0 || n > rows - 1) {
-      if (says) flag(a.status, MK_OP_BAD_LENGTH);
-      n = min(max(n, 0), rows - 1);
-    }
-    // log of the probability of a row's token
-    auto log_p = [&](const T* row, const Part& s, int x) -> double {
+  // ---- the drafts, each by a thread, up to the first that is refused ---------------------------------------------------
+  const bool says = share == 0;  // one CTA writes
+  if (tid < n) {
+    auto log_of = [&](float logit_x, const Part& s) -> float {
       if (s.at < 0) return -INFINITY;
-      if (c == 0.0f) return x == s.at ? 0.0 : -INFINITY;
-      return (static_cast<double>(logit(as_float(row[x]))) - s.top) * c * 0.6931471805599453 - log(static_cast<double>(s.sum));
+      if (c == 0.0f) return x == s.at ? 0.0f : -INFINITY;
+      return log_p(logit_x, s.top, s.sum, c);
     };
-    int r = 0;
-    for (; r < n; ++r) {
-      const int x = a.tokens[static_cast<long long>(b) * rows + r + 1];
-      bool good = false;
-      if (x < 0 || x >= a.vocab) {
-        if (says) flag(a.status, MK_OP_BAD_TOKEN);
-      } else {
-        const double lp = log_p(z + r * a.logits_stride, stats[r], x);
-        const double q = a.draft_logits ? exp(log_p(y + r * a.draft_stride, stats[rows + r], x)) : 1.0;
-        good = a.uniforms[static_cast<long long>(b) * (rows - 1) + r] * q < exp(lp);
-        if (good && says && a.logprobs) a.logprobs[static_cast<long long>(b) * rows + r] = static_cast<float>(lp);
-      }
-      if (!good) break;
+    int good = -1;
+    if (x >= 0 && x < a.vocab) {
+      const float lp = log_of(zx, stats[tid]), q = a.draft_logits ? expf(log_of(yx, stats[rows + tid])) : 1.0f;
+      // (the product in 64 bits: a uniform number below 1 of equal probabilities is below them)
+      good = static_cast<double>(uniform) * q < expf(lp);
+      draft_log_p[tid] = lp;
     }
+    verdict[tid] = good;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (says && asked != n) flag(a.status, MK_OP_BAD_LENGTH);
+    int r = 0;
+    for (; r < n && verdict[r] == 1; ++r)
+      if (says && a.logprobs) a.logprobs[static_cast<long long>(b) * rows + r] = draft_log_p[r];
+    if (says && r < n && verdict[r] < 0) flag(a.status, MK_OP_BAD_TOKEN);
     chosen.row = r;
     chosen.cut = r < n;
     chosen.top = stats[r].top;
@@ -196,25 +263,46 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const __grid_constant__ 
   const Chosen ch = chosen;
   const T* zr = z + ch.row * a.logits_stride;
   int token = ch.token;
-  if (ch.token >= 0 && c != 0.0f) {
+  const bool race = ch.token >= 0 && c != 0.0f;
+  if (!race && share) return;
+  if (race) {
     // ---- the race ----------------------------------------------------------------------------------------------------
-    const float* noise = a.noise + b * a.noise_stride;
     const T* yr = y + ch.row * a.draft_stride;
     const int out = ch.cut && !a.draft_logits ? a.tokens[static_cast<long long>(b) * rows + ch.row + 1] : -1;  // not drawn
     const bool minus = ch.cut && a.draft_logits && ch.draft_top > -INFINITY;
     const float by = 1.0f / ch.sum, draft_by = minus ? 1.0f / ch.draft_sum : 0.0f;
-    const int i0 = static_cast<int>(static_cast<long long>(a.vocab) * rank / ctas);
-    const int i1 = static_cast<int>(static_cast<long long>(a.vocab) * (rank + 1) / ctas);
-    for (int pass = 0; pass < 2; ++pass) {  // the second one where max(p - q, 0) is 0 everywhere
-      float score = 0;
-      int at = -1;
-      for (int i = i0 + tid; i < i1; i += kThreads) {
-        // (rounded products, so that equal probabilities leave 0 and not what a fused difference would)
-        float p = __fmul_rn(exp2_fast((logit(as_float(zr[i])) - ch.top) * c), by);
-        if (pass == 0 && minus) p -= __fmul_rn(exp2_fast((logit(as_float(yr[i])) - ch.draft_top) * c), draft_by);
-        if (pass == 0 && i == out) p = 0.0f;
-        const float s = __fdividef(p, noise[i]);
-        if (s > score) score = s, at = i;
+    // The best of tokens from .. to - 1, for every thread. `cut`: of max(p - q, 0), or without `out`.
+    auto best = [&](int from, int to, bool cut, float& score, int& at) {
+      score = 0, at = -1;
+      const bool less = cut && minus;
+      const int left_out = cut ? out : -1;
+      // Batches that end inside to and are without the token left out have no comparisons of indices, and loads from one address.
+      auto batch = [&](int i, auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        T p_in[kFlight], q_in[kFlight];
+        float e[kFlight];
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const int j = kWhole ? i + k * kThreads : min(i + k * kThreads, to - 1);
+          p_in[k] = zr[j];
+          e[k] = noise[j];
+          if (less) q_in[k] = yr[j];
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const int j = i + k * kThreads;
+          // (rounded products, so that equal probabilities leave 0 and not what a fused difference would)
+          float p = __fmul_rn(exp2_fast((logit(as_float(p_in[k])) - ch.top) * c), by);
+          if (less) p -= __fmul_rn(exp2_fast((logit(as_float(q_in[k])) - ch.draft_top) * c), draft_by);
+          if (!kWhole && (j >= to || j == left_out)) p = 0.0f;
+          const float s = __fdividef(p, e[k]);
+          if (s > score) score = s, at = j;
+        }
+      };
+      for (int first = from; first < to; first += kFlight * kThreads) {
+        const int end = first + kFlight * kThreads;
+        if (end <= to && (left_out < first || left_out >= end)) batch(first + tid, std::true_type{});
+        else batch(first + tid, std::false_type{});
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) {
@@ -224,28 +312,41 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const __grid_constant__ 
       }
       if (lane == 0) best_score[warp] = score, best_at[warp] = at;
       __syncthreads();
+      for (int k = 0; k < kWarps; ++k) better(score, at, best_score[k], best_at[k]);
+      __syncthreads();
+    };
+    float score;
+    best(i0, i1, ch.cut, score, token);
+    if (w.shares > 1) {
+      const long long place = static_cast<long long>(b) * w.shares;
       if (tid == 0) {
-        for (int k = 1; k < kThreads / 32; ++k) better(score, at, best_score[k], best_at[k]);
-        mine_score = score, mine_at = at;
+        w.score[place + share] = score, w.score_at[place + share] = token;
+        __threadfence();
+        last = atomicAdd(&w.ended[b], 1) == w.shares - 1;
+        __threadfence();
       }
-      cluster.sync();
-      score = 0, at = -1;
-      for (int k = 0; k < ctas; ++k) better(score, at, *cluster.map_shared_rank(&mine_score, k), *cluster.map_shared_rank(&mine_at, k));
-      token = at;
-      cluster.sync();  // the others' results stay until they have been read
-      if (token >= 0 || !ch.cut) break;
+      __syncthreads();
+      if (!last) return;
+      // (every warp; a share's place has been written by another CTA of this launch)
+      score = 0, token = -1;
+      for (int k = lane; k < w.shares; k += 32) better(score, token, __ldcg(&w.score[place + k]), __ldcg(&w.score_at[place + k]));
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        const float os = __shfl_xor_sync(~0u, score, d);
+        const int oa = __shfl_xor_sync(~0u, token, d);
+        better(score, token, os, oa);
+      }
     }
+    // max(p - q, 0) is 0 everywhere, as far as fp32 shows it: a draw from p (too seldom to share)
+    if (token < 0 && ch.cut) best(0, a.vocab, false, score, token);
   }
-  if (rank == 0 && tid == 0) {
+  if (tid == 0) {
     a.accept_out[b] = ch.row + 1;
     a.accept_out[a.batch + b] = token;
     a.accept_out[2 * a.batch + b] = (a.positions ? a.positions[b] : 0) + ch.row + 1;
     if (a.logprobs) {
       float lp = -INFINITY;
-      if (token >= 0)
-        lp = c == 0.0f ? 0.0f
-                       : static_cast<float>((static_cast<double>(logit(as_float(zr[token]))) - ch.top) * c * 0.6931471805599453 -
-                                            log(static_cast<double>(ch.sum)));
+      if (token >= 0) lp = c == 0.0f ? 0.0f : log_p(as_float(zr[token]), ch.top, ch.sum, c);
       a.logprobs[static_cast<long long>(b) * rows + ch.row] = lp;
     }
   }
@@ -262,11 +363,19 @@ mk_status check_shape(const mk_verify_drafts_args& a, int device) {
 }
 
 int parts_of(const mk_verify_drafts_args& a) {
-  const int parts = (a.vocab + 16383) / 16384;
+  // parts of 16384 elements; where that leaves SMs with less than they hold, more and smaller ones (one request of 15 rows: 480 parts
+  // instead of 150, statistics 12 -> 7 us)
+  const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(a.batch) * (2 * a.rows - 1));
+  const int parts = std::max<int64_t>((a.vocab + 16383) / 16384, std::min<int64_t>(152 * 8 / rows, (a.vocab + 1023) / 1024));
   return parts > kMaxParts ? kMaxParts : parts;
 }
+// So many shares that the GPU holds all requests' at once (6 CTAs an SM; 4 of them with 8 elements in flight leave more SMs with one
+// less than others: 128 rows 58.0 -> 55.6 us), of 1024 tokens at least
+int shares_of(const mk_verify_drafts_args& a) {
+  return std::max<int64_t>(1, std::min<int64_t>({kMaxShares, 152 * 6 / std::max(1, a.batch), (a.vocab + 1023) / 1024}));
+}
 uint64_t workspace_of(const mk_verify_drafts_args& a) {
-  return static_cast<uint64_t>(a.batch) * (2 * a.rows - 1) * parts_of(a) * sizeof(Part);
+  return static_cast<uint64_t>(a.batch) * ((2 * a.rows - 1) * static_cast<uint64_t>(parts_of(a)) * sizeof(Part) + (2 * shares_of(a) + 1) * 4);
 }
 
 mk_status check(const mk_verify_drafts_args& a, int device) {
@@ -292,23 +401,20 @@ mk_status check(const mk_verify_drafts_args& a, int device) {
 }
 
 template <typename T>
-cudaError_t launch(const Work& w, int ctas, cudaStream_t s) {
+cudaError_t launch(const Work& w, cudaStream_t s) {
   const mk_verify_drafts_args& a = w.a;
   const unsigned all = static_cast<unsigned>(a.batch) * (a.draft_logits ? 2 * a.rows - 1 : a.rows);
   if (const cudaError_t e = start(stats_kernel<T>, all * w.parts, kThreads, 0, s, w)) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.batch * ctas);
+  cfg.gridDim = dim3(a.batch * w.shares);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, draw_kernel<T>, w, ctas);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, draw_kernel<T>, w);
 }
 
 }  // namespace
@@ -339,9 +445,11 @@ extern "C" mk_status mk_verify_drafts(const mk_verify_drafts_args* p, int device
   w.a = *p;
   if (w.a.rows == 1) w.a.draft_logits = nullptr;
   w.parts = parts_of(w.a);
+  w.shares = shares_of(w.a);
   w.part = static_cast<Part*>(w.a.workspace);
-  const int ctas = 8;
+  w.score = reinterpret_cast<float*>(w.part + static_cast<int64_t>(p->batch) * (2 * p->rows - 1) * w.parts);
+  w.score_at = reinterpret_cast<int*>(w.score + static_cast<int64_t>(p->batch) * w.shares);
+  w.ended = w.score_at + static_cast<int64_t>(p->batch) * w.shares;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return launched(kMe, p->dtype == MK_BF16 ? launch<__nv_bfloat16>(w, ctas, s)
-                       : p->dtype == MK_F16 ? launch<__half>(w, ctas, s) : launch<float>(w, ctas, s));
+  return launched(kMe, p->dtype == MK_BF16 ? launch<__nv_bfloat16>(w, s) : p->dtype == MK_F16 ? launch<__half>(w, s) : launch<float>(w, s));
 }
