@@ -1,8 +1,8 @@
 // mk_rms_norm: root-mean-square norm of rows with the residual's addition and, where asked, e4m3 results with scales.
 //
 // Bound by memory: each value is read once and written once, with about 10 operations in between. A CTA has a row and
-// keeps it in registers (8 elements a thread and round), so the norm's second look at it costs nothing: all loads are in
-// flight together, one block-wide sum, one look at the registers, stores. A scale's group of at most 256 columns
+// keeps it in registers (8 elements a thread and round, up to 4 rounds), so the norm's second look at it costs nothing: all loads
+// are in flight together, one block-wide sum, one look at the registers, stores. A scale's group of at most 256 columns
 // lies with neighbouring lanes (shuffles); a scale for the whole row takes a second block-wide step.
 #include "mk_ops.cuh"
 
@@ -64,7 +64,7 @@ __device__ inline float of_block(float x, float* red) {
 }
 
 template <typename T, int ROUNDS, bool E4M3>
-__global__ void __launch_bounds__(ROUNDS > 2 ? 512 : kMaxThreads) norm_kernel(const __grid_constant__ mk_rms_norm_args a) {
+__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const __grid_constant__ mk_rms_norm_args a) {
   __shared__ float red[2][kMaxThreads / 32];
   const long long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
@@ -158,8 +158,7 @@ template <typename T, bool E4M3>
 cudaError_t launch(const mk_rms_norm_args& a, int rounds, int threads, cudaStream_t s) {
   return rounds == 1   ? start(norm_kernel<T, 1, E4M3>, a.rows, threads, 0, s, a)
          : rounds == 2 ? start(norm_kernel<T, 2, E4M3>, a.rows, threads, 0, s, a)
-         : rounds == 4 ? start(norm_kernel<T, 4, E4M3>, a.rows, threads, 0, s, a)
-                       : start(norm_kernel<T, 8, E4M3>, a.rows, threads, 0, s, a);
+                       : start(norm_kernel<T, 4, E4M3>, a.rows, threads, 0, s, a);
 }
 
 }  // namespace
@@ -202,7 +201,11 @@ extern "C" mk_status mk_rms_norm(const mk_rms_norm_args* p, int device, void* st
   DeviceGuard guard(device);
   if (guard.err != cudaSuccess) return launched(me, guard.err);
   const int vectors = a.width / 8;
-  const int rounds = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 8;
+  // One round is best where an SM has one row (1 x 5120 bf16: 6.8 us, 2 rounds 8.1, 4 rounds 8.9) and in fp32, where a round is 32
+  // bytes already (4000 x 5120: 54.9 us, 56.0, 60.1); 16 bits are better with 4 (8191 x 6144 to e4m3: 84.6 us, 72.4, 66.2; 512 x 7168
+  // 17.1, 15.0, 13.6): an SM has several rows, one's loads run beside another's sums and stores.
+  int rounds = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 4;
+  if (a.rows > 152 && a.dtype != MK_F32 && vectors >= 64) rounds = vectors >= 128 ? 4 : 2;
   const int threads = (vectors + rounds * 32 - 1) / (rounds * 32) * 32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = a.dtype == MK_BF16  ? e4m3 ? launch<__nv_bfloat16, true>(a, rounds, threads, s) : launch<__nv_bfloat16, false>(a, rounds, threads, s)
