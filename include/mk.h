@@ -558,13 +558,13 @@ mk_status mk_paged_attention_workspace(const mk_paged_attention_args* args, int 
  * table[b][p / page_size], so own pages begin a page of their own wherever the prefix ends. out and lse are of one softmax over both;
  * a row that sees nothing gives out = 0 and lse = -infinity.
  * prefix_len counts as within 0 .. max_prefix_pages * page_size (MK_OP_BAD_LENGTH). All else (types, scales, lengths, pages
- * out of range, what unseen values may hold, infinities) is as in mk_paged_attention, and own positions are computed by it, in fp32 up to
- * the sum of both parts. Over the prefix probabilities are rounded once to 16 bits before they meet the values (2^-8 of
- * each in bf16, 2^-11 in fp16 and over e4m3 caches, which is at most what out's own rounding takes); fp16 ones below 2^-38 of a row's
- * largest may vanish. Sums and statistics are fp32.
+ * out of range, what unseen values may hold, infinities) is as in mk_paged_attention. Probabilities are rounded once to 16 bits before
+ * they meet the values (2^-8 of each in bf16, 2^-11 in fp16 and over e4m3 caches, which is at most what out's own rounding
+ * takes); fp16 ones below 2^-38 of a row's largest may vanish. Sums and statistics are fp32.
  * The result does not depend on timing. `workspace`: mk_prefix_attention_workspace bytes of device scratch, 16-byte aligned, any
- * contents; calls that may overlap need one each. Three launches, or four.
- * Errors: as mk_paged_attention; batch * rows * n_q_heads / n_kv_heads beyond 2^24. */
+ * contents; calls that may overlap need one each. Two launches.
+ * Errors: as mk_paged_attention; batch * rows * n_q_heads / n_kv_heads beyond 2^24, batch * rows * n_q_heads beyond 2^31 - 64, tables that
+ * reach beyond position 2^31 - 1024. */
 typedef struct mk_prefix_attention_args {
   const void* q;               /* device [batch][rows][n_q_heads][head_dim], dtype                  */
   const void* k_pages;         /* device, cache_dtype                                             */
@@ -686,8 +686,8 @@ mk_status mk_rms_norm(const mk_rms_norm_args* args, int device, void* stream);
  * Temperatures above 0 count as within 2^-100 .. 2^100. Logits that are NaN count as -infinity; where a row has some of +infinity, these share it. Noise below 0 or NaN: the token is
  * not drawn; 0: it comes before all others. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
  * as within 0 .. rows - 1 (MK_OP_BAD_LENGTH).
- * Weights and sums are fp32: where uniforms * q and p, or the two largest quotients, are within 2^-18 of each other,
- * either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.
+ * Weights, sums and log-probabilities are fp32: where uniforms * q and p, or the two largest quotients, are within 2^-17 of each other
+ * (for probabilities of e^-x: x / 2^22 more), either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.
  * `workspace`: mk_verify_drafts_workspace bytes of device scratch, 16-byte aligned, any contents; calls that may
  * overlap need one each. Two launches. */
 typedef struct mk_verify_drafts_args {
