@@ -362,20 +362,27 @@ mk_status check_shape(const mk_verify_drafts_args& a, int device) {
   return check_device(kMe, device);
 }
 
+// CTAs that the GPU holds at once: of the statistics 8 an SM, of the race 6
+constexpr int64_t kStatsCtas = 152 * 8, kRaceCtas = 152 * 6;
+
+int64_t all_rows(const mk_verify_drafts_args& a) { return static_cast<int64_t>(a.batch) * (2 * a.rows - 1); }
+int whole_parts(const mk_verify_drafts_args& a) { return std::min(kMaxParts, (a.vocab + 16383) / 16384); }
+// parts of 16384 elements; where that leaves SMs with less than they hold, more and smaller ones (one request of 15 rows: 480 parts
+// instead of 150, statistics 12 -> 7 us)
 int parts_of(const mk_verify_drafts_args& a) {
-  // parts of 16384 elements; where that leaves SMs with less than they hold, more and smaller ones (one request of 15 rows: 480 parts
-  // instead of 150, statistics 12 -> 7 us)
-  const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(a.batch) * (2 * a.rows - 1));
-  const int parts = std::max<int64_t>((a.vocab + 16383) / 16384, std::min<int64_t>(152 * 8 / rows, (a.vocab + 1023) / 1024));
-  return parts > kMaxParts ? kMaxParts : parts;
+  const int64_t more = std::min<int64_t>({kMaxParts, kStatsCtas / std::max<int64_t>(1, all_rows(a)), (a.vocab + 1023) / 1024});
+  return std::max<int64_t>(whole_parts(a), more);
 }
 // So many shares that the GPU holds all requests' at once (6 CTAs an SM; 4 of them with 8 elements in flight leave more SMs with one
 // less than others: 128 rows 58.0 -> 55.6 us), of 1024 tokens at least
 int shares_of(const mk_verify_drafts_args& a) {
-  return std::max<int64_t>(1, std::min<int64_t>({kMaxShares, 152 * 6 / std::max(1, a.batch), (a.vocab + 1023) / 1024}));
+  return std::max<int64_t>(1, std::min<int64_t>({kMaxShares, kRaceCtas / std::max(1, a.batch), (a.vocab + 1023) / 1024}));
 }
+// What any such parts and shares take: never less for more requests, rows or tokens.
 uint64_t workspace_of(const mk_verify_drafts_args& a) {
-  return static_cast<uint64_t>(a.batch) * ((2 * a.rows - 1) * static_cast<uint64_t>(parts_of(a)) * sizeof(Part) + (2 * shares_of(a) + 1) * 4);
+  const int64_t parts = std::max(all_rows(a) * whole_parts(a), std::min(all_rows(a) * kMaxParts, kStatsCtas));
+  const int64_t shares = std::max<int64_t>(a.batch, std::min<int64_t>(static_cast<int64_t>(a.batch) * kMaxShares, kRaceCtas));
+  return parts * sizeof(Part) + shares * (sizeof(float) + sizeof(int)) + a.batch * sizeof(int);
 }
 
 mk_status check(const mk_verify_drafts_args& a, int device) {

@@ -710,7 +710,8 @@ typedef struct mk_verify_drafts_args {
 } mk_verify_drafts_args;
 mk_status mk_verify_drafts(const mk_verify_drafts_args* args, int device, void* stream);
 
-/* Bytes of workspace mk_verify_drafts needs (batch, rows and vocab decide; nothing is read through a pointer). */
+/* Bytes of workspace mk_verify_drafts needs (batch, rows and vocab decide, and more of them never need less; nothing is read
+ * through a pointer). */
 mk_status mk_verify_drafts_workspace(const mk_verify_drafts_args* args, int device, uint64_t* bytes);
 
 /* What mk_verify_drafts would return for these arguments, short of enqueueing anything. */

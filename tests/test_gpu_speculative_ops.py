@@ -390,6 +390,36 @@ def test_verify_drafts_tokens_and_counts_out_of_range():
         assert accept[0, same].item() == 4
 
 
+def test_verify_drafts_refused_where_draft_and_target_agree():
+    """Long rows, raced in many shares: the draft's own distribution leaves nothing, so the token comes from the target's."""
+    s = draft_inputs(5, 2, 30011, F32, seed=21)
+    s["draft_logits"] = s["logits"].view(5, 2, -1)[:, 0].clone()
+    s["tokens"][:, 1] = -1
+    s["n_drafts"] = i32([1] * 5)
+    accept, lp = run_drafts(s, status=i32([0]))
+    check_drafts(s, accept, lp)
+    assert (accept[0] == 1).all() and (accept[1] >= 0).all()
+
+
+def test_verify_drafts_workspace_of_the_largest_call_fits_all():
+    """One buffer of any contents for calls of all shapes, one after another."""
+    from decode_megakernel_04_gb300 import verify_drafts_workspace
+    shapes = [(1, 1, 1), (1, 8, 20000), (3, 8, 20000), (33, 2, 20000), (36, 2, 20000), (64, 2, 20000), (64, 8, 20000), (64, 8, 40000)]
+    last = 0
+    for batch, rows, vocab in shapes:  # each at least as large as the one before
+        size = verify_drafts_workspace(torch.empty(batch * rows, vocab, device=DEV), torch.empty(batch, rows, dtype=torch.int32, device=DEV))
+        assert size >= last
+        last = size
+    ws = torch.full((last + 16,), 255, dtype=torch.uint8, device=DEV)
+    for k in (7, 1, 3, 0, 6, 2, 1):
+        s = draft_inputs(*shapes[k], F32, seed=30 + k)
+        accept, lp = run_drafts(s, workspace=ws[:last])
+        check_drafts(s, accept, lp)
+        again = run_drafts(s)
+        assert torch.equal(again[0], accept) and torch.equal(again[1], lp)
+    assert (ws[last:] == 255).all()
+
+
 def test_verify_drafts_defaults():
     s = draft_inputs(5, 3, 777, F32, seed=6)
     for k in ("temperature", "n_drafts", "positions"):
@@ -623,6 +653,16 @@ def test_prefix_scores_of_any_size():
             s["k"][s["table"][0, 0].long()] *= 8
         got, lse = run_prefix(s, scale=1.0)
         check_prefix(s, got, lse, 1.0)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30])
+@pytest.mark.parametrize("dtype, cache, d", [(BF16, BF16, 128), (F16, F16, 64), (BF16, BF16, 256), (BF16, E4M3, 128), (F16, E4M3, 64)])
+def test_prefix_scales_of_any_sign(dtype, cache, d, scale):
+    """Also e4m3 caches whose heads' scales have different signs."""
+    s = prefix_inputs(300, [40, 3, 200], 3, 12, 2, d, 16, dtype, cache, seed=17)
+    if s["ks"] is not None:
+        s["ks"][1] *= -1
+    check_prefix(s, *run_prefix(s, scale=scale), scale)
 
 
 @pytest.mark.parametrize("cache", [BF16, E4M3])
