@@ -7,7 +7,9 @@
 // - Work: 128 query rows of a kv head are a row tile. Three lines of key tiles, each cut into equal pieces, one piece a CTA:
 //   pairs of row tiles over the prefix (a tile of keys and values is read once for 256 rows), single row tiles over the prefix
 //   (an odd one; all of them 256 wide, where the tensor memory holds one), and row tiles of one request (of up to 8 of its
-//   new rows) over its own keys. CTAs are dealt to the lines in proportion to their products, by a rule on the lengths alone.
+//   new rows) over its own keys. CTAs are dealt to the lines by what their tiles take, a rule on the lengths alone; an item over
+//   own keys counts as two tiles more (with CTAs dealt and cut by tiles alone, 64 requests behind 32768 positions took 128 us
+//   instead of 117: those with many short requests ended last).
 //   Where a CTA has one row tile, even and odd key tiles go to two sets of sums, so that there are two streams of work
 //   in any case (one 256 wide).
 // - Units: the product of one row tile and one key tile. A warp for each stream issues S of its first unit, then for each
@@ -19,14 +21,18 @@
 // - Loads: warps for keys and for values copy boxes of a page's rows (TMA, through the page table) into a ring of slots
 //   each; a copy takes its warp 140 cycles, so the two 64-column pieces of a tile have a warp each. Over own keys few query rows
 //   leave room for a third tile, which memory's latency under load asks for. (Prefetches into L2 by warps of their own
-//   made it slower, 169 us against 127 for the 64 requests below.) Codes of e4m3 caches go through a stage of 64 rows, from
-//   where two warps each make fp16 of them. Queries are stored by the softmax threads; those of the next item while the last
-//   product of this one runs.
+//   made it slower, 169 us against 127 for the 64 requests below.) Codes of e4m3 caches land in the half of their slot where two
+//   warps each make fp16 of them in place (through stages of 64 rows of their own, half as many bytes were on their way: 65536
+//   positions 175 us instead of 154). Queries are stored by the softmax threads, an item ahead where there is room for two.
 // - Keys that not every row of a request's tile sees (at most 7) have probability 0 in the others. Should their values hold an
 //   infinity or NaN (0 times that is NaN), they are left out of the product and added one by one by the rows that see them.
 // Probabilities are one 16-bit number (a pair hi + lo would be half as much work again for the tensor cores). bf16: 2^-8 of each
 // at most; fp16: 2^-11, against a base 14 under the maximum, so that what falls under its range is 2^-39 of the largest. Sums of
 // probabilities are those of the unrounded ones.
+// Measured: 64 requests behind 32768 positions with own ones of up to 2000 (48/8 heads of 128, bf16) 118 us, 32 x 8 rows behind
+// 8191 93 us (590 TFLOP/s), 64 requests behind 65536 in e4m3 154 us (670 TFLOP/s), 4 samples of 4096 positions 256 wide 25 us. What bounds
+// it is the chain of products, scores out of tensor memory, softmax and probabilities back: a pair's tile takes about 3700 cycles,
+// 3300 with almost all products left out and 3500 without exponentials, and two streams are all that tensor memory holds.
 // Every wait has a limit (2 s), after which the CTA gives up, drains and frees what it holds and MK_OP_TIMEOUT is set.
 #pragma once
 #include <cuda.h>
@@ -49,9 +55,11 @@ constexpr int kTileRows = 128;        // query rows of a row tile
 constexpr int kGroupRows = 8;         // new rows of a request that share an item over its own keys
 constexpr int kItemTiles = 2;         // what an item over own keys takes besides its tiles, in tiles
 enum { kPairs, kSingles, kOwn };      // the lines
-// What a tile of a line takes of a CTA (in 250 cycles, 128 wide)
+// What a tile of a line takes of a CTA, in parts of 12 of a pair's: as measured 128 wide, where a pair's tile takes 1.85 to 2.1 us, a single
+// one 1.3 to 1.4, one of an item (with its share of the two for the item) 1.35 to 1.6. With 12 / 12 / 12 instead, 64 requests behind
+// 32768 positions take 136 us and not 118, in e4m3 behind 65536 179 and not 154, 32 x 8 rows 95 and not 93.
 template <bool E4M3>
-constexpr int kLineCost[3] = {12, E4M3 ? 11 : 9, E4M3 ? 11 : 9};
+constexpr int kLineCost[3] = {12, E4M3 ? 8 : 9, E4M3 ? 10 : 9};
 
 // What the first CTA writes for the join. Piece c's part of item i of a line goes to place c + i (after `place0`): along the line
 // either grows by one from part to part.
@@ -86,7 +94,7 @@ struct PrefixParams {
   float2* own_ml;     // [places][streams][own_rows] over own keys
   Head* head;
   long long* cum;     // [batch * groups + 1] as total[kOwn], of the row groups so far (of one row tile)
-  int box;            // rows of a copied box: the largest power of two that divides the page size, up to the slot or stage
+  int box;            // rows of a copied box: the largest power of two that divides the page size, up to a tile
   CUtensorMap keys, values;  // [n_pages][n_kv_heads][page_size][head_dim]
   __device__ int first_single() const { return blocks[kPairs] * 2 * kTileRows; }
   __device__ int rows_of(int group_index) const { return min(kGroupRows, a.rows - group_index * kGroupRows); }
@@ -150,14 +158,16 @@ struct PrefixShape {
   static constexpr int kWide = D == 256 ? 128 : D;          // columns of a slot
   static constexpr int kPieces = kWide / 64;                // of 64 columns: [128 rows][128 bytes] each
   static constexpr int kSlot = kPrefixTile * kWide * 2;
-  static constexpr int kKeySlots = D == 64 ? 4 : 2, kValueSlots = D == 64 ? 4 : 2;
-  static constexpr int kStageRows = 64, kStages = D == 256 ? 1 : 2, kStage = kStageRows * 128;  // codes
+  static constexpr int kKeySlots = E4M3 ? 3 : D == 64 ? 4 : 2, kValueSlots = D != 64 ? 2 : E4M3 ? 3 : 4;
   static constexpr int kConverters = 64;                    // threads, of keys and of values
+  // Codes of a tile arrive in the second half of their slot, where their row of fp16 values goes; 64 wide, in places of their own.
+  static constexpr bool kInPlace = E4M3 && kWide == 128;
+  static constexpr int kCodes = kPrefixTile * 128;          // rows of 128 bytes (zeros behind a head's columns)
   static constexpr int kQ = kTileRows * D * 2;              // a stream's queries
   // Queries, keys' slots, values' slots. 128 wide, 16 bits, items of up to 64 or 32 rows: 5 or 6 slots and queries twice.
   static constexpr bool kFewRows = D == 128 && !E4M3;
-  static constexpr int kOffStage = kFewRows ? 7 * kSlot : (kKeySlots + kValueSlots) * kSlot + kStreams * kQ;  // [keys, values][kStages]
-  static constexpr int kOffBar = kOffStage + (E4M3 ? 2 * kStages * kStage : 0);
+  static constexpr int kOffCodes = kFewRows ? 7 * kSlot : (kKeySlots + kValueSlots) * kSlot + kStreams * kQ;  // [keys, values][slots]
+  static constexpr int kOffBar = kOffCodes + (E4M3 && !kInPlace ? (kKeySlots + kValueSlots) * kCodes : 0);
   static constexpr int kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -180,7 +190,7 @@ struct Ring {
 };
 
 struct PrefixBars {
-  uint64_t key_full[6], key_empty[6], value_full[6], value_empty[6], stage_full[4], stage_empty[4];
+  uint64_t key_full[6], key_empty[6], value_full[6], value_empty[6], codes_full[12];
   uint64_t q_full[4], s_full[2], p_full[2], pv_done[2], issued[2], tail[2], drained;
   uint32_t tmem;
   int dead;
@@ -400,11 +410,11 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
       bar_init(&bars.key_full[i], E4M3 ? S::kConverters : S::kPieces), bar_init(&bars.key_empty[i], line == kPairs ? 2 : 1);
       bar_init(&bars.value_full[i], E4M3 ? S::kConverters : S::kPieces), bar_init(&bars.value_empty[i], line == kPairs ? 2 : 1);
     }
-    for (int i = 0; i < 4; ++i) bar_init(&bars.stage_full[i], 1), bar_init(&bars.stage_empty[i], S::kConverters);
+    for (int i = 0; i < 12; ++i) bar_init(&bars.codes_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       bar_init(&bars.q_full[i], S::kStreamThreads), bar_init(&bars.q_full[2 + i], S::kStreamThreads), bar_init(&bars.s_full[i], 1);
       bar_init(&bars.p_full[i], S::kStreamThreads), bar_init(&bars.pv_done[i], 1), bar_init(&bars.issued[i], 1);
-      bar_init(&bars.tail[i], 1);
+      bar_init(&bars.tail[i], E4M3 ? 2 : 1);
     }
     bar_init(&bars.drained, S::kStreams);
     bars.dead = 0;
@@ -455,13 +465,13 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
       // ---- loaders: keys, values --------------------------------------------------------------------------------------
       const bool value = E4M3 ? warp == 10 : warp >= 12;
       const int piece = E4M3 ? 0 : warp - (value ? 12 : 9);  // 64 columns of a slot's
-      uint64_t* full = E4M3 ? bars.stage_full + 2 * value : value ? bars.value_full : bars.key_full;
-      uint64_t* empty = E4M3 ? bars.stage_empty + 2 * value : value ? bars.value_empty : bars.key_empty;
-      // A turn is a slot, or 64 rows of one on their way through a stage.
-      constexpr int kRows = E4M3 ? S::kStageRows : kPrefixTile, kParts = kPrefixTile / kRows;
-      Ring ring(E4M3 ? S::kStages : value ? value_slots : key_slots), freed = ring;
-      const uint32_t base = E4M3 ? s0 + S::kOffStage + value * S::kStages * S::kStage : value ? at_v : at_k;
-      constexpr uint32_t kBytes = E4M3 ? S::kStage : S::kSlot;
+      uint64_t* full = E4M3 ? bars.codes_full + 6 * value : value ? bars.value_full : bars.key_full;
+      uint64_t* empty = value ? bars.value_empty : bars.key_empty;
+      Ring ring(value ? value_slots : key_slots), freed = ring;
+      // a slot, or its codes
+      const uint32_t base = E4M3 && !S::kInPlace ? s0 + S::kOffCodes + value * S::kKeySlots * S::kCodes
+                                                 : (value ? at_v : at_k) + (E4M3 ? S::kSlot / 2 : 0);
+      constexpr uint32_t kBytes = E4M3 && !S::kInPlace ? S::kCodes : S::kSlot;
       const CUtensorMap* map = value ? &p.values : &p.keys;
       const int box = of_warp(p.box);
       // Own keys are read once: the prefix keeps its place in L2 (64 requests behind 32768 positions 120.6 -> 118.2 us, 32 x 8 rows 95.5 ->
@@ -487,55 +497,53 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
         const long long item = w.item;
 #pragma unroll 1
         for (int h = 0; ok && h < S::kHalves; ++h) {
-#pragma unroll 1
-          for (int part = 0; ok && part < kParts; ++part, ++turn) {
-            if (turn >= ring.slots) {
-              ok = __all_sync(~0u, bar_wait(&empty[freed.bar], freed.phase, dead));
-              freed.next();
-            }
-            if (!ok) break;
-            const int row0 = part * kRows, end = min(len - key0, row0 + kRows);  // rows with keys
-            uint64_t* bar = tail ? &bars.tail[piece] : &full[ring.bar];
-            if (lane == 0) {
-              if (!E4M3 && !value && piece == 0) bars.since[j & 15] = static_cast<uint8_t>(since);
-              bar_expect(bar, max((end - row0 + box - 1) / box, 0) * box * 128);
-            }
-            __syncwarp();
-            const uint32_t to = base + ring.slot * kBytes + piece * (kPrefixTile * 128);
-#pragma unroll 1
-            for (int i = row0 / box & ~31; i * box < end; i += 32) {
-              if (held != i) held = i, page = pages_from(i);
-              const int row = (i + lane) * box, key = key0 + row;
-              if (row < row0 || row >= end) continue;
-              int id = page;
-              if (id < 0 || id >= a.n_pages) {
-                flag(a.status, MK_OP_BAD_PAGE);
-                id = a.n_pages;  // outside of the tensor: zeros
-              }
-              copy_box(to + (row - row0) * 128, map, h * S::kWide + piece * 64, key - p.page(key) * a.page_size, head, id, bar, policy);
-            }
-            __syncwarp();
-            if (tail) {
-              // Rows that are not there have to be zeros (0 times what they hold may be NaN), and so those that not every row sees,
-              // if they hold such values.
-              ok = __all_sync(~0u, bar_wait(bar, tails++ & 1, dead));
-              uint4* at = reinterpret_cast<uint4*>(smem + (to - s0));  // 8 a row
-              bool bad = false;
-#pragma unroll 1
-              for (int i = max(all_see - key0, 0) * 8 + lane; i < end * 8; i += 32) {
-                const uint4 x = at[i];
-                bad |= not_finite<T>(x.x) || not_finite<T>(x.y) || not_finite<T>(x.z) || not_finite<T>(x.w);
-              }
-              bad = __any_sync(~0u, bad);
-              if (lane == 0) bars.slow[j & 15][h * 2 + piece] = bad;
-#pragma unroll 1
-              for (int i = (bad ? max(all_see - key0, 0) : end) * 8 + lane; i < kPrefixTile * 8; i += 32) at[i] = make_uint4(0, 0, 0, 0);
-              proxy_fence();
-              __syncwarp();
-              if (lane == 0) bar_arrive(&full[ring.bar]);
-            }
-            ring.next();
+          if (turn >= ring.slots) {
+            ok = __all_sync(~0u, bar_wait(&empty[freed.bar], freed.phase, dead));
+            freed.next();
           }
+          if (!ok) break;
+          ++turn;
+          const int end = min(len - key0, kPrefixTile);  // rows with keys
+          uint64_t* bar = tail ? &bars.tail[piece] : &full[ring.bar];
+          if (lane == 0) {
+            if (!E4M3 && !value && piece == 0) bars.since[j & 15] = static_cast<uint8_t>(since);
+            bar_expect(bar, max((end + box - 1) / box, 0) * box * 128);
+          }
+          __syncwarp();
+          const uint32_t to = base + ring.slot * kBytes + piece * (kPrefixTile * 128);
+#pragma unroll 1
+          for (int i = 0; i * box < end; i += 32) {
+            if (held != i) held = i, page = pages_from(i);
+            const int row = (i + lane) * box, key = key0 + row;
+            if (row >= end) continue;
+            int id = page;
+            if (id < 0 || id >= a.n_pages) {
+              flag(a.status, MK_OP_BAD_PAGE);
+              id = a.n_pages;  // outside of the tensor: zeros
+            }
+            copy_box(to + row * 128, map, h * S::kWide + piece * 64, key - p.page(key) * a.page_size, head, id, bar, policy);
+          }
+          __syncwarp();
+          if (tail) {
+            // Rows that are not there have to be zeros (0 times what they hold may be NaN), and so those that not every row sees,
+            // if they hold such values.
+            ok = __all_sync(~0u, bar_wait(bar, tails++ & 1, dead));
+            uint4* at = reinterpret_cast<uint4*>(smem + (to - s0));  // 8 a row
+            bool bad = false;
+#pragma unroll 1
+            for (int i = max(all_see - key0, 0) * 8 + lane; i < end * 8; i += 32) {
+              const uint4 x = at[i];
+              bad |= not_finite<T>(x.x) || not_finite<T>(x.y) || not_finite<T>(x.z) || not_finite<T>(x.w);
+            }
+            bad = __any_sync(~0u, bad);
+            if (lane == 0) bars.slow[j & 15][h * 2 + piece] = bad;
+#pragma unroll 1
+            for (int i = (bad ? max(all_see - key0, 0) : end) * 8 + lane; i < kPrefixTile * 8; i += 32) at[i] = make_uint4(0, 0, 0, 0);
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&full[ring.bar]);
+          }
+          ring.next();
         }
         w.next();
         since = w.item != item ? 0 : min(since + 1, 2ll);
@@ -545,64 +553,72 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
       int alive = 0;
       for (uint32_t i = 0; i < min(turn, ring.slots); ++i, freed.next()) bar_wait(&full[freed.bar], freed.phase, &alive);
     } else if (E4M3 && warp >= 11 && warp < 15) {
-      // ---- converters: codes of a stage become a slot's fp16 values -------------------------------------------------------
+      // ---- converters: a tile's codes become its slot's fp16 values -------------------------------------------------------
       const bool value = warp >= 13;
       const int t = tid - (value ? 416 : 352);
-      Ring ring(value ? value_slots : key_slots), freed = ring;
-      uint64_t *full = value ? bars.value_full : bars.key_full, *empty = value ? bars.value_empty : bars.key_empty;
+      Ring ring(value ? value_slots : key_slots);
+      uint64_t* full = value ? bars.value_full : bars.key_full;
       PrefixWalk w = walk();
       long long since = 0;
-      uint32_t turn = 0;
-      Ring stage(S::kStages);
       bool ok = true;
-      constexpr int kSrc = S::kWide / 16, kStep = S::kConverters / kSrc;
-      const int chunk = t % kSrc, row0 = t / kSrc;
+      uint32_t tails = 0;
+      // Four lanes have a row: each 16 of its first 64 codes and, 128 wide, 16 of its second. In place a row's codes lie where its
+      // second 64 values go, so they are all read before any is written.
+      constexpr int kLanes = 4, kStep = S::kConverters / kLanes, kSets = S::kWide / 64;
+      const int chunk = t % kLanes, row0 = t / kLanes;
       for (long long j = 0; ok && j < count; ++j) {
         const int key0 = w.tile * kPrefixTile;
         const int all_see = w.all_see() - key0, end = w.len - key0;
 #pragma unroll 1
-        for (int h = 0; ok && h < S::kHalves; ++h, ++turn) {
-          if (turn >= ring.slots) {
-            ok = __all_sync(~0u, bar_wait(&empty[freed.bar], freed.phase, dead));
-            freed.next();
-          }
-          unsigned char* to = smem + ((value ? at_v : at_k) - s0) + ring.slot * S::kSlot + (chunk >> 2) * (kPrefixTile * 128);
-#pragma unroll 1
-          for (int part = 0; ok && part < kPrefixTile / S::kStageRows; ++part, stage.next()) {
-            ok = __all_sync(~0u, bar_wait(&bars.stage_full[2 * value + stage.bar], stage.phase, dead));
-            if (!ok) break;
-            const unsigned char* codes = smem + S::kOffStage + (value * S::kStages + stage.slot) * S::kStage;
-            const unsigned char* from = codes + row0 * 128 + chunk * 16;
-            int live = value ? end : kPrefixTile;  // rows from there on are zeros (see the loaders; each warp looks at all of them)
-            if (value && all_see < end && all_see < kPrefixTile) {
-              const int first = max(all_see, part * S::kStageRows), last = min(min(end, kPrefixTile), (part + 1) * S::kStageRows);
-              bool bad = false;
-              for (int i = first * 32 + lane; i < last * 32; i += 32) {  // four codes
-                const uint32_t x = *reinterpret_cast<const uint32_t*>(codes + (i - part * S::kStageRows * 32) * 4);
-#pragma unroll
-                for (int k = 0; k < 32; k += 8) bad |= (x >> k & 0x7f) == 0x7f && (i & 31) * 4 + k / 8 < a.head_dim - h * S::kWide;
-              }
-              bad = __any_sync(~0u, bad);
-              if (bad) live = all_see;
-              if (t == 0) bars.slow[j & 15][h * 2 + part] = bad;
-            }
-#pragma unroll 4
-            for (int i = 0; i < S::kStageRows / kStep; ++i) {
-              const int row = part * S::kStageRows + row0 + i * kStep;
-              uint4 x = *reinterpret_cast<const uint4*>(from + i * kStep * 128);
-              if (row >= live) x = make_uint4(0, 0, 0, 0);
-              const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {  // codes 16 chunk .. become pieces 2 chunk and 2 chunk + 1
-                uint32_t lo[2], hi[2];
-                e4m3_to_f16(lo, v[2 * k]);
-                e4m3_to_f16(hi, v[2 * k + 1]);
-                *reinterpret_cast<uint4*>(to + row * 128 + ((((2 * chunk + k) ^ row) & 7) << 4)) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
-              }
-            }
-            bar_arrive(&bars.stage_empty[2 * value + stage.bar]);
-          }
+        for (int h = 0; ok && h < S::kHalves; ++h) {
+          unsigned char* slot = smem + ((value ? at_v : at_k) - s0) + ring.slot * S::kSlot;
+          const unsigned char* codes = S::kInPlace ? slot + S::kSlot / 2
+                                                   : smem + S::kOffCodes + (value * S::kKeySlots + ring.slot) * S::kCodes;
+          ok = __all_sync(~0u, bar_wait(&bars.codes_full[6 * value + ring.bar], ring.phase, dead));
           if (!ok) break;
+          int live = value ? end : kPrefixTile;  // rows from there on are zeros (see the loaders; each warp looks at all of them)
+          if (value && all_see < end && all_see < kPrefixTile) {
+            const int first = max(all_see, 0), last = min(end, kPrefixTile);
+            bool bad = false;
+            for (int i = first * 32 + lane; i < last * 32; i += 32) {  // four codes
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(codes + i * 4);
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) bad |= (x >> k & 0x7f) == 0x7f && (i & 31) * 4 + k / 8 < a.head_dim - h * S::kWide;
+            }
+            bad = __any_sync(~0u, bad);
+            if (bad) live = all_see;
+            if (t == 0) bars.slow[j & 15][h * 2] = bars.slow[j & 15][h * 2 + 1] = bad;
+            // both warps have looked before either's rows change
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.tail[0]);
+            ok = __all_sync(~0u, bar_wait(&bars.tail[0], tails++ & 1, dead));
+            if (!ok) break;
+          }
+#pragma unroll 2
+          for (int i = 0; i < kPrefixTile / kStep; ++i) {
+            const int row = row0 + i * kStep;
+            uint4 x[kSets];
+            // (of odd rows the second 64 codes first: so 8 lanes have 32 banks)
+            const int turned = kSets == 2 ? row & 1 : 0;
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) {
+              x[k] = *reinterpret_cast<const uint4*>(codes + row * 128 + (k ^ turned) * 64 + chunk * 16);
+              if (row >= live) x[k] = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) {
+              const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              unsigned char* to = slot + (k ^ turned) * (kPrefixTile * 128) + row * 128;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                uint32_t lo[2], hi[2];
+                e4m3_to_f16(lo, v[2 * g]);
+                e4m3_to_f16(hi, v[2 * g + 1]);
+                *reinterpret_cast<uint4*>(to + (((2 * chunk + g) ^ row) & 7) * 16) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+              }
+            }
+          }
           if (!value && h == 0 && t == 0) bars.since[j & 15] = static_cast<uint8_t>(since);
           proxy_fence();
           bar_arrive(&full[ring.bar]);
@@ -1020,8 +1036,7 @@ cudaError_t launch_prefix(const PrefixParams& p, int device, cudaStream_t s) {
   PrefixParams q = p;
   const mk_prefix_attention_args& a = p.a;
   q.box = a.page_size & -a.page_size;
-  const int most = E4M3 ? S::kStageRows : kPrefixTile;
-  if (q.box > most) q.box = most;
+  if (q.box > kPrefixTile) q.box = kPrefixTile;
   const int64_t *ks = a.k_page_stride, *vs = a.v_page_stride;
   cudaError_t e = map_cache(&q.keys, a.k_pages, a, ks, q.box, E4M3);
   if (e == cudaSuccess) e = map_cache(&q.values, a.v_pages, a, vs, q.box, E4M3);
