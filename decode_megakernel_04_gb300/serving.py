@@ -12,6 +12,7 @@ element that collects the OP_* flags of what only the device can see.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import struct
 
 import torch
@@ -280,16 +281,20 @@ def _pack_prefix_args(q, k_pages, v_pages, prefix_table, prefix_len, table, lens
     return head[:3] + prefix + head[3:], tail[:-3] + (pages,) + tail[-3:]
 
 
+@functools.lru_cache(maxsize=1024)
+def _prefix_size(what, dev, *shape) -> int:
+    """The workspace of a call whose shape fields are these (they alone decide)."""
+    return _workspace_size(load().mk_prefix_attention_workspace, _pack_prefix(*(0,) * 27, *shape, 1.0), dev, what)
+
+
 def prefix_attention_workspace(q, k_pages, prefix_table, table) -> int:
     """Bytes of device scratch prefix_attention needs for q, k_pages and tables of these shapes and types."""
     dev = q.get_device()
     _need(dev >= 0, "prefix_attention needs CUDA tensors")
     lens = torch.empty(q.shape[0], dtype=_I32, device=q.device)
     scale = torch.empty(k_pages.shape[1], dtype=_F32, device=q.device)
-    head, tail = _pack_prefix_args(q, k_pages, k_pages, prefix_table, prefix_table[:1], table, lens, q, None, None, scale,
-                                   scale, dev)
-    return _workspace_size(load().mk_prefix_attention_workspace, _pack_prefix(*head, 0, 0, 0, *tail), dev,
-                           "prefix_attention_workspace")
+    _, tail = _pack_prefix_args(q, k_pages, k_pages, prefix_table, prefix_table[:1], table, lens, q, None, None, scale, scale, dev)
+    return _prefix_size("prefix_attention_workspace", dev, *tail[13:-1])
 
 
 def prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, table, lens, out, *, scale: float | None = None,
@@ -308,11 +313,12 @@ def prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, table, lens,
                                    v_scale, dev)
     st = _vector(status, _I32, 1, dev, "status")
     if workspace is None:
-        size = _workspace_size(load().mk_prefix_attention_workspace, _pack_prefix(*head, 0, st, 0, *tail), dev,
-                               "prefix_attention")
+        size = _prefix_size("prefix_attention", dev, *tail[13:-1])
         workspace = _workspace(size, q.device, dev, stream)
-    packed = _pack_prefix(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), st, workspace.numel(), *tail)
-    _call(load().mk_prefix_attention, packed, dev, stream, "prefix_attention")
+        at = workspace.data_ptr()
+    else:
+        at, size = _vector(workspace, torch.uint8, None, dev, "workspace"), workspace.numel()
+    _call(load().mk_prefix_attention, _pack_prefix(*head, at, st, size, *tail), dev, stream, "prefix_attention")
 
 
 def logit_controls(logits, out, *, history=None, prompt_len=None, total_len=None, repetition=None, presence=None,
@@ -391,12 +397,17 @@ def _pack_drafts_args(logits, tokens, noise, uniforms, accept_out, draft_logits,
             (ls, ys, ns, b, rows, vocab, _DTYPE[dt]))
 
 
+@functools.lru_cache(maxsize=1024)
+def _drafts_size(what, dev, *shape) -> int:
+    """The workspace of a call whose shape fields are these (they alone decide)."""
+    return _workspace_size(load().mk_verify_drafts_workspace, _pack_drafts(*(0,) * 16, *shape), dev, what)
+
+
 def verify_drafts_workspace(logits, tokens) -> int:
     """Bytes of device scratch verify_drafts needs for logits [batch * rows, vocab] and tokens [batch, rows]."""
     dev = logits.get_device()
     _need(dev >= 0 and logits.dim() == 2 and tokens.dim() == 2 and logits.dtype in _DTYPE, "verify_drafts needs CUDA tensors")
-    packed = _pack_drafts(*(0,) * 10, 0, 0, 0, 0, 0, 0, *tokens.shape, logits.shape[1], _DTYPE[logits.dtype])
-    return _workspace_size(load().mk_verify_drafts_workspace, packed, dev, "verify_drafts_workspace")
+    return _drafts_size("verify_drafts_workspace", dev, *tokens.shape, logits.shape[1], _DTYPE[logits.dtype])
 
 
 def verify_drafts(logits, tokens, noise, uniforms, accept_out, *, draft_logits=None, n_drafts=None, temperature=None,
@@ -424,10 +435,12 @@ def prepare_verify_drafts(logits, tokens, noise=None, uniforms=None, accept_out=
                                    logprobs, dev)
     st = _vector(status, _I32, 1, dev, "status")
     if workspace is None:
-        size = _workspace_size(load().mk_verify_drafts_workspace, _pack_drafts(*head, 0, st, 0, *tail), dev, "verify_drafts")
+        size = _drafts_size("verify_drafts", dev, *tail[3:])
         workspace = _workspace(size, logits.device, dev, stream)
-    packed = _pack_drafts(*head, _vector(workspace, torch.uint8, None, dev, "workspace"), st, workspace.numel(), *tail)
-    return (load().mk_verify_drafts, packed, dev, stream, "verify_drafts"), workspace
+        at = workspace.data_ptr()
+    else:
+        at, size = _vector(workspace, torch.uint8, None, dev, "workspace"), workspace.numel()
+    return (load().mk_verify_drafts, _pack_drafts(*head, at, st, size, *tail), dev, stream, "verify_drafts"), workspace
 
 
 def check_verify_drafts(call) -> None:
