@@ -8,8 +8,8 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-// W warps for each row of out: its parts over the prefix and over its own keys, weighted by exp2(base - largest base). Launched
-// so that it may start while the first kernel runs, whose end it waits for.
+// W warps for each row of out: its parts over the prefix and over its own keys, weighted by exp2(base - largest base). (Launched
+// early, to wait for the first kernel's end by itself, it cost that kernel a microsecond: 13.5 us instead of 12.3 for a short call.)
 template <typename T, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ PrefixParams p) {
   __shared__ float4 part_sums[kJoinWarps][32];
@@ -18,7 +18,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const int row = blockIdx.x * (kJoinWarps / W) + warp / W;
   const int br = p.q_head_div(row), h = row - br * a.n_q_heads, head = p.group_div(h), m = br * p.group + h - head * p.group;
   const int b = p.row_div(br), r = br - b * a.rows;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (br >= a.batch * a.rows) return;  // (W = 8: the whole CTA)
   const Head& hd = *p.head;
   // Parts 0 .. n0 - 1 are over the prefix, n0 .. n - 1 over own keys. Part k of either is place0 + k / subs, stream k % subs (of a
@@ -181,17 +180,8 @@ mk_status plan(const mk_prefix_attention_args& a, int device, Plan* out) {
 
 template <typename T, int W>
 cudaError_t join(const PrefixParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
   const long long rows = static_cast<long long>(p.n_rows) * p.a.n_kv_heads;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows * W + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, W>, p);
+  return start(join_kernel<T, W>, static_cast<unsigned>((rows * W + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, s, p);
 }
 template <typename T>
 cudaError_t join(const PrefixParams& p, cudaStream_t s) {

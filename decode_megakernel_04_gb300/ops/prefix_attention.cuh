@@ -313,7 +313,6 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
   } ends;
 
   // ---- the lines, and this CTA's piece of one -------------------------------------------------------------------------
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Head hd;
   int line, c = blockIdx.x;
   long long begin;
