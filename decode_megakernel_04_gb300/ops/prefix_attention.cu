@@ -244,6 +244,10 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   const mk_prefix_attention_args& a = p.a;
   if (mk_status s = check_shape(a, device)) return s;
   if (mk_status s = attn::check(kMe, own_call(a), device)) return s;
+  const int counts[3] = {a.n_pages, a.n_kv_heads, a.page_size};
+  for (int i = 0; i < 3; ++i)
+    if (counts[i] > 1 && (a.k_page_stride[i] == 0 || a.v_page_stride[i] == 0))  // (not as a copied box's tensor)
+      return refuse(MK_ERR_UNSUPPORTED, kMe, "a cache stride of 0");
   if (static_cast<int64_t>(a.max_prefix_pages) * a.page_size > INT32_MAX - 1024)
     return refuse(MK_ERR_UNSUPPORTED, kMe, "positions beyond 2^31 - 1024");
   if (a.batch == 0) return MK_OK;

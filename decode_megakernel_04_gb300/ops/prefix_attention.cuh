@@ -240,13 +240,6 @@ __device__ inline void tc_ld64(float (&v)[128], int at, uint32_t addr) {
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[at + i] = __uint_as_float(r[i]);
 }
-// One column.
-__device__ inline void tc_ld1(float& v, uint32_t addr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n"
-               "tcgen05.wait::ld.sync.aligned;" : "=&r"(r) : "r"(addr) : "memory");
-  v = __uint_as_float(r);
-}
 // 16 consecutive columns of this warp's lanes from packed values (tcgen05.wait::st follows separately)
 __device__ inline void tc_st_packed(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),

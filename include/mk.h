@@ -564,7 +564,7 @@ mk_status mk_paged_attention_workspace(const mk_paged_attention_args* args, int 
  * The result does not depend on timing. `workspace`: mk_prefix_attention_workspace bytes of device scratch, 16-byte aligned, any
  * contents; calls that may overlap need one each. Two launches.
  * Errors: as mk_paged_attention; batch * rows * n_q_heads / n_kv_heads beyond 2^24, batch * rows * n_q_heads beyond 2^31 - 64, tables that
- * reach beyond position 2^31 - 1024. */
+ * reach beyond position 2^31 - 1024, a cache stride of 0 in a dimension of more than one element. */
 typedef struct mk_prefix_attention_args {
   const void* q;               /* device [batch][rows][n_q_heads][head_dim], dtype                  */
   const void* k_pages;         /* device, cache_dtype                                             */

@@ -90,6 +90,17 @@ def test_refusals(lib, name, make, code, change):
     assert getattr(lib, name)(C.byref(make(**change)), 0, None) == code
 
 
+@pytest.mark.parametrize("field", ["k_page_stride", "v_page_stride"])
+@pytest.mark.parametrize("strides", [(0, 2048, 128), (4096, 0, 128), (4096, 2048, 0)])
+def test_caches_expanded_over_a_dimension(lib, field, strides):
+    """Refused by mk_prefix_attention, except where the dimension has one element."""
+    counts = dict(n_pages=32, n_kv_heads=2, page_size=16)
+    assert lib.mk_prefix_attention(C.byref(prefix(**{field: strides})), 0, None) == UNSUPPORTED
+    one = [k for k, x in zip(counts, strides) if x == 0][0]
+    shape = {one: 1, **({"n_q_heads": 1} if one == "n_kv_heads" else {})}
+    assert lib.mk_prefix_attention(C.byref(prefix(**{field: strides}, **shape, batch=0)), 0, None) == 0
+
+
 @pytest.mark.parametrize("name, make", [("mk_rms_norm", norm), ("mk_prefix_attention", prefix), ("mk_verify_drafts", drafts)])
 def test_null_arguments_and_devices(lib, name, make):
     fn = getattr(lib, name)
