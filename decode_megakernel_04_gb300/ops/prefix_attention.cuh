@@ -220,13 +220,14 @@ __device__ inline void copy_box(uint32_t to, const CUtensorMap* map, int column,
   asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], "
                "[%6], %7;" ::"r"(to), "l"(map), "r"(column), "r"(place), "r"(head), "r"(page), "r"(smem_u32(bar)), "l"(policy) : "memory");
 }
-// 64 consecutive fp32 columns of this warp's 32 lanes into v[at ..]. Load and wait are one statement: before the wait the
-// registers do not hold the values.
-__device__ inline void tc_ld64(float (&v)[128], int at, uint32_t addr) {
+// 64 consecutive fp32 columns of this warp's 32 lanes into v[at ..], and a lane's largest. Load and wait are one statement: before
+// the wait the registers do not hold the values.
+__device__ inline float tc_ld64_max(float (&v)[128], int at, uint32_t addr) {
   uint32_t r[64];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+  float largest;
+  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
                "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,"
-               "%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+               "%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, %64, [%65];\n"
                "tcgen05.wait::ld.sync.aligned;"
                : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
                  "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
@@ -235,10 +236,12 @@ __device__ inline void tc_ld64(float (&v)[128], int at, uint32_t addr) {
                  "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]),
                  "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47]),
                  "=&r"(r[48]), "=&r"(r[49]), "=&r"(r[50]), "=&r"(r[51]), "=&r"(r[52]), "=&r"(r[53]), "=&r"(r[54]), "=&r"(r[55]),
-                 "=&r"(r[56]), "=&r"(r[57]), "=&r"(r[58]), "=&r"(r[59]), "=&r"(r[60]), "=&r"(r[61]), "=&r"(r[62]), "=&r"(r[63])
+                 "=&r"(r[56]), "=&r"(r[57]), "=&r"(r[58]), "=&r"(r[59]), "=&r"(r[60]), "=&r"(r[61]), "=&r"(r[62]), "=&r"(r[63]),
+                 "=&f"(largest)
                : "r"(addr) : "memory");
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[at + i] = __uint_as_float(r[i]);
+  return largest;
 }
 // 16 consecutive columns of this warp's lanes from packed values (tcgen05.wait::st follows separately)
 __device__ inline void tc_st_packed(uint32_t addr, const uint32_t (&r)[16]) {
@@ -880,25 +883,29 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
           tc_after();
           const uint32_t at = tmem + lanes + static_cast<uint32_t>(u & 1) * 128;
           float s[128];
-          tc_ld64(s, 0, at);
-          tc_ld64(s, 64, at + 64);
-          if (!E4M3 && p.flip)  // a negative scale
+          float largest = tc_ld64_max(s, 0, at);
+          largest = fmaxf(largest, tc_ld64_max(s, 64, at + 64));
+          const bool hidden = key0 + kPrefixTile > all_see, flip = !E4M3 && p.flip;  // (flip: a negative scale)
+          if (hidden || flip) {
+            if (flip)
 #pragma unroll
-            for (int x = 0; x < 128; ++x) s[x] = -s[x];
-          if (key0 + kPrefixTile > all_see) {
-            const int valid = limit - key0;
+              for (int x = 0; x < 128; ++x) s[x] = -s[x];
+            if (hidden) {
+              const int valid = limit - key0;
 #pragma unroll
-            for (int x = 0; x < 128; ++x)
-              if (x >= valid) s[x] = -INFINITY;
+              for (int x = 0; x < 128; ++x)
+                if (x >= valid) s[x] = -INFINITY;
+            }
+            float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int x = 4; x < 124; x += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) tops[k] = max3(tops[k], s[x + k], s[x + 4 + k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], s[124 + k]);
+            largest = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
           }
-          float tops[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int x = 4; x < 124; x += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tops[k] = max3(tops[k], s[x + k], s[x + 4 + k]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], s[124 + k]);
-          const float top = fmaxf(__fadd_ru(fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * cs, -kPrefixLift<T>), kNoBase);
+          const float top = fmaxf(__fadd_ru(largest * cs, -kPrefixLift<T>), kNoBase);
           const bool grew = first || top > base + kPrefixGrow<T>;
           if (__any_sync(~0u, grew)) {
             // the base moves: what there is so far follows it
