@@ -8,7 +8,7 @@
 //   pairs of row tiles over the prefix (a tile of keys and values is read once for 256 rows), single row tiles over the prefix
 //   (an odd one; all of them 256 wide, where the tensor memory holds one), and row tiles of one request (of up to 8 of its
 //   new rows) over its own keys. CTAs are dealt to the lines by what their tiles take, a rule on the lengths alone; an item over
-//   own keys counts as two tiles more (with CTAs dealt and cut by tiles alone, 64 requests behind 32768 positions took 128 us
+//   own keys counts as four tiles more (with CTAs dealt and cut by tiles alone, 64 requests behind 32768 positions took 128 us
 //   instead of 117: those with many short requests ended last).
 //   Where a CTA has one row tile, even and odd key tiles go to two sets of sums, so that there are two streams of work
 //   in any case (one 256 wide).
@@ -29,10 +29,10 @@
 // Probabilities are one 16-bit number (a pair hi + lo would be half as much work again for the tensor cores). bf16: 2^-8 of each
 // at most; fp16: 2^-11, against a base 14 under the maximum, so that what falls under its range is 2^-39 of the largest. Sums of
 // probabilities are those of the unrounded ones.
-// Measured: 64 requests behind 32768 positions with own ones of up to 2000 (48/8 heads of 128, bf16) 118 us, 32 x 8 rows behind
-// 8191 93 us (590 TFLOP/s), 64 requests behind 65536 in e4m3 154 us (670 TFLOP/s), 4 samples of 4096 positions 256 wide 25 us. What bounds
-// it is the chain of products, scores out of tensor memory, softmax and probabilities back: a pair's tile takes about 3700 cycles,
-// 3300 with almost all products left out and 3500 without exponentials, and two streams are all that tensor memory holds.
+// Measured: 64 requests behind 32768 positions with own ones of up to 2000 (48/8 heads of 128, bf16) 114 us, 32 x 8 rows behind
+// 8191 92 us (600 TFLOP/s), 64 requests behind 65536 in e4m3 155 us (670 TFLOP/s), 4 samples of 4096 positions 256 wide 25 us. What bounds
+// it is the chain of products, scores out of tensor memory, softmax and probabilities back: a pair's tile takes about 3500 cycles,
+// 400 less with almost all products left out and 200 less without exponentials, and two streams are all that tensor memory holds.
 // Every wait has a limit (2 s), after which the CTA gives up, drains and frees what it holds and MK_OP_TIMEOUT is set.
 #pragma once
 #include <cuda.h>
@@ -53,13 +53,14 @@ __device__ inline long long scaled(long long a, long long b, long long c) {
 constexpr int kPrefixTile = 128;      // keys
 constexpr int kTileRows = 128;        // query rows of a row tile
 constexpr int kGroupRows = 8;         // new rows of a request that share an item over its own keys
-constexpr int kItemTiles = 2;         // what an item over own keys takes besides its tiles, in tiles
+constexpr int kItemTiles = 4;         // what an item over own keys takes besides its tiles, in tiles
 enum { kPairs, kSingles, kOwn };      // the lines
-// What a tile of a line takes of a CTA, in parts of 12 of a pair's: as measured 128 wide, where a pair's tile takes 1.85 to 2.1 us, a single
-// one 1.3 to 1.4, one of an item (with its share of the two for the item) 1.35 to 1.6. With 12 / 12 / 12 instead, 64 requests behind
-// 32768 positions take 136 us and not 118, in e4m3 behind 65536 179 and not 154, 32 x 8 rows 95 and not 93.
+// What a tile of a line takes of a CTA, in parts of 24 of a pair's: as measured 128 wide, where a pair's tile takes 1.8 to 2.1 us, a single
+// one 1.3 to 1.4, one of an item (with its share of the four for the item) 1.0 to 1.2. 64 requests behind 32768 positions and 32 x 8 rows
+// behind 8191 take 113 and 91 us; with 24 / 18 / 18 122 and 90, with two tiles an item and 24 / 18 / 18 116 and 95, with 24 / 24 / 24 136
+// and 95; e4m3 behind 65536 155, with 24 / 16 / 20 161.
 template <bool E4M3>
-constexpr int kLineCost[3] = {12, E4M3 ? 8 : 9, E4M3 ? 10 : 9};
+constexpr int kLineCost[3] = {24, E4M3 ? 17 : 18, E4M3 ? 16 : 14};
 
 // What the first CTA writes for the join. Piece c's part of item i of a line goes to place c + i (after `place0`): along the line
 // either grows by one from part to part.
@@ -356,10 +357,7 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
     if (!cost[2]) (cost[1] ? n1 : n0) += most - n0 - n1;
     const int got[3] = {n0, n1, ctas - n0 - n1};
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {  // (a piece has a tile)
-      const long long worth = i == kOwn ? hd.total[i] / (kItemTiles + 1) : hd.total[i];
-      hd.used[i] = static_cast<int>(worth < got[i] ? worth : got[i]);
-    }
+    for (int i = 0; i < 3; ++i) hd.used[i] = static_cast<int>(hd.total[i] < got[i] ? hd.total[i] : got[i]);
     line = c < n0 ? kPairs : c < n0 + n1 ? kSingles : kOwn;
     c -= line == kPairs ? 0 : line == kSingles ? n0 : n0 + n1;
     begin = hd.used[line] ? scaled(c, hd.total[line], hd.used[line]) : 0;  // (as piece_of() has it)
@@ -400,6 +398,11 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
       }
     }
   }
+  if (c >= hd.used[line]) return;
+  if (line == kOwn) {
+    __syncthreads();
+    if (ends.tiles[0] == ends.tiles[1]) return;  // (a piece of nothing but what an item takes besides its tiles)
+  }
   if (tid == 0) {
     for (int i = 0; i < 6; ++i) {
       bar_init(&bars.key_full[i], E4M3 ? S::kConverters : S::kPieces), bar_init(&bars.key_empty[i], line == kPairs ? 2 : 1);
@@ -416,7 +419,6 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
     for (auto& x : bars.slow) *reinterpret_cast<uint32_t*>(x) = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (c >= hd.used[line]) return;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
