@@ -138,15 +138,15 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const __grid_constant__
   };
   if (i0 + tid < v0) one(i0 + tid);
   const uint4* from = reinterpret_cast<const uint4*>(z + v0);
-  int k = tid;
-  for (; k + (kVectors - 1) * kThreads < nv; k += kVectors * kThreads) {
+  for (int k = tid; k < nv; k += kVectors * kThreads) {
     uint4 u[kVectors];
 #pragma unroll
-    for (int x = 0; x < kVectors; ++x) u[x] = from[k + x * kThreads];
+    for (int x = 0; x < kVectors; ++x)
+      if (k + x * kThreads < nv) u[x] = from[k + x * kThreads];
 #pragma unroll
-    for (int x = 0; x < kVectors; ++x) s.add(logits_of<T>(u[x]).v, v0 + (k + x * kThreads) * kPer, c);
+    for (int x = 0; x < kVectors; ++x)
+      if (k + x * kThreads < nv) s.add(logits_of<T>(u[x]).v, v0 + (k + x * kThreads) * kPer, c);
   }
-  for (; k < nv; k += kThreads) s.add(logits_of<T>(from[k]).v, v0 + k * kPer, c);
   if (v0 + nv * kPer + tid < i1) one(v0 + nv * kPer + tid);
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
