@@ -518,10 +518,10 @@ def run_prefix(s, scale=None, **kw):
     return out[..., :d], lse
 
 
-def check_prefix(s, got, lse, scale, what="", weak=False):
-    """check_attention's bounds (test_gpu_serving_ops.py), with a probability over the prefix rounded once to 16 bits: bf16 half
-    a step 2^-8, fp16 and e4m3 2^-11; fp16 ones against a largest of 2^14, so off by another 2^-25 / 2^14 = 2^-39 of
-    the largest where they are subnormal. Own keys of e4m3 caches: 2^-25 absolute there (weak: 2^-39)."""
+def check_prefix(s, got, lse, scale, what=""):
+    """check_attention's bounds (test_gpu_serving_ops.py), with a probability rounded once to 16 bits: bf16 half a step 2^-8, fp16
+    and e4m3 2^-11; fp16 ones against a largest of 2^14, so off by another 2^-25 / 2^14 = 2^-39 of the largest where they are
+    subnormal."""
     d = s["q"].shape[-1]
     out, l64, av, qk = prefix_reference(s, scale)
     n = (s["lens"].clamp(min=0) + s["prefix_len"].clamp(min=0)).double()[:, None, None]
@@ -530,7 +530,7 @@ def check_prefix(s, got, lse, scale, what="", weak=False):
     rel = 2 * (ds + 2.0 ** -21 + n * 2.0 ** -23) + (2.0 ** -11 if e4 or s["q"].dtype is F16 else 2.0 ** -8)
     v_max = s["v"].float().nan_to_num().abs().amax((0, 2, 3))
     v_max = (v_max if s["vs"] is None else v_max * s["vs"]).max().double()
-    slack = rel[..., None] * av + (n * (2.0 ** -25 if e4 and not weak else 2.0 ** -39))[..., None] * v_max
+    slack = rel[..., None] * av + (n * 2.0 ** -39)[..., None] * v_max
     assert not got.isnan().any(), what
     empty = l64 == -math.inf
     assert (got[empty] == 0).all() and (lse[empty] == -math.inf).all(), what
@@ -610,7 +610,7 @@ def test_prefix_scores_that_grow_and_that_begin_at_minus_infinity(dtype, cache, 
         k0[..., 0] = grow * scale_up
         s["k"][pages] = k0.to(cache)
         got, lse = run_prefix(s, scale=0.25)
-        check_prefix(s, got, lse, 0.25, "growing", weak=cache is not E4M3)
+        check_prefix(s, got, lse, 0.25, "growing")
     if cache is E4M3:
         return
     k0 = s["k"][pages].float()
@@ -641,7 +641,7 @@ def test_prefix_many_weak_keys_behind_a_strong_one(dtype, cache, d, first):
     s["k"][at, :, 3, 0] = (14.0 + torch.arange(8, device=DEV) % 5).to(cache)
     s["v"][at, :, 3] = 0.0
     got, lse = run_prefix(s, scale=0.25)
-    check_prefix(s, got, lse, 0.25, weak=True)
+    check_prefix(s, got, lse, 0.25)
 
 
 def test_prefix_scores_of_any_size():
