@@ -1029,10 +1029,13 @@ cudaError_t launch_prefix(const PrefixParams& p, int device, cudaStream_t s) {
   using S = PrefixShape<D, E4M3>;
   if (const cudaError_t e = allow_smem<kernel>(device, S::kSmem)) return e;
   // setmaxnreg hands out what the block was launched with; a build with less would wait for ever
-  static const int regs = [] {
+  static std::atomic<int> known{0};
+  int regs = known.load(std::memory_order_relaxed);
+  if (!regs) {
     cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
+    if (const cudaError_t e = cudaFuncGetAttributes(&f, kernel)) return e;
+    known.store(regs = f.numRegs, std::memory_order_relaxed);
+  }
   if (regs * S::kThreads < 256 * S::kSoftmaxRegs + (S::kThreads - 256) * S::kOtherRegs) return cudaErrorInvalidConfiguration;
   PrefixParams q = p;
   const mk_prefix_attention_args& a = p.a;
