@@ -174,7 +174,8 @@ mk_status plan(const mk_prefix_attention_args& a, int device, Plan* out) {
   pl.own_ml_at = pl.own_at + whole(own_rows * pl.dp * sizeof(float));
   pl.head_at = pl.own_ml_at + whole(own_rows * sizeof(float2));
   pl.cum_at = pl.head_at + whole(sizeof(Head));
-  pl.bytes = pl.cum_at + whole((groups + 1) * sizeof(long long));
+  // the first kernel stores sums by 32 bytes: places begin at the workspace's first 32-byte boundary
+  pl.bytes = pl.cum_at + whole((groups + 1) * sizeof(long long)) + 16;
   return MK_OK;
 }
 
@@ -261,7 +262,7 @@ extern "C" mk_status mk_prefix_attention(const mk_prefix_attention_args* args, i
   if (!a.workspace || a.workspace_bytes < 0 || static_cast<uint64_t>(a.workspace_bytes) < pl.bytes)
     return refuse(MK_ERR_INVALID_ARG, kMe, "workspace of %lld bytes, %llu needed", static_cast<long long>(a.workspace_bytes),
                   static_cast<unsigned long long>(pl.bytes));
-  char* ws = static_cast<char*>(a.workspace);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(a.workspace) + 31) & ~uintptr_t{31});
   p.page = div_by(a.page_size);
   p.group_div = div_by(pl.group);
   p.group = pl.group;

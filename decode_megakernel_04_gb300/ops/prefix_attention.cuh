@@ -89,7 +89,7 @@ struct PrefixParams {
   float scale_log2;   // |scale| * log2(e)
   uint32_t flip;      // sign bits of two 16-bit values where the scale is negative: queries change their sign instead
   uint32_t k_step[3], v_step[3];  // the caches' strides (page, head, place) in units of 16 bytes
-  float* part;        // [places][streams][128][dp] sums of a part over the prefix
+  float* part;        // [places][streams][128][dp] sums of a part over the prefix (on 32 bytes, as `own`)
   float2* part_ml;    // [places][streams][128] its base (log2 units) and sum of probabilities; sum 0: an empty part, sums not written
   float* own;         // [places][streams][own_rows][dp] and
   float2* own_ml;     // [places][streams][own_rows] over own keys

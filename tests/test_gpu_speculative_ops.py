@@ -769,6 +769,23 @@ def test_prefix_workspace_of_the_largest_call_fits_all():
                          workspace=ws[:prefix_attention_workspace(s["q"], s["k"], s["prefix_table"], s["table"]) - 16])
 
 
+@pytest.mark.parametrize("at", [16, 32, 48, 240])
+@pytest.mark.parametrize("case", [(700, 1, BF16, BF16, 128), (300, 2, F16, F16, 64), (900, 1, BF16, BF16, 256), (500, 1, BF16, E4M3, 128)], ids=str)
+def test_prefix_workspace_that_begins_between_32_byte_boundaries(case, at):
+    """A part of a larger buffer, on 16 bytes as documented: the result is that of any other workspace, and nothing is written
+    outside of it."""
+    from decode_megakernel_04_gb300 import prefix_attention_workspace
+    prefix, R, dtype, cache, d = case
+    s = prefix_inputs(prefix, [40, 3, 0, 150], R, 12, 2, d, 16, dtype, cache, seed=at)
+    size = prefix_attention_workspace(s["q"], s["k"], s["prefix_table"], s["table"])
+    ws = torch.full((size + 512,), 255, dtype=torch.uint8, device=DEV)
+    got, lse = run_prefix(s, workspace=ws[at:at + size])
+    check_prefix(s, got, lse, d ** -0.5)
+    want, lse2 = run_prefix(s)
+    assert torch.equal(got, want) and torch.equal(lse, lse2)
+    assert (ws[:at] == 255).all() and (ws[at + size:] == 255).all()
+
+
 # ---- streams, graphs, threads, steps ------------------------------------------------------------------------------------
 
 def operator_calls(seed=0):
