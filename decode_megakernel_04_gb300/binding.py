@@ -362,11 +362,13 @@ class Megakernel:
         the same stream; R = 1 samples a token."""
         B, R = tokens.shape
         if sampling is not None:
+            import torch
             from .serving import _call, check_verify_drafts, prepare_verify_drafts
             z = None if logits is None else logits.view(-1, self.cfg.vocab)
-            # (the step writes its rows one after the other)
-            if z is None or z.shape[0] != B * R or z.get_device() != self.device or not z.is_contiguous():
-                raise ValueError("sampling needs contiguous logits [batch * rows, vocab] on the handle's device")
+            # (the step writes fp32 rows, one after the other)
+            if (z is None or z.dtype is not torch.float32 or z.shape[0] != B * R or z.get_device() != self.device
+                    or not z.is_contiguous()):
+                raise ValueError("sampling needs contiguous fp32 logits [batch * rows, vocab] on the handle's device")
             # what does not fit is refused before the step, which cannot be taken back
             call, workspace = prepare_verify_drafts(z, tokens, accept_out=accept_out, positions=positions, stream=stream or 0,
                                                     **sampling)

@@ -986,6 +986,15 @@ def test_sampling_that_the_library_refuses_is_refused_before_the_step():
         m.verify(tok, i32([0, 0]), accept, torch.zeros(4, vocab + 1, device=DEV)[:, :vocab], sampling=dict(noise=noise, uniforms=u))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_sampling_of_16_bit_logits_is_refused_before_the_step(dtype):
+    """The step writes fp32 rows; verify_drafts alone takes these."""
+    m, vocab = stepless()[0], 8
+    tok, z, accept = i32([[1, 2], [3, 4]]), torch.zeros(4, vocab, dtype=dtype, device=DEV), i32([[0, 0]] * 3)
+    with pytest.raises(ValueError):
+        m.verify(tok, i32([0, 0]), accept, z, sampling=dict(noise=torch.ones(2, vocab, device=DEV), uniforms=torch.zeros(2, 1, device=DEV)))
+
+
 def test_wrappers_refuse():
     import decode_megakernel_04_gb300 as mk
     x = torch.zeros(4, 256, dtype=BF16, device=DEV)

@@ -194,6 +194,23 @@ def test_sampling_that_does_not_fit_is_refused_before_the_step():
             m.verify(tok, tok[:, 0], accept, z, sampling=dict(noise=torch.ones(2, 8)))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float64, torch.int32])
+def test_sampling_of_logits_that_are_not_fp32_is_refused_before_the_step(monkeypatch, dtype):
+    """The step writes fp32 rows, so a buffer of another type is not one for it, whatever the operator takes."""
+    class Lib:
+        def mk_decode_step(self, *args):
+            raise AssertionError("the step ran")
+
+    monkeypatch.setattr(serving, "prepare_verify_drafts", lambda *args, **kw: ((), None))
+    monkeypatch.setattr(serving, "check_verify_drafts", lambda call: None)
+    m = binding.Megakernel.__new__(binding.Megakernel)
+    m.lib, m.device, m.h = Lib(), -1, None
+    m.cfg = type("Cfg", (), {"vocab": 8})
+    tok = torch.zeros(2, 2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        m.verify(tok, tok[:, 0], torch.zeros(3, 2, dtype=torch.int32), torch.zeros(4, 8, dtype=dtype), sampling={})
+
+
 def test_wrappers_refuse_cpu_tensors():
     i = torch.zeros(2, dtype=torch.int32)
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
