@@ -293,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, 6) draw_kernel(const __grid_constant
           const int j = i + k * kThreads;
           // (rounded products, so that equal probabilities leave 0 and not what a fused difference would)
           float p = __fmul_rn(exp2_fast((logit(as_float(p_in[k])) - ch.top) * c), by);
-          if (less) p -= __fmul_rn(exp2_fast((logit(as_float(q_in[k])) - ch.draft_top) * c), draft_by);
+          if (less) p = fmaxf(p - __fmul_rn(exp2_fast((logit(as_float(q_in[k])) - ch.draft_top) * c), draft_by), 0.0f);
           if (!kWhole && (j >= to || j == left_out)) p = 0.0f;
-          const float s = __fdividef(p, e[k]);
+          const float s = __fdividef(p, e[k] + 0.0f);  // (-0 + 0 is 0)
           if (s > score) score = s, at = j;
         }
       };

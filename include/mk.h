@@ -684,7 +684,7 @@ mk_status mk_rms_norm(const mk_rms_norm_args* args, int device, void* stream);
  * logprobs[b][r] = log p_r of the token that follows row r: the drafts r < a, the bonus token at a (-infinity for token -1), 0
  * behind it.
  * Temperatures above 0 count as within 2^-100 .. 2^100. Logits that are NaN count as -infinity; where a row has some of +infinity, these share it. Noise below 0 or NaN: the token is
- * not drawn; 0: it comes before all others. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
+ * not drawn; 0 (or -0): it comes before all others that have a weight. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
  * as within 0 .. rows - 1 (MK_OP_BAD_LENGTH).
  * Weights, sums and log-probabilities are fp32: where uniforms * q and p, or the two largest quotients, are within 2^-17 of each other
  * (for probabilities of e^-x: x / 2^22 more), either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.

@@ -401,6 +401,37 @@ def test_verify_drafts_refused_where_draft_and_target_agree():
     assert (accept[0] == 1).all() and (accept[1] >= 0).all()
 
 
+def refused_drafts(batch, vocab, away, seed, dtype=F32, temperature=1.0):
+    """Two rows a request whose draft is the token that the draft model favours most against the target, with a uniform number
+    next to 1: refused in every request."""
+    s = draft_inputs(batch, 2, vocab, dtype, seed=seed, away=away)
+    s["temperature"].fill_(temperature)
+    s["n_drafts"].fill_(1)
+    s["uniforms"].fill_(1 - 2.0 ** -24)
+    s["draft_logits"][:, 0] = s["logits"].view(batch, 2, -1)[:, 0, 0] + 1  # (of these it is likely enough)
+    s["tokens"][:, 1] = (s["draft_logits"].double() - s["logits"].view(batch, 2, -1)[:, 0].double()).argmax(-1)
+    return s
+
+
+@pytest.mark.parametrize("vocab", [40, 30011])
+def test_verify_drafts_signs_of_noise_behind_a_refusal(vocab):
+    """Where the draft's probability is the larger one a token's weight is 0, whatever its noise; -0 is 0."""
+    s = refused_drafts(5, vocab, 0.8, seed=41)
+    z = s["logits"].view(5, 2, -1)[:, 0]
+    p, q = (torch.softmax(x.double(), -1) for x in (z, s["draft_logits"]))
+    for b, bad in enumerate((-1.0, -0.0, float("nan"), -1e-30, 0.0)):
+        s["noise"][b, q[b] > p[b]] = bad
+    accept, lp = run_drafts(s)
+    check_drafts(s, accept, lp)
+    assert (accept[0] == 1).all() and (p > q).gather(1, accept[1].long()[:, None]).all()
+    at = torch.where(p > 1.5 * q, p, 0.0).argsort(-1, descending=True)[:, 3]  # some token with a weight
+    s["noise"].scatter_(1, at[:, None], -0.0)
+    accept, _ = run_drafts(s)
+    assert torch.equal(accept[1].long(), at)
+    s = dict(logits=z.contiguous(), tokens=i32([[0]] * 5), noise=s["noise"])
+    assert torch.equal(run_drafts(s)[0][1, :1].long(), at[:1])  # (behind a row without drafts too; other rows have zeros elsewhere)
+
+
 def test_verify_drafts_workspace_of_the_largest_call_fits_all():
     """One buffer of any contents for calls of all shapes, one after another."""
     from decode_megakernel_04_gb300 import verify_drafts_workspace
