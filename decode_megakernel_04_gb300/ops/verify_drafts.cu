@@ -271,6 +271,12 @@ __global__ void __launch_bounds__(kThreads, 6) draw_kernel(const __grid_constant
     const int out = ch.cut && !a.draft_logits ? a.tokens[static_cast<long long>(b) * rows + ch.row + 1] : -1;  // not drawn
     const bool minus = ch.cut && a.draft_logits && ch.draft_top > -INFINITY;
     const float by = 1.0f / ch.sum, draft_by = minus ? 1.0f / ch.draft_sum : 0.0f;
+    // A token's weight where a draft was refused, but for `out`; else its probability.
+    auto weight = [&](T z_in, T y_in, bool less) -> float {
+      // (rounded products, so that equal probabilities leave 0 and not what a fused difference would)
+      const float p = __fmul_rn(exp2_fast((logit(as_float(z_in)) - ch.top) * c), by);
+      return less ? fmaxf(p - __fmul_rn(exp2_fast((logit(as_float(y_in)) - ch.draft_top) * c), draft_by), 0.0f) : p;
+    };
     // The best of tokens from .. to - 1, for every thread. `cut`: of max(p - q, 0), or without `out`.
     auto best = [&](int from, int to, bool cut, float& score, int& at) {
       score = 0, at = -1;
@@ -291,11 +297,9 @@ __global__ void __launch_bounds__(kThreads, 6) draw_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int j = i + k * kThreads;
-          // (rounded products, so that equal probabilities leave 0 and not what a fused difference would)
-          float p = __fmul_rn(exp2_fast((logit(as_float(p_in[k])) - ch.top) * c), by);
-          if (less) p = fmaxf(p - __fmul_rn(exp2_fast((logit(as_float(q_in[k])) - ch.draft_top) * c), draft_by), 0.0f);
+          float p = weight(p_in[k], q_in[k], less);
           if (!kWhole && (j >= to || j == left_out)) p = 0.0f;
-          const float s = __fdividef(p, e[k] + 0.0f);  // (-0 + 0 is 0)
+          const float s = __fdividef(p, e[k] + 0.0f);  // (-0, as -log(1) is, counts as 0; past 2^126 the quotient is 0)
           if (s > score) score = s, at = j;
         }
       };
@@ -337,8 +341,14 @@ __global__ void __launch_bounds__(kThreads, 6) draw_kernel(const __grid_constant
         better(score, token, os, oa);
       }
     }
-    // max(p - q, 0) is 0 everywhere, as far as fp32 shows it: a draw from p (too seldom to share)
-    if (token < 0 && ch.cut) best(0, a.vocab, false, score, token);
+    // No token, as max(p - q, 0) is 0 everywhere, as far as fp32 shows it: a draw from p (too seldom to share). Not so where tokens
+    // with a weight have noise that does not draw them.
+    if (token < 0 && ch.cut) {
+      bool barred = false;
+      for (int j = tid; j < a.vocab; j += kThreads)
+        barred |= j != out && !(noise[j] >= 0.0f && noise[j] <= 0x1p126f) && weight(zr[j], minus ? yr[j] : zr[j], minus) > 0.0f;
+      if (!__syncthreads_or(barred)) best(0, a.vocab, false, score, token);
+    }
   }
   if (tid == 0) {
     a.accept_out[b] = ch.row + 1;

@@ -680,11 +680,12 @@ mk_status mk_rms_norm(const mk_rms_norm_args* args, int device, void* stream);
  * that is 0 everywhere) and w = p_a if a = n: for noise from the exponential distribution, a draw from w. T = 0 (or
  * below, or NaN): p_r and q_r are 1 at the first largest logit, so drafts are accepted while they are the greedy token.
  * accept_out is mk_verify_step's: accept_out[b] = a + 1 accepted rows, accept_out[batch + b] = the bonus token (-1 when every logit
- * of its row is -infinity), accept_out[2 * batch + b] = positions[b] + a + 1.
+ * of its row is -infinity, or no token with a weight has noise that draws it), accept_out[2 * batch + b] = positions[b] + a + 1.
  * logprobs[b][r] = log p_r of the token that follows row r: the drafts r < a, the bonus token at a (-infinity for token -1), 0
  * behind it.
- * Temperatures above 0 count as within 2^-100 .. 2^100. Logits that are NaN count as -infinity; where a row has some of +infinity, these share it. Noise below 0 or NaN: the token is
- * not drawn; 0 (or -0): it comes before all others that have a weight. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
+ * Temperatures above 0 count as within 2^-100 .. 2^100. Logits that are NaN count as -infinity; where a row has some of +infinity, these share it.
+ * Noise below 0, above 2^126 or NaN: the token is not drawn; 0 (or -0, or so near that the quotient passes fp32): it comes before
+ * all others that have a weight. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
  * as within 0 .. rows - 1 (MK_OP_BAD_LENGTH).
  * Weights, sums and log-probabilities are fp32: where uniforms * q and p, or the two largest quotients, are within 2^-17 of each other
  * (for probabilities of e^-x: x / 2^22 more), either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.

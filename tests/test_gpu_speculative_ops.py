@@ -432,6 +432,28 @@ def test_verify_drafts_signs_of_noise_behind_a_refusal(vocab):
     assert torch.equal(run_drafts(s)[0][1, :1].long(), at[:1])  # (behind a row without drafts too; other rows have zeros elsewhere)
 
 
+@pytest.mark.parametrize("vocab", [40, 30011])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_drafts_noise_that_draws_none_of_the_weights(vocab, draft):
+    """Behind a refusal some tokens have a weight, but no noise that draws: -1, not a token without a weight."""
+    s = refused_drafts(5, vocab, 0.8, seed=43)
+    z = s["logits"].view(5, 2, -1)[:, 0]
+    p, q = (torch.softmax(x.double(), -1) for x in (z, s["draft_logits"]))
+    if draft:
+        weight = p > q * (1 - 2.0 ** -15)  # (all that may have one in fp32)
+    else:  # (a draft that the target does not want: every other token has a weight)
+        s["draft_logits"] = None
+        weight = torch.ones_like(p, dtype=torch.bool).scatter_(1, s["tokens"][:, 1:].long(), False)
+        z.scatter_(1, s["tokens"][:, 1:].long(), -20.0)
+    for b, bad in enumerate((-1.0, float("inf"), float("nan"), 3e38)):
+        s["noise"][b, weight[b]] = bad
+    accept, lp = run_drafts(s)
+    assert accept[0].tolist() == [1] * 5 and accept[1, :4].tolist() == [-1] * 4 and accept[1, 4].item() >= 0
+    assert (lp[:4, 0] == -math.inf).all() and lp[4, 0].isfinite() and (lp[:, 1] == 0).all()
+    s["noise"][s["noise"] > 2.0 ** 126] = float("inf")  # (as they count)
+    check_drafts(s, accept, lp)
+
+
 def test_verify_drafts_workspace_of_the_largest_call_fits_all():
     """One buffer of any contents for calls of all shapes, one after another."""
     from decode_megakernel_04_gb300 import verify_drafts_workspace
