@@ -687,8 +687,10 @@ mk_status mk_rms_norm(const mk_rms_norm_args* args, int device, void* stream);
  * Noise below 0, above 2^126 or NaN: the token is not drawn; 0 (or -0, or so near that the quotient passes fp32): it comes before
  * all others that have a weight. A draft outside 0 .. vocab - 1 is refused (MK_OP_BAD_TOKEN); n_drafts counts
  * as within 0 .. rows - 1 (MK_OP_BAD_LENGTH).
- * Weights, sums and log-probabilities are fp32: where uniforms * q and p, or the two largest quotients, are within 2^-17 of each other
- * (for probabilities of e^-x: x / 2^22 more), either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.
+ * Weights, sums and log-probabilities are fp32: p and q are each off by at most 2^-16 of themselves (x / 2^22 more where they are e^-x,
+ * vocab / 2^37 more for vocabularies above 2^19), most by less than 2^-18, and a refused draft's w by what p and q are: little of
+ * w where the two differ, all of it where they agree to that. Where uniforms * q and p, or the two largest quotients, are nearer than that
+ * makes them, either may be taken. The result does not depend on timing. rows = 1 samples a token of each request.
  * `workspace`: mk_verify_drafts_workspace bytes of device scratch, 16-byte aligned, any contents; calls that may
  * overlap need one each. Two launches. */
 typedef struct mk_verify_drafts_args {

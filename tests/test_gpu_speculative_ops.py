@@ -454,6 +454,42 @@ def test_verify_drafts_noise_that_draws_none_of_the_weights(vocab, draft):
     check_drafts(s, accept, lp)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab, batch", [(4000, 1000), (151936, 20)])
+@pytest.mark.parametrize("away", [1e-1, 1e-2, 1e-3, 1e-5])
+def test_verify_drafts_refused_from_a_draft_model_near_the_target(away, vocab, batch, dtype):
+    """w = p - q is a difference of two fp32 numbers, so its error goes by p + q. A weight e^-x of the largest is off by 2^-22 x for
+    its exponent (the difference, the constant, its quotient and the product 2^-24 each), 2^-22 for exp2 and 2^-23 for two
+    products; the sum by that of its terms (the mean of their x is at most ln(vocab) < 12: 2^-18.4), 63 additions in a thread and
+    two roundings at each of 17 joins (97 x 2^-24 = 2^-17.4) and what the joins' factors are off by (17 x 2^-22 = 2^-17.9). In all less than
+    2^-16, and 2^-22 x. The token may be any whose quotient with that much more weight (and a quotient's 2^-22) is not under
+    the largest that is sure."""
+    s = draft_inputs(batch, 2, vocab, dtype, seed=vocab + batch, away=away)
+    t = s["temperature"] = 0.5 + torch.rand(batch, generator=gen(5), device=DEV)
+    s["n_drafts"].fill_(1)
+    s["uniforms"].fill_(1 - 2.0 ** -24)
+    z, y = s["logits"].view(batch, 2, -1)[:, 0].double(), s["draft_logits"].double()
+    x = (y - z).argmax(-1)
+    s["tokens"][:, 1] = x
+    accept, lp = run_drafts(s)
+    down = [(v.amax(-1, keepdim=True) - v) / t.double()[:, None] for v in (z, y)]
+    p, q = (torch.softmax(-v, -1) for v in down)
+    dp, dq = (w * (2.0 ** -16 + v * 2.0 ** -22) for w, v in zip((p, q), down))
+    of = lambda v, i: v.gather(1, i[:, None])[:, 0]  # noqa: E731
+    refused = accept[0] == 1
+    assert not (~refused & ((1 - 2.0 ** -24) * of(q - dq, x) >= of(p + dp, x))).any()
+    assert away < 1e-4 or refused.float().mean() > 0.9
+    sure = ((p - q - dp - dq) / s["noise"].double()).amax(-1)
+    token = accept[1].long()
+    assert (token[refused] >= 0).all() and (token < vocab).all()
+    token = token.clamp(min=0)
+    most = of(p - q + dp + dq, token) / of(s["noise"].double(), token)
+    assert (most >= sure * (1 - 2.0 ** -21))[refused].all()
+    assert (most > 0)[refused & (sure > 0)].all()
+    want = of(p, token).log()
+    assert ((lp[:, 0].double() - want).abs() <= 2.0 ** -16 + want.abs() * 2.0 ** -21)[refused].all()
+
+
 def test_verify_drafts_workspace_of_the_largest_call_fits_all():
     """One buffer of any contents for calls of all shapes, one after another."""
     from decode_megakernel_04_gb300 import verify_drafts_workspace
