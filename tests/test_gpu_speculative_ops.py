@@ -1058,6 +1058,44 @@ def test_verify_with_sampling():
     a.close(), b.close()
 
 
+@pytest.mark.parametrize("model", ["hybrid", "moe"])
+def test_verify_with_sampling_over_recurrent_states(model):
+    """Stacks whose layers carry a state from row to row: the rows that sampling refused are not in the state that the next block
+    begins with. Logits against the oracle, which takes the same blocks at the positions that the device decided."""
+    from decode_megakernel_04_gb300 import Megakernel
+    from gpu_harness import Report, compare_logits
+    from oracle import Oracle
+    from synthetic import make_tokens, make_weights
+    from test_gpu_steps import TOL, _hybrid, _moe
+    cfg = _hybrid() if model == "hybrid" else _moe()
+    dev = torch.device(DEV)
+    w = make_weights(cfg, seed=6, device=dev)
+    B, T, g, rep = 2, 19, gen(23), Report()
+    ctx = make_tokens(6, "ctx", (B, T), cfg.vocab, device=dev).contiguous()
+    m = Megakernel(cfg, w, max_batch=B, max_rows=4, max_ctx=64)
+    m.prefill(ctx)
+    orc = Oracle(cfg, w, B, 64)
+    orc.prefill(ctx.cpu().numpy())
+    token, pos = make_tokens(6, "first", (B, 1), cfg.vocab, device=dev), torch.full((B,), T, dtype=torch.int32, device=dev)
+    # drafts up to the first number of 1 are kept (any token has some probability), that one is refused
+    for turn, (R, keep) in enumerate(((4, (1, 3)), (4, (0, 2)), (3, (2, 0)), (1, (0, 0)), (2, (0, 1)))):
+        drafted = torch.randint(0, cfg.vocab, (B, R - 1), generator=g, device=DEV, dtype=torch.int32)
+        tokens = torch.cat([token.view(B, 1).to(torch.int32), drafted], 1).contiguous()
+        u = torch.ones(B, R - 1, device=DEV)
+        for b in range(B):
+            u[b, :keep[b]] = 0
+        logits, accept = torch.empty(B * R, cfg.vocab, device=DEV), i32([[0] * B] * 3)
+        s = dict(noise=torch.empty(B, cfg.vocab, device=DEV).exponential_(generator=g), uniforms=u, logprobs=torch.empty(B, R, device=DEV))
+        m.verify(tokens, pos, accept, logits, sampling=s)
+        assert m.status() == 0
+        ref = orc.step(tokens.cpu().numpy().astype(np.int64), pos.cpu().numpy().astype(np.int64))
+        compare_logits(logits.cpu().numpy().reshape(B, R, -1), ref, TOL, rep, f"block {turn}")
+        check_drafts(dict(s, logits=logits, tokens=tokens, positions=pos), accept, s["logprobs"])
+        assert accept[0].tolist() == [k + 1 for k in keep]
+        token, pos = accept[1].clone(), accept[2].clone()
+    m.close()
+
+
 def test_sampling_that_the_library_refuses_is_refused_before_the_step():
     from decode_megakernel_04_gb300 import MKError
     m, vocab = stepless()[0], 8
