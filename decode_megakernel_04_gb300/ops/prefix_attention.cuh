@@ -173,6 +173,9 @@ struct PrefixShape {
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
+// What scores are taken times. A score of -infinity stays one where the scale is 0; NaN stays NaN.
+__device__ inline float score_scale(float x) { return x < 1.17549435e-38f ? 1.17549435e-38f : x; }
+
 template <typename T>
 constexpr float kPrefixLift = std::is_same<T, __half>::value ? 14.0f : 0.0f;  // the base is this much under the maximum
 template <typename T>
@@ -762,8 +765,8 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
       const int st = warp >> 2, row = tid & 127;
       const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
       const uint32_t sums_at = tmem + lanes + 256 + static_cast<uint32_t>(st) * D;
-      float cs = fmaxf(p.scale_log2, 1.17549435e-38f);  // (a score of -infinity stays one where the scale is 0)
-      float next_cs = cs;                               // of the queries loaded last
+      float cs = score_scale(p.scale_log2);
+      float next_cs = cs;  // of the queries loaded last
       // Where this thread's row of an item's queries is, in elements; -1: the item has fewer rows.
       auto query_at = [&](const PrefixWalk& w) -> long long {
         const int head = w.kv_head();
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
               v[k] = pack2<__half>(f.x * down, f.y * down);
             }
             const float up = __shfl_sync(~0u, __uint_as_float((127 + e) << 23), (lane % kRows) * kLanes);
-            if (lane / kRows == i0 + i) next_cs = fmaxf(p.scale_log2 * fabsf(ks), 1.17549435e-38f) * up;
+            if (lane / kRows == i0 + i) next_cs = score_scale(p.scale_log2 * fabsf(ks)) * up;
             *reinterpret_cast<uint4*>(smem + (to - s0) + r * 128 + (((chunk ^ r) & 7) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
@@ -1008,7 +1011,9 @@ __global__ void __launch_bounds__(PrefixShape<D, E4M3>::kThreads, 1) prefix_kern
               asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + d + x), "f"(v[x]), "f"(v[x + 1]),
                            "f"(v[x + 2]), "f"(v[x + 3]), "f"(v[x + 4]), "f"(v[x + 5]), "f"(v[x + 6]), "f"(v[x + 7]) : "memory");
         }
-        if (write) *ml = make_float2(l == 0.0f ? -INFINITY : base, l);
+        // (a row that sees none of the item's keys has no part, whatever its scale)
+        const bool none = l == 0.0f || limit <= 0;
+        if (write) *ml = make_float2(none ? -INFINITY : base, none ? 0.0f : l);
         tc_before();
       }
     }

@@ -754,6 +754,34 @@ def test_prefix_scales_of_any_sign(dtype, cache, d, scale):
     check_prefix(s, *run_prefix(s, scale=scale), scale)
 
 
+@pytest.mark.parametrize("dtype, cache, d", [(BF16, BF16, 128), (F16, F16, 64), (BF16, BF16, 256), (BF16, E4M3, 128), (F16, E4M3, 64)])
+def test_prefix_scales_that_are_nan_reach_their_rows(dtype, cache, d):
+    """A scale of NaN gives NaN, as in mk_paged_attention; rows that see nothing are 0 all the same."""
+    from decode_megakernel_04_gb300 import paged_attention
+    for prefix in (200, 0):
+        s = prefix_inputs(prefix, [40, 1, 200], 3, 12, 2, d, 16, dtype, cache, seed=18)
+        nan = float("nan")
+        scale = d ** -0.5
+        if cache is E4M3:
+            s["ks"][1] = nan
+        else:
+            scale = nan
+        got, lse = run_prefix(s, scale=scale)
+        seen = torch.ones(3, 3, 12, dtype=torch.bool, device=DEV)
+        if prefix == 0:
+            seen[1, :2] = False  # (one position: the newest row's)
+        bad = seen.clone()
+        if cache is E4M3:
+            bad[..., :6] = False
+        assert got[bad].isnan().all() and lse[bad].isnan().all()
+        assert (got[~seen] == 0).all() and (lse[~seen] == -math.inf).all()
+        assert not got[~bad].isnan().any() and not lse[~bad].isnan().any()
+        if prefix == 0:  # the same call without the prefix
+            out, l2 = torch.empty_like(s["q"]), torch.empty_like(lse)
+            paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], out, scale=scale, lse=l2, k_scale=s["ks"], v_scale=s["vs"])
+            assert torch.equal(out.isnan(), got.isnan()) and torch.equal(l2.isnan(), lse.isnan())
+
+
 @pytest.mark.parametrize("cache", [BF16, E4M3])
 def test_prefix_hidden_values_do_not_leak(cache):
     """NaN and infinities behind the prefix's end in its last page, and in the places of later rows of a verify block."""
