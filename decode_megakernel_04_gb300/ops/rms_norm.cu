@@ -204,8 +204,10 @@ extern "C" mk_status mk_rms_norm(const mk_rms_norm_args* p, int device, void* st
   // One round is best where an SM has one row (1 x 5120 bf16: 6.8 us, 2 rounds 8.1, 4 rounds 8.9) and in fp32, where a round is 32
   // bytes already (4000 x 5120: 54.9 us, 56.0, 60.1); 16 bits are better with 4 (8191 x 6144 to e4m3: 84.6 us, 72.4, 66.2; 512 x 7168
   // 17.1, 15.0, 13.6): an SM has several rows, one's loads run beside another's sums and stores.
+  int sms = 0;
+  if (const cudaError_t e = sm_count(device, &sms)) return launched(me, e);
   int rounds = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 4;
-  if (a.rows > 152 && a.dtype != MK_F32 && vectors >= 64) rounds = vectors >= 128 ? 4 : 2;
+  if (a.rows > sms && a.dtype != MK_F32 && vectors >= 64) rounds = vectors >= 128 ? 4 : 2;
   const int threads = (vectors + rounds * 32 - 1) / (rounds * 32) * 32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = a.dtype == MK_BF16  ? e4m3 ? launch<__nv_bfloat16, true>(a, rounds, threads, s) : launch<__nv_bfloat16, false>(a, rounds, threads, s)

@@ -372,26 +372,27 @@ mk_status check_shape(const mk_verify_drafts_args& a, int device) {
   return check_device(kMe, device);
 }
 
-// CTAs that the GPU holds at once: of the statistics 8 an SM, of the race 6
-constexpr int64_t kStatsCtas = 152 * 8, kRaceCtas = 152 * 6;
+// CTAs that an SM holds at once, and SMs that workspaces are made for: their sizes and the checks of arguments need no device. More SMs
+// are not made use of by few rows.
+constexpr int64_t kStatsCtas = 8, kRaceCtas = 6, kMostSms = 152;
 
 int64_t all_rows(const mk_verify_drafts_args& a) { return static_cast<int64_t>(a.batch) * (2 * a.rows - 1); }
 int whole_parts(const mk_verify_drafts_args& a) { return std::min(kMaxParts, (a.vocab + 16383) / 16384); }
 // parts of 16384 elements; where that leaves SMs with less than they hold, more and smaller ones (one request of 15 rows: 480 parts
 // instead of 150, statistics 12 -> 7 us)
-int parts_of(const mk_verify_drafts_args& a) {
-  const int64_t more = std::min<int64_t>({kMaxParts, kStatsCtas / std::max<int64_t>(1, all_rows(a)), (a.vocab + 1023) / 1024});
+int parts_of(const mk_verify_drafts_args& a, int64_t sms) {
+  const int64_t more = std::min<int64_t>({kMaxParts, kStatsCtas * sms / std::max<int64_t>(1, all_rows(a)), (a.vocab + 1023) / 1024});
   return std::max<int64_t>(whole_parts(a), more);
 }
 // So many shares that the GPU holds all requests' at once (6 CTAs an SM; 4 of them with 8 elements in flight leave more SMs with one
 // less than others: 128 rows 58.0 -> 55.6 us), of 1024 tokens at least
-int shares_of(const mk_verify_drafts_args& a) {
-  return std::max<int64_t>(1, std::min<int64_t>({kMaxShares, kRaceCtas / std::max(1, a.batch), (a.vocab + 1023) / 1024}));
+int shares_of(const mk_verify_drafts_args& a, int64_t sms) {
+  return std::max<int64_t>(1, std::min<int64_t>({kMaxShares, kRaceCtas * sms / std::max(1, a.batch), (a.vocab + 1023) / 1024}));
 }
 // What any such parts and shares take: never less for more requests, rows or tokens.
 uint64_t workspace_of(const mk_verify_drafts_args& a) {
-  const int64_t parts = std::max(all_rows(a) * whole_parts(a), std::min(all_rows(a) * kMaxParts, kStatsCtas));
-  const int64_t shares = std::max<int64_t>(a.batch, std::min<int64_t>(static_cast<int64_t>(a.batch) * kMaxShares, kRaceCtas));
+  const int64_t parts = std::max(all_rows(a) * whole_parts(a), std::min(all_rows(a) * kMaxParts, kStatsCtas * kMostSms));
+  const int64_t shares = std::max<int64_t>(a.batch, std::min<int64_t>(static_cast<int64_t>(a.batch) * kMaxShares, kRaceCtas * kMostSms));
   return parts * sizeof(Part) + shares * (sizeof(float) + sizeof(int)) + a.batch * sizeof(int);
 }
 
@@ -461,8 +462,10 @@ extern "C" mk_status mk_verify_drafts(const mk_verify_drafts_args* p, int device
   Work w;
   w.a = *p;
   if (w.a.rows == 1) w.a.draft_logits = nullptr;
-  w.parts = parts_of(w.a);
-  w.shares = shares_of(w.a);
+  int sms = 0;
+  if (const cudaError_t e = sm_count(device, &sms)) return launched(kMe, e);
+  w.parts = parts_of(w.a, std::min<int64_t>(sms, kMostSms));
+  w.shares = shares_of(w.a, std::min<int64_t>(sms, kMostSms));
   w.part = static_cast<Part*>(w.a.workspace);
   w.score = reinterpret_cast<float*>(w.part + static_cast<int64_t>(p->batch) * (2 * p->rows - 1) * w.parts);
   w.score_at = reinterpret_cast<int*>(w.score + static_cast<int64_t>(p->batch) * w.shares);
