@@ -48,10 +48,17 @@ struct Eight<float> {
   }
 };
 
+// The larger of two; NaN if one is.
+__device__ inline float max_nan(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
 // The sum or the largest of a block's values, for every thread; `red` holds a value for each warp.
 template <bool SUM>
 __device__ inline float of_block(float x, float* red) {
-  auto both = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+  auto both = [](float a, float b) { return SUM ? a + b : max_nan(a, b); };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int d = 16; d; d >>= 1) x = both(x, __shfl_xor_sync(~0u, x, d));
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const __grid_constant
       if (i < a.width) Eight<T>::store(static_cast<T*>(a.out) + row * a.out_stride, i, h[r]);
     } else if (a.group == a.width) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(h[r][k]));
+      for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(h[r][k]));
     }
   }
   if (!E4M3) return;
@@ -135,8 +142,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const __grid_constant
     if (a.group != a.width) {
       top = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(h[r][k]));
-      for (int d = 1; d < a.group / 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(h[r][k]));
+      for (int d = 1; d < a.group / 8; d <<= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, d));
     }
     float s = top / 448.0f;
     const bool code = fine && s < INFINITY;

@@ -648,7 +648,8 @@ mk_status mk_logit_controls_check(const mk_logit_controls_args* args, int device
  *   out = the code of y / s (nearest even, saturating; s = 0: code 0)
  * h, the mean square and y are fp32 (y is made of the unrounded h); each result is rounded once. Sums whose squares pass fp32
  * (rows with elements of 2^60 and more, infinities or NaN): 16- and 32-bit results follow the formula with a mean of infinity or
- * NaN, scales and codes of such a row are NaN.
+ * NaN, scales and codes of such a row are NaN. A y that is infinite or NaN (of such a gain, or 0 / 0 with eps = 0)
+ * makes its group's scale and codes NaN.
  * residual_out may be x or residual, and a 16- or 32-bit out may be x or residual (not both the same buffer), where the strides
  * are the same; other overlaps are not allowed. One launch.
  * Errors: width not a multiple of 8 in 8..32768; group not width or 8, 16, 32, 64, 128 or 256 dividing it; pointers not 16-byte

@@ -124,6 +124,38 @@ def test_rms_norm_special_rows():
             check_norm(x[[0, 4, 5]], None, None, 1e-6, codes[[0, 4, 5]], None, scales[[0, 4, 5]])
 
 
+def test_rms_norm_gains_that_are_not_finite():
+    """They are their column's alone; among codes they make their group's codes and scale NaN, also where the rest of it is 0."""
+    from decode_megakernel_04_gb300 import rms_norm
+    for dtype in (BF16, F16, F32):
+        x = 1 + torch.rand(3, 512, generator=gen(2), device=DEV).to(dtype)
+        gain = torch.ones(512, dtype=dtype, device=DEV)
+        gain[5], gain[200] = float("nan"), float("inf")
+        out = torch.empty_like(x)
+        rms_norm(x, out, gain=gain)
+        at = torch.ones(512, dtype=torch.bool, device=DEV)
+        at[[5, 200]] = False
+        assert out[:, 5].isnan().all() and (out[:, 200] == math.inf).all()
+        check_norm(x, None, None, 1e-6, torch.where(at, out, (x.double() / (x.double() ** 2).mean(-1, keepdim=True).add(1e-6).sqrt()).to(dtype)), None, None)
+        plain, ps = torch.empty(3, 512, device=DEV).to(E4M3), torch.empty(3, 8, device=DEV)
+        rms_norm(x, plain, gain=gain.nan_to_num(nan=0.0, posinf=1.0), scales=ps)
+        codes, scales = torch.empty_like(plain), torch.empty_like(ps)
+        rms_norm(x, codes, gain=gain, scales=scales)
+        f = codes.float()
+        at[:64] = at[192:256] = False
+        assert f[:, ~at].isnan().all() and scales[:, [0, 3]].isnan().all()
+        assert torch.equal(f[:, at], plain.float()[:, at]) and torch.equal(scales[:, [1, 2, 4, 5, 6, 7]], ps[:, [1, 2, 4, 5, 6, 7]])
+        one = torch.empty(3, 1, device=DEV)
+        gain[:] = 0
+        gain[5] = float("nan")
+        for sc in (one, scales):
+            rms_norm(x, codes, gain=gain, scales=sc)
+            assert codes.float()[:, :64].isnan().all() and sc[:, 0].isnan().all()
+            assert codes.float()[:, 64:].isnan().all() if sc is one else (codes.float()[:, 64:] == 0).all() and (sc[:, 1:] == 0).all()
+            rms_norm(torch.zeros_like(x), codes, eps=0.0, scales=sc)  # 0 / 0, as with 16-bit results
+            assert codes.float().isnan().all() and sc.isnan().all()
+
+
 def test_rms_norm_groups_of_zeros_and_of_the_smallest_values():
     """A group without a value gets scale 0 and codes 0; one whose scale is subnormal keeps its codes."""
     from decode_megakernel_04_gb300 import rms_norm
