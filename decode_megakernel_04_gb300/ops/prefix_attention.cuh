@@ -19,7 +19,10 @@
 //   Probabilities go back to tensor memory over the first half of the scores' columns as the product's operand (16 bits).
 //   They are taken against a base that moves only when a score passes it by kPrefixGrow: else sums stay as they are.
 // - Loads: warps for keys and for values copy boxes of a page's rows (TMA, through the page table) into a ring of slots
-//   each; a copy takes its warp 140 cycles, so the two 64-column pieces of a tile have a warp each. Over own keys few query rows
+//   each; a copy takes its warp 140 cycles, so the two 64-column pieces of a tile have a warp each. A box has as many rows as the largest
+//   power of two that divides the page size: 8 and more copy a tile of 16 or fewer boxes while another is worked on, but
+//   pages of one position (or of an odd number) take 128 boxes a tile, 18 thousand cycles (32 x 8 rows behind 8191 in pages of 8 and more 87
+//   to 89 us, 4: 97, 2: 136, 1: 220, 25: 209). Over own keys few query rows
 //   leave room for a third tile, which memory's latency under load asks for. (Prefetches into L2 by warps of their own
 //   made it slower, 169 us against 127 for the 64 requests below.) Codes of e4m3 caches land in the half of their slot where two
 //   warps each make fp16 of them in place (through stages of 64 rows of their own, half as many bytes were on their way: 65536
@@ -29,10 +32,12 @@
 // Probabilities are one 16-bit number (a pair hi + lo would be half as much work again for the tensor cores). bf16: 2^-8 of each
 // at most; fp16: 2^-11, against a base 14 under the maximum, so that what falls under its range is 2^-39 of the largest. Sums of
 // probabilities are those of the unrounded ones.
-// Measured: 64 requests behind 32768 positions with own ones of up to 2000 (48/8 heads of 128, bf16) 114 us, 32 x 8 rows behind
-// 8191 92 us (600 TFLOP/s), 64 requests behind 65536 in e4m3 155 us (670 TFLOP/s), 4 samples of 4096 positions 256 wide 25 us. What bounds
-// it is the chain of products, scores out of tensor memory, softmax and probabilities back: a pair's tile takes about 3500 cycles,
-// 400 less with almost all products left out and 200 less without exponentials, and two streams are all that tensor memory holds.
+// Measured: 64 requests behind 32768 positions with own ones of up to 2000 (48/8 heads of 128, bf16) 112 us, 32 x 8 rows behind
+// 8191 90 us (610 TFLOP/s), 64 requests behind 65536 in e4m3 155 us (670 TFLOP/s), 4 samples of 4096 positions 256 wide 25 us. A pair's
+// tile takes about 3500 cycles, 2048 of them the tensor cores' (75 % of the rate measured for large products); its chain of products, scores out
+// of tensor memory, softmax and probabilities back takes 400 less with almost all products left out and 200 less without exponentials.
+// Further from their bounds are single row tiles (71 to 75 % of a pair's time for half of its work), the steps between own items, and what is
+// outside of the tiles: 32 x 8 rows are 51 us of tiles and items, 21 of starting, ending and uneven pieces, 15 of the join.
 // Every wait has a limit (2 s), after which the CTA gives up, drains and frees what it holds and MK_OP_TIMEOUT is set.
 #pragma once
 #include <cuda.h>
@@ -55,7 +60,8 @@ constexpr int kTileRows = 128;        // query rows of a row tile
 constexpr int kGroupRows = 8;         // new rows of a request that share an item over its own keys
 constexpr int kItemTiles = 4;         // what an item over own keys takes besides its tiles, in tiles
 enum { kPairs, kSingles, kOwn };      // the lines
-// What a tile of a line takes of a CTA, in parts of 24 of a pair's: as measured 128 wide, where a pair's tile takes 1.8 to 2.1 us, a single
+// What a tile of a line takes of a CTA, in parts of 24 of a pair's (64 and 256 wide are dealt by the same numbers, without measurements of their
+// own): as measured 128 wide, where a pair's tile takes 1.8 to 2.1 us, a single
 // one 1.3 to 1.4, one of an item (with its share of the four for the item) 1.0 to 1.2. 64 requests behind 32768 positions and 32 x 8 rows
 // behind 8191 take 113 and 91 us; with 24 / 18 / 18 122 and 90, with two tiles an item and 24 / 18 / 18 116 and 95, with 24 / 24 / 24 136
 // and 95; e4m3 behind 65536 155, with 24 / 16 / 20 161.
@@ -165,7 +171,8 @@ struct PrefixShape {
   static constexpr bool kInPlace = E4M3 && kWide == 128;
   static constexpr int kCodes = kPrefixTile * 128;          // rows of 128 bytes (zeros behind a head's columns)
   static constexpr int kQ = kTileRows * D * 2;              // a stream's queries
-  // Queries, keys' slots, values' slots. 128 wide, 16 bits, items of up to 64 or 32 rows: 5 or 6 slots and queries twice.
+  // Queries, keys' slots, values' slots. 128 wide, 16 bits, items of up to 64 or 32 rows: 5 or 6 slots and queries twice. (Lines over the
+  // prefix leave the seventh 32 KB empty.)
   static constexpr bool kFewRows = D == 128 && !E4M3;
   static constexpr int kOffCodes = kFewRows ? 7 * kSlot : (kKeySlots + kValueSlots) * kSlot + kStreams * kQ;  // [keys, values][slots]
   static constexpr int kOffBar = kOffCodes + (E4M3 && !kInPlace ? (kKeySlots + kValueSlots) * kCodes : 0);

@@ -208,9 +208,10 @@ extern "C" mk_status mk_rms_norm(const mk_rms_norm_args* p, int device, void* st
   DeviceGuard guard(device);
   if (guard.err != cudaSuccess) return launched(me, guard.err);
   const int vectors = a.width / 8;
-  // One round is best where an SM has one row (1 x 5120 bf16: 6.8 us, 2 rounds 8.1, 4 rounds 8.9) and in fp32, where a round is 32
-  // bytes already (4000 x 5120: 54.9 us, 56.0, 60.1); 16 bits are better with 4 (8191 x 6144 to e4m3: 84.6 us, 72.4, 66.2; 512 x 7168
-  // 17.1, 15.0, 13.6): an SM has several rows, one's loads run beside another's sums and stores.
+  // One round is best where an SM has one row (1 x 5120 bf16: 2.0 us in a graph, 2 rounds 2.4, 4 rounds 2.8) and in fp32, where a round
+  // is 32 bytes already (4000 x 5120: 50.2 us, 50.9, 56.2; 4 rounds, for rows above 16384, spill 64 to 92 bytes a thread); 16 bits are better with 4
+  // (8191 x 6144 to e4m3: 80.6 us, 67.4, 61.1; 512 x 7168 7.5, 7.7, 7.2): an SM has several rows, one's loads run beside another's
+  // sums and stores.
   int sms = 0;
   if (const cudaError_t e = sm_count(device, &sms)) return launched(me, e);
   int rounds = vectors <= 1024 ? 1 : vectors <= 2048 ? 2 : 4;

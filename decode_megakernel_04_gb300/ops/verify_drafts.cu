@@ -7,9 +7,9 @@
 // With given exponential noise the race is a draw from the weights, and unlike an inverse distribution function it is no sum
 // over the vocabulary: a token's quotient depends on that token alone, in fp32, whatever the order of the work.
 // Bound by memory: every logit once, and the drawn row, its draft row and the noise. 64 requests of 4 rows of 202048 fp32 logits
-// and 3 of the drafts: 92 us, 60 of them for the statistics (6.0 TB/s); one request of 8 x 151936: 18 us, all latencies (the
-// statistics 7, the draw 11: a row's parts, the drafts' probabilities, the race and its join wait for each other); 128 rows of
-// 163841 bf16: 49. (Figures of single steps below are with cold caches.)
+// and 3 of the drafts: 92 us, 60 of them for the statistics (6.0 TB/s; rows that n_drafts leaves out are read too); one request of 8 x
+// 151936: 18 us, all latencies (the statistics 7, the draw 11: a row's parts, the drafts' probabilities, the race and its join wait for each
+// other); 128 rows of 163841 bf16: 48. (Figures of single steps below are with cold caches.)
 #include <algorithm>
 #include <type_traits>
 
